@@ -70,14 +70,15 @@ extern "C" {
 typedef enum {
   RA_OK = 0,
   RA_ERR_NULL = 1,     /* a required pointer is NULL                              */
-  RA_ERR_SHAPE = 2,    /* a size <= 0, H_q % H_kv != 0, merge n out of range       */
+  RA_ERR_SHAPE = 2,    /* a size <= 0, H_q % H_kv != 0, merge n out of range,
+                          a cache capacity that is not a multiple of 16          */
   RA_ERR_HEADDIM = 3,  /* D is not 64 or 128 (attention), not 32-256 (merge)     */
   RA_ERR_ALIGN = 4,    /* a data pointer is not 16-byte aligned                    */
   RA_ERR_DTYPE = 5,    /* unknown dtype or order value                             */
   RA_ERR_DEVICE = 6,   /* current device is not compute capability 10.3            */
   RA_ERR_LAUNCH = 7,   /* CUDA runtime error while preparing or launching          */
   RA_ERR_TIMEOUT = 8,  /* a device-side bounded wait expired (dev_status only)     */
-  RA_ERR_BUFFER = 9,   /* a caller buffer is too small                             */
+  RA_ERR_BUFFER = 9,   /* a caller buffer is too small or overlaps an input        */
   RA_ERR_RANGE = 10,   /* a size overflows 32-bit indexing, or step out of range;
                           in dev_status (checked build only): a device index out
                           of its tensor's range                                   */
@@ -421,11 +422,110 @@ ra_status ring_attn_expiry_test(const void* q, const void* k, const void* v,
                                 void* out, float* lse, int S, int* dev_status,
                                 void* stream);
 
+/*
+ * The 4-bit key/value cache: what a served sequence has attended to so far,
+ * kept at 4.5 bits a value for the decoding steps that follow a prompt. The
+ * pages have no counterpart; it continues the forward above (the same
+ * definition of attention, the same lse, so that its partial results merge
+ * with attn_lse_merge).
+ *
+ * A cache of capacity C holds, for each sequence b and key/value head, C
+ * slots; a slot is one token's key row and value row of D values, in groups
+ * of 64 along D:
+ *     k_codes, v_codes   [B, H_kv, C, D / 2]      bytes: dimension 2i in the
+ *                        low, 2i + 1 in the high half of byte i of a row
+ *     k_meta, v_meta     [B, H_kv, C, D / 64, 2]  bfloat16: scale, zero point
+ * A code c stands for scale * (c - 8) + zero. C is a multiple of 16, D 64 or
+ * 128; the four tensors are 16-byte aligned. How many slots a sequence uses
+ * is the caller's `lens` (device int32 [B]); slots past it may hold anything,
+ * including NaN. Nothing here reads lens on the host, so a step can be
+ * captured into a graph and replayed while lens grows.
+ *
+ * kv4_append - quantises T tokens a sequence, k and v [B, T, H_kv, D] of
+ * `dtype` (RA_BF16 or RA_F32), into slots start[b], start[b] + 1, ...
+ * (start: device int32 [B]). n_new: NULL, or device int32 [B]: only the first
+ * n_new[b] tokens of sequence b count, the rest of a padded batch is not
+ * written. Per group, in float32: scale = bf16(max / 15 - min / 15), zero =
+ * bf16(min + 8 scale), code = clamp(rint((x - zero) / scale) + 8, 0, 15), or
+ * 8 where scale is 0. A group that holds an infinity or a NaN reads back as
+ * NaN. A slot outside [0, C) is not written and sets RA_ERR_RANGE in
+ * `dev_status` (device int, may be NULL).
+ */
+ra_status kv4_append(const void* k, const void* v, void* k_codes, void* k_meta,
+                     void* v_codes, void* v_meta, const int* start,
+                     const int* n_new, int B, int T, int H_kv, int D, int C,
+                     int dtype, int* dev_status, void* stream);
+
+/*
+ * kv4_read - the values of slots start[b] ... start[b] + T - 1 (start NULL:
+ * from slot 0), as k and v [B, T, H_kv, D] of `dtype` (either may be NULL).
+ * A slot outside [0, C) gives zeros and sets RA_ERR_RANGE in `dev_status`.
+ */
+ra_status kv4_read(const void* k_codes, const void* k_meta, const void* v_codes,
+                   const void* v_meta, const int* start, void* k, void* v,
+                   int B, int T, int H_kv, int D, int C, int dtype,
+                   int* dev_status, void* stream);
+
+/* Bytes of workspace kv4_attn needs for these sizes (host only; 0 for short
+ * axes without scores). Errors as kv4_attn's sizes. */
+ra_status kv4_attn_workspace(int B, int S_q, int H_q, int H_kv, int D, int C,
+                             int max_len, int window, int n_sink,
+                             int with_score, size_t* bytes);
+
+/*
+ * kv4_attn - attention of S_q new tokens a sequence (one in plain decoding)
+ * over its cache, which already holds them (append first).
+ * lens: device int32 [B], slots in use, the S_q new ones included (clamped to
+ * [0, max_len]); max_len in [1, C] bounds them and sizes the launch. Query t
+ * of sequence b is at slot p = lens[b] - S_q + t and sees the slots j <= p;
+ * with window > 0 only those with j > p - window or j < n_sink (window 0: no
+ * window, n_sink is ignored). Slots are counted as they lie, so after an
+ * eviction a window counts kept slots. Head h reads key/value head
+ * h / (H_q / H_kv). A row that sees no slot gets out = 0, lse = -inf.
+ *     q, out  [B, S_q, H_q, D] bfloat16    lse  [B, H_q, S_q] float32 or NULL
+ * score: NULL, or float32 [B, H_kv, C]: every slot's attention weight, summed
+ * over the queries and the heads of its group, is ADDED to it.
+ * dtype RA_BF16. scale <= 0 means 1 / sqrt(D). The workspace is the caller's,
+ * 16-byte aligned; its contents do not matter. Calls that may overlap on the
+ * GPU need workspaces of their own. Results repeat bit for bit.
+ * Errors: RA_ERR_NULL, RA_ERR_SHAPE, RA_ERR_HEADDIM, RA_ERR_ALIGN,
+ * RA_ERR_DTYPE, RA_ERR_RANGE (max_len, window, n_sink, sizes), RA_ERR_BUFFER,
+ * RA_ERR_DEVICE, RA_ERR_LAUNCH.
+ */
+ra_status kv4_attn(const void* q, const void* k_codes, const void* k_meta,
+                   const void* v_codes, const void* v_meta, const int* lens,
+                   void* out, float* lse, float* score, int B, int S_q, int H_q,
+                   int H_kv, int D, int C, int max_len, int window, int n_sink,
+                   float scale, int dtype, void* workspace,
+                   size_t workspace_bytes, int* dev_status, void* stream);
+
+/*
+ * kv4_evict - cuts every sequence down to `budget` slots a head by its
+ * accumulated weights, into another cache of capacity C_dst >= budget.
+ * Of n = lens[b] > budget slots a head keeps the first n_sink, the last
+ * n_recent and, of those between, the budget - n_sink - n_recent with the
+ * largest score (score float32 [B, H_kv, C]; among equal scores the lowest
+ * slot, NaN below every number). n <= budget keeps all. Kept slots keep their
+ * order. Outputs: the four dst tensors' first min(n, budget) slots, dst_score
+ * [B, H_kv, C_dst] likewise (may be NULL), dst_lens [B] = min(n, budget), and
+ * kept int32 [B, H_kv, budget], each kept slot's place in the source, -1 past
+ * the last. Slots past the last stay as they were. n_sink + n_recent <=
+ * budget (else RA_ERR_RANGE). Nothing written may overlap anything read
+ * (RA_ERR_BUFFER): evict into a spare cache and swap the two.
+ */
+ra_status kv4_evict(const void* k_codes, const void* k_meta, const void* v_codes,
+                    const void* v_meta, const float* score, const int* lens,
+                    void* dst_k_codes, void* dst_k_meta, void* dst_v_codes,
+                    void* dst_v_meta, float* dst_score, int* dst_lens, int* kept,
+                    int B, int H_kv, int D, int C, int C_dst, int budget,
+                    int n_sink, int n_recent, int* dev_status, void* stream);
+
 /* Human-readable text of a status; never NULL. */
 const char* ring_attn_strerror(int status);
 
 /* Library ABI version (major * 100 + minor); 103 adds the backward, the
- * packed variable-length and the Ulysses-layout entry points. */
+ * packed variable-length and the Ulysses-layout entry points, 104 the 4-bit
+ * key/value cache. */
 int ring_attn_version(void);
 
 #ifdef __cplusplus

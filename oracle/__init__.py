@@ -26,11 +26,13 @@ Everything here is float64 NumPy, written to be read against the pages:
   sequences of different lengths, each its own problem.
 * ``ulysses_attention`` - the Ulysses steps (all-to-all to heads, full
   attention per head group, all-to-all back) on sequence-sharded tensors.
+* ``kv4``               - the 4-bit key/value cache: quantising, what codes
+  stand for, attention of a few tokens over a cache, eviction.
 * ``tile_visits``       - expands the chunk-level schedule into the sequence of
   fixed-size key tiles a tiled kernel must visit, classifying every tile by
   brute force over its (query, key) pairs.
 
-Pins: every function above is checked in ``tests/test_oracle.py`` against
+Pins: every function above is checked in ``tests/test_oracle*.py`` against
 brute force, closed forms, invariants and hand-derived fixtures under
 ``tests/golden/``; none is "parity unpinned".
 """
@@ -45,6 +47,7 @@ from .schedule import (
 from .ring import ring_attention
 from .backward import attention_backward, ring_attention_backward, backward_rows
 from .varlen import attention_varlen, attention_backward_varlen
+from . import kv4
 from .ulysses import (ulysses_attention, to_sequence_shards, from_sequence_shards,
                       all_to_all_seq_to_head, all_to_all_head_to_seq)
 
@@ -53,7 +56,7 @@ __all__ = [
     "lse_merge", "lse_merge_n",
     "SKIP", "FULL", "PARTIAL", "ORDER_CONTIGUOUS", "ORDER_ZIGZAG",
     "rank_segments", "ring_schedule", "schedule_table", "tile_visits",
-    "ring_attention",
+    "ring_attention", "kv4",
     "attention_backward", "ring_attention_backward", "backward_rows",
     "attention_varlen", "attention_backward_varlen",
     "ulysses_attention", "to_sequence_shards", "from_sequence_shards",

@@ -10,9 +10,11 @@ kernels of ``_lib/libringattn.so``; there is no fallback of any kind, and a
 missing library raises at the first call.
 """
 
+import contextlib
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -32,7 +34,9 @@ EXPORTS = ("ring_attn_fwd", "ring_attn_fwd_ex", "ring_attn_visit_log_len",
            "ring_attn_bwd_ulysses",
            "ring_attn_bwd_workspace", "ring_attn_bwd", "ring_attn_bwd_ex",
            "ring_attn_bwd_noalloc",
-           "attn_lse_merge", "attn_lse_merge_n", "ring_attn_plan",
+           "attn_lse_merge", "attn_lse_merge_n",
+           "kv4_append", "kv4_read", "kv4_attn_workspace", "kv4_attn", "kv4_evict",
+           "ring_attn_plan",
            "ring_attn_expiry_test", "ring_attn_strerror", "ring_attn_version")
 
 _lib = None
@@ -102,6 +106,16 @@ def load():
     lib.attn_lse_merge.argtypes = [vp] * 6 + [c_int] * 5 + [vp]
     lib.attn_lse_merge_n.restype = c_int
     lib.attn_lse_merge_n.argtypes = [vp, vp, c_int, vp, vp] + [c_int] * 5 + [vp]
+    lib.kv4_append.restype = c_int
+    lib.kv4_append.argtypes = [vp] * 8 + [c_int] * 6 + [vp, vp]
+    lib.kv4_read.restype = c_int
+    lib.kv4_read.argtypes = [vp] * 7 + [c_int] * 6 + [vp, vp]
+    lib.kv4_attn_workspace.restype = c_int
+    lib.kv4_attn_workspace.argtypes = [c_int] * 10 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.kv4_attn.restype = c_int
+    lib.kv4_attn.argtypes = [vp] * 9 + [c_int] * 9 + [c_float, c_int, vp, ctypes.c_size_t, vp, vp]
+    lib.kv4_evict.restype = c_int
+    lib.kv4_evict.argtypes = [vp] * 13 + [c_int] * 8 + [vp, vp]
     lib.ring_attn_plan.restype = c_int
     lib.ring_attn_plan.argtypes = [c_int, c_int, c_int, c_int, ip, ctypes.c_size_t]
     lib.ring_attn_expiry_test.restype = c_int
@@ -556,6 +570,220 @@ def attn_lse_merge_n(os_, lses, out=None, lse=None, stream=None):
                               _dtype_code(os_[0].dtype), _stream(stream))
     _check(st, "attn_lse_merge_n")
     return out, lse
+
+
+# ------------------------------------------------------------------ 4-bit key/value cache
+
+class KV4Cache(NamedTuple):
+    """A key/value cache held in 4 bits (format: ``include/ring_attn.h``):
+    codes uint8 [B, H_kv, C, D/2], meta bfloat16 [B, H_kv, C, D/64, 2]."""
+    k_codes: "torch.Tensor"   # noqa: F821
+    k_meta: "torch.Tensor"    # noqa: F821
+    v_codes: "torch.Tensor"   # noqa: F821
+    v_meta: "torch.Tensor"    # noqa: F821
+
+
+def kv4_cache(B, H_kv, C, D, device="cuda"):
+    """A zeroed cache of capacity C (a multiple of 16) slots a sequence."""
+    import torch
+    if D not in (64, 128) or C <= 0 or C % 16:
+        raise ValueError("D must be 64 or 128 and C a positive multiple of 16")
+    parts = []
+    for _ in range(2):
+        parts.append(torch.zeros(B, H_kv, C, D // 2, dtype=torch.uint8, device=device))
+        parts.append(torch.zeros(B, H_kv, C, D // 64, 2, dtype=torch.bfloat16, device=device))
+    return KV4Cache(*parts)
+
+
+def _kv4_dims(cache):
+    """(B, H_kv, C, D) of a cache whose tensors agree."""
+    import torch
+    codes = cache.k_codes
+    if codes.dim() != 4:
+        raise ValueError("k_codes must be [B, H_kv, C, D/2]")
+    B, H_kv, C, half = codes.shape
+    _like(cache.k_codes, "k_codes", codes.shape, torch.uint8)
+    _like(cache.v_codes, "v_codes", codes.shape, torch.uint8)
+    meta = (B, H_kv, C, half // 32, 2)
+    _like(cache.k_meta, "k_meta", meta, torch.bfloat16)
+    _like(cache.v_meta, "v_meta", meta, torch.bfloat16)
+    return B, H_kv, C, 2 * half
+
+
+def _kv4_named(cache, what=""):
+    return tuple((t, what + n) for t, n in zip(cache, KV4Cache._fields))
+
+
+def _ints(t, name, n):
+    """A contiguous int32 [n] tensor (None: not given)."""
+    import torch
+    _like(t, name, (n,), torch.int32)
+
+
+def _on_stream(stream):
+    """Memory handed out inside belongs to the stream the call runs on."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def kv4_append(cache, k, v, start, n_new=None, dev_status=None, stream=None):
+    """Quantises k, v [B, T, H_kv, D] (bf16 or float32) into slots start[b],
+    start[b] + 1, ... of ``cache``; with ``n_new`` int32 [B] only the first
+    n_new[b] tokens of a padded batch. start: int32 [B] (CUDA)."""
+    lib = load()
+    B, H_kv, C, D = _kv4_dims(cache)
+    if k.dim() != 4:
+        raise ValueError("k must be [B, T, H_kv, D]")
+    T = k.shape[1]
+    _like(k, "k", (B, T, H_kv, D), k.dtype)
+    _like(v, "v", k.shape, k.dtype)
+    _ints(start, "start", B)
+    _ints(n_new, "n_new", B)
+    _int_buffer(dev_status, "dev_status", 1)
+    code = _dtype_code(k.dtype)
+    _on_device(_kv4_named(cache) + ((k, "k"), (v, "v"), (start, "start"), (n_new, "n_new"),
+                                    (dev_status, "dev_status")))
+    st = lib.kv4_append(_ptr(k), _ptr(v), *map(_ptr, cache), _ptr(start), _ptr(n_new), B, T, H_kv,
+                        D, C, code, _ptr(dev_status), _stream(stream))
+    _check(st, "kv4_append")
+
+
+def kv4_read(cache, start, T, dtype=None, k=None, v=None, dev_status=None, stream=None):
+    """The values (k, v) [B, T, H_kv, D] of slots start[b] ... start[b] + T - 1
+    (start None: from slot 0), bf16 unless ``dtype`` or given tensors say
+    float32."""
+    import torch
+    lib = load()
+    B, H_kv, C, D = _kv4_dims(cache)
+    dtype = dtype if dtype is not None else (torch.bfloat16 if k is None else k.dtype)
+    code = _dtype_code(dtype)
+    T = int(T)
+    if T <= 0:
+        raise ValueError("T must be positive")
+    _like(k, "k", (B, T, H_kv, D), dtype)
+    _like(v, "v", (B, T, H_kv, D), dtype)
+    _ints(start, "start", B)
+    _int_buffer(dev_status, "dev_status", 1)
+    _on_device(_kv4_named(cache) + ((k, "k"), (v, "v"), (start, "start"),
+                                    (dev_status, "dev_status")))
+    with _on_stream(stream):
+        if k is None:
+            k = torch.empty(B, T, H_kv, D, dtype=dtype, device=cache.k_codes.device)
+        if v is None:
+            v = torch.empty_like(k)
+    st = lib.kv4_read(*map(_ptr, cache), _ptr(start), _ptr(k), _ptr(v), B, T, H_kv, D, C, code,
+                      _ptr(dev_status), _stream(stream))
+    _check(st, "kv4_read")
+    return k, v
+
+
+def kv4_attn_workspace_bytes(B, S_q, H_q, H_kv, D, C, max_len=None, window=0, n_sink=0,
+                             with_score=False):
+    """Bytes of device workspace ``kv4_attn`` needs for these sizes."""
+    lib = load()
+    n = ctypes.c_size_t()
+    _check(lib.kv4_attn_workspace(B, S_q, H_q, H_kv, D, C, C if max_len is None else int(max_len),
+                                  int(window), int(n_sink), int(bool(with_score)),
+                                  ctypes.byref(n)), "kv4_attn_workspace")
+    return n.value
+
+
+def kv4_attn(q, cache, lens, max_len=None, window=0, n_sink=0, scale=None, out=None, lse=None,
+             score=None, workspace=None, dev_status=None, stream=None):
+    """Attention of new tokens q [B, S_q, H_q, D] (bf16) over a 4-bit cache.
+
+    ``lens`` int32 [B] (CUDA) counts the slots in use, the S_q new tokens'
+    included; ``max_len`` (default: the capacity) bounds it and sizes the
+    launch. ``window`` > 0 limits every query to its last ``window`` slots and
+    the first ``n_sink``. ``score`` float32 [B, H_kv, C]: every slot's weight
+    is added to it. Returns (out [B, S_q, H_q, D], lse [B, H_q, S_q]). A
+    ``workspace`` (uint8, ``kv4_attn_workspace_bytes``) is allocated here when
+    not given; calls that may overlap need their own.
+    """
+    import torch
+    lib = load()
+    B, H_kv, C, D = _kv4_dims(cache)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
+        raise ValueError("q must be [B, S_q, H_q, D] matching the cache")
+    _, S_q, H_q, _ = q.shape
+    max_len = C if max_len is None else int(max_len)
+    _like(out, "out", q.shape, q.dtype)
+    _like(lse, "lse", (B, H_q, S_q), torch.float32)
+    _like(score, "score", (B, H_kv, C), torch.float32)
+    _ints(lens, "lens", B)
+    _int_buffer(dev_status, "dev_status", 1)
+    if workspace is not None and workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a uint8 tensor")
+    code = _dtype_code(q.dtype)
+    _on_device(_kv4_named(cache) + ((q, "q"), (lens, "lens"), (out, "out"), (lse, "lse"),
+                                    (score, "score"), (workspace, "workspace"),
+                                    (dev_status, "dev_status")))
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(B, H_q, S_q, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            need = kv4_attn_workspace_bytes(B, S_q, H_q, H_kv, D, C, max_len, window, n_sink,
+                                            score is not None)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    sc = float(scale) if scale is not None else 0.0
+    st = lib.kv4_attn(_ptr(q), *map(_ptr, cache), _ptr(lens), _ptr(out), _ptr(lse), _ptr(score), B,
+                      S_q, H_q, H_kv, D, C, max_len, int(window), int(n_sink), sc, code,
+                      _ptr(workspace), workspace.numel() if workspace is not None else 0,
+                      _ptr(dev_status), _stream(stream))
+    _check(st, "kv4_attn")
+    return out, lse
+
+
+def kv4_evict(cache, score, lens, budget, n_sink=0, n_recent=0, dst=None, dst_score=None,
+              dst_lens=None, kept=None, dev_status=None, stream=None):
+    """Keeps at most ``budget`` slots a sequence and head: the first
+    ``n_sink``, the last ``n_recent`` and the largest ``score`` float32
+    [B, H_kv, C] between them (ties: the lowest slot), in their order.
+
+    Returns (dst, dst_score, dst_lens, kept): another cache (of capacity
+    ``budget`` rounded up to 16 unless given; it may not share memory with
+    ``cache``), its scores, its lens int32 [B], and kept int32
+    [B, H_kv, budget], every kept slot's place in ``cache`` (-1 past the last).
+    Slots of ``dst`` past the last are left as they were.
+    """
+    import torch
+    lib = load()
+    B, H_kv, C, D = _kv4_dims(cache)
+    budget, n_sink, n_recent = int(budget), int(n_sink), int(n_recent)
+    if budget <= 0:
+        raise ValueError("budget must be positive")
+    dev = cache.k_codes.device
+    C_dst = -(-budget // 16) * 16
+    if dst is not None:
+        dB, dH, C_dst, dD = _kv4_dims(dst)
+        if (dB, dH, dD) != (B, H_kv, D):
+            raise ValueError("dst must have the cache's B, H_kv and D")
+    _like(score, "score", (B, H_kv, C), torch.float32)
+    _like(dst_score, "dst_score", (B, H_kv, C_dst), torch.float32)
+    _like(kept, "kept", (B, H_kv, budget), torch.int32)
+    _ints(lens, "lens", B)
+    _ints(dst_lens, "dst_lens", B)
+    _int_buffer(dev_status, "dev_status", 1)
+    _on_device(_kv4_named(cache) + (_kv4_named(dst, "dst ") if dst is not None else ()) +
+               ((score, "score"), (lens, "lens"), (dst_score, "dst_score"),
+                (dst_lens, "dst_lens"), (kept, "kept"), (dev_status, "dev_status")))
+    with _on_stream(stream):
+        if dst is None:
+            dst = kv4_cache(B, H_kv, C_dst, D, dev)
+        if dst_score is None:
+            dst_score = torch.zeros(B, H_kv, C_dst, dtype=torch.float32, device=dev)
+        if dst_lens is None:
+            dst_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        if kept is None:
+            kept = torch.empty(B, H_kv, budget, dtype=torch.int32, device=dev)
+    st = lib.kv4_evict(*map(_ptr, cache), _ptr(score), _ptr(lens), *map(_ptr, dst),
+                       _ptr(dst_score), _ptr(dst_lens), _ptr(kept), B, H_kv, D, C, C_dst, budget,
+                       n_sink, n_recent, _ptr(dev_status), _stream(stream))
+    _check(st, "kv4_evict")
+    return dst, dst_score, dst_lens, kept
 
 
 def expiry_test(q, k, v, out, lse, dev_status, stream=None):

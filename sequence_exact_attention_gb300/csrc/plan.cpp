@@ -179,8 +179,8 @@ const char* ring_attn_strerror(int status) {
     case RA_ERR_DEVICE: return "no usable CUDA device of compute capability 10.3 (GB300)";
     case RA_ERR_LAUNCH: return "CUDA error while preparing or launching a kernel";
     case RA_ERR_TIMEOUT: return "a device-side bounded wait expired";
-    case RA_ERR_BUFFER: return "caller buffer too small";
-    case RA_ERR_RANGE: return "size out of range (32-bit indexing) or ring step outside [-1, P)";
+    case RA_ERR_BUFFER: return "caller buffer too small, or it overlaps an input";
+    case RA_ERR_RANGE: return "size or index out of range (32-bit indexing; ring step outside [-1, P); cache slots)";
     case RA_ERR_SCRATCH:
       return "problem too large for the library's built-in backward scratch "
              "(8 MiB: at most 2^20 tile-padded query rows; use ring_attn_bwd with a workspace)";
@@ -188,6 +188,6 @@ const char* ring_attn_strerror(int status) {
   }
 }
 
-int ring_attn_version(void) { return 103; }   // 1.03: backward, packed variable lengths, Ulysses layout
+int ring_attn_version(void) { return 104; }   // 1.04: 4-bit key/value cache
 
 }  // extern "C"
