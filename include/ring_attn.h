@@ -360,6 +360,62 @@ ra_status ring_attn_bwd_ulysses(const void* q, const void* k, const void* v,
                                 int* dev_status, void* stream);
 
 /*
+ * ring_attn_fwd_window - ring attention with a sliding window and a few first
+ * tokens that stay visible. The pages have no counterpart; definition, ring
+ * and layouts are those of ring_attn_fwd_ex (causal, all steps), with the
+ * allowed keys
+ *     A(i) = { j <= i : j > i - window  or  j < n_sink }
+ * window >= 1 (1: only the query's own token, and the first ones), n_sink >=
+ * 0, else RA_ERR_RANGE; values of S and more mean all tokens. A query tile
+ * meets only the key tiles that some row of it sees, so the work grows with
+ * S * window. dtype RA_BF16 or RA_F32; no visit log. Errors as
+ * ring_attn_fwd_ex.
+ * ring_attn_fwd_window_varlen - the same for packed sequences (conventions of
+ * ring_attn_fwd_varlen): windows and first tokens are each sequence's own.
+ */
+ra_status ring_attn_fwd_window(const void* q, const void* k, const void* v,
+                               void* out, float* lse, int B, int H_q, int H_kv,
+                               int S, int D, int P, int window, int n_sink,
+                               float scale, int dtype, int order,
+                               int* dev_status, void* stream);
+ra_status ring_attn_fwd_window_varlen(const void* q, const void* k, const void* v,
+                                      void* out, float* lse, const int* cu_seqlens,
+                                      int n_seq, int total, int max_seqlen,
+                                      int H_q, int H_kv, int D, int P, int window,
+                                      int n_sink, float scale, int dtype, int order,
+                                      int* dev_status, void* stream);
+
+/*
+ * ring_attn_bwd_window - gradients of ring_attn_fwd_window (formulas and
+ * conventions of ring_attn_bwd, sums over A(i)); ring_attn_bwd_window_varlen
+ * those of the packed form. RA_BF16 only. The workspace size comes from
+ * ring_attn_bwd_window_workspace with the call's sizes (packed: B = n_seq,
+ * S = max_seqlen, varlen = 1); beside the row statistics it holds float32
+ * parts of dK and dV of the key tiles with first tokens, which the whole
+ * sequence sees and whose work is therefore shared out. Gradients repeat bit
+ * for bit. Errors as ring_attn_bwd, RA_ERR_RANGE for window and n_sink.
+ */
+ra_status ring_attn_bwd_window_workspace(int B, int H_q, int H_kv, int S, int D, int P,
+                                         int window, int n_sink, int order, int varlen,
+                                         size_t* bytes);
+ra_status ring_attn_bwd_window(const void* q, const void* k, const void* v,
+                               const void* out, const float* lse, const void* dout,
+                               void* dq, void* dk, void* dv,
+                               int B, int H_q, int H_kv, int S, int D, int P,
+                               int window, int n_sink, float scale, int dtype,
+                               int order, void* workspace, size_t workspace_bytes,
+                               int* dev_status, void* stream);
+ra_status ring_attn_bwd_window_varlen(const void* q, const void* k, const void* v,
+                                      const void* out, const float* lse,
+                                      const void* dout, void* dq, void* dk, void* dv,
+                                      const int* cu_seqlens, int n_seq, int total,
+                                      int max_seqlen, int H_q, int H_kv, int D, int P,
+                                      int window, int n_sink, float scale, int dtype,
+                                      int order, void* workspace,
+                                      size_t workspace_bytes, int* dev_status,
+                                      void* stream);
+
+/*
  * attn_lse_merge - exact merge of two partial attention results over
  * disjoint key sets (glossary "sequence parallelism transformers",
  * §Ring Attention and §Implementation Considerations):
@@ -525,7 +581,7 @@ const char* ring_attn_strerror(int status);
 
 /* Library ABI version (major * 100 + minor); 103 adds the backward, the
  * packed variable-length and the Ulysses-layout entry points, 104 the 4-bit
- * key/value cache. */
+ * key/value cache and the windowed entry points. */
 int ring_attn_version(void);
 
 #ifdef __cplusplus

@@ -26,6 +26,8 @@ Everything here is float64 NumPy, written to be read against the pages:
   sequences of different lengths, each its own problem.
 * ``ulysses_attention`` - the Ulysses steps (all-to-all to heads, full
   attention per head group, all-to-all back) on sequence-sharded tensors.
+* ``window_attention``, ``window_backward`` (and ``_varlen``) - attention with
+  a sliding window and first tokens that stay visible, and its gradients.
 * ``kv4``               - the 4-bit key/value cache: quantising, what codes
   stand for, attention of a few tokens over a cache, eviction.
 * ``tile_visits``       - expands the chunk-level schedule into the sequence of
@@ -48,6 +50,8 @@ from .ring import ring_attention
 from .backward import attention_backward, ring_attention_backward, backward_rows
 from .varlen import attention_varlen, attention_backward_varlen
 from . import kv4
+from .window import (window_attention, window_attention_varlen, window_backward,
+                     window_backward_varlen)
 from .ulysses import (ulysses_attention, to_sequence_shards, from_sequence_shards,
                       all_to_all_seq_to_head, all_to_all_head_to_seq)
 
@@ -57,6 +61,7 @@ __all__ = [
     "SKIP", "FULL", "PARTIAL", "ORDER_CONTIGUOUS", "ORDER_ZIGZAG",
     "rank_segments", "ring_schedule", "schedule_table", "tile_visits",
     "ring_attention", "kv4",
+    "window_attention", "window_attention_varlen", "window_backward", "window_backward_varlen",
     "attention_backward", "ring_attention_backward", "backward_rows",
     "attention_varlen", "attention_backward_varlen",
     "ulysses_attention", "to_sequence_shards", "from_sequence_shards",

@@ -34,6 +34,9 @@ EXPORTS = ("ring_attn_fwd", "ring_attn_fwd_ex", "ring_attn_visit_log_len",
            "ring_attn_bwd_ulysses",
            "ring_attn_bwd_workspace", "ring_attn_bwd", "ring_attn_bwd_ex",
            "ring_attn_bwd_noalloc",
+           "ring_attn_fwd_window", "ring_attn_fwd_window_varlen",
+           "ring_attn_bwd_window_workspace", "ring_attn_bwd_window",
+           "ring_attn_bwd_window_varlen",
            "attn_lse_merge", "attn_lse_merge_n",
            "kv4_append", "kv4_read", "kv4_attn_workspace", "kv4_attn", "kv4_evict",
            "ring_attn_plan",
@@ -102,6 +105,21 @@ def load():
     lib.ring_attn_bwd_varlen.restype = c_int
     lib.ring_attn_bwd_varlen.argtypes = ([vp] * 10 + [c_int] * 8 + [c_float, c_int, c_int, vp,
                                                                     ctypes.c_size_t, vp, vp])
+    lib.ring_attn_fwd_window.restype = c_int
+    lib.ring_attn_fwd_window.argtypes = ([vp] * 5 + [c_int] * 8 + [c_float, c_int, c_int, vp, vp])
+    lib.ring_attn_fwd_window_varlen.restype = c_int
+    lib.ring_attn_fwd_window_varlen.argtypes = ([vp] * 6 + [c_int] * 9 + [c_float, c_int, c_int,
+                                                                          vp, vp])
+    lib.ring_attn_bwd_window_workspace.restype = c_int
+    lib.ring_attn_bwd_window_workspace.argtypes = ([c_int] * 10 +
+                                                   [ctypes.POINTER(ctypes.c_size_t)])
+    lib.ring_attn_bwd_window.restype = c_int
+    lib.ring_attn_bwd_window.argtypes = ([vp] * 9 + [c_int] * 8 + [c_float, c_int, c_int, vp,
+                                                                   ctypes.c_size_t, vp, vp])
+    lib.ring_attn_bwd_window_varlen.restype = c_int
+    lib.ring_attn_bwd_window_varlen.argtypes = ([vp] * 10 + [c_int] * 9 +
+                                                [c_float, c_int, c_int, vp, ctypes.c_size_t, vp,
+                                                 vp])
     lib.attn_lse_merge.restype = c_int
     lib.attn_lse_merge.argtypes = [vp] * 6 + [c_int] * 5 + [vp]
     lib.attn_lse_merge_n.restype = c_int
@@ -522,6 +540,160 @@ def ring_attn_bwd_ulysses(q, k, v, out, lse, dout, S, causal, scale=None, worksp
     return dq, dk, dv
 
 
+def _on_stream(stream):
+    """Memory handed out inside belongs to the stream the call runs on."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def ring_attn_fwd_window(q, k, v, P, window, n_sink=0, scale=None, order="contiguous", out=None,
+                         lse=None, want_lse=True, dev_status=None, stream=None):
+    """Causal ring attention in which query i sees the ``window`` tokens up to
+    itself and the first ``n_sink`` tokens; q [B,S,H_q,D], k/v [B,S,H_kv,D],
+    bf16 or float32. Returns (out, lse)."""
+    import torch
+    lib = load()
+    B, S, H_q, D = q.shape
+    H_kv = k.shape[2]
+    _like(k, "k", (B, S, H_kv, D), q.dtype)
+    _like(v, "v", (B, S, H_kv, D), q.dtype)
+    _like(out, "out", q.shape, q.dtype)
+    _like(lse, "lse", (B, H_q, S), torch.float32)
+    _int_buffer(dev_status, "dev_status", 1)
+    code = _dtype_code(q.dtype)
+    _on_device(((q, "q"), (k, "k"), (v, "v"), (out, "out"), (lse, "lse"),
+                (dev_status, "dev_status")))
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty(B, H_q, S, device=q.device, dtype=torch.float32)
+    sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
+    st = lib.ring_attn_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H_q, H_kv, S,
+                                  D, P, int(window), int(n_sink), sc, code, ORDERS[order],
+                                  _ptr(dev_status), _stream(stream))
+    _check(st, "ring_attn_fwd_window")
+    return out, lse
+
+
+def ring_attn_fwd_window_varlen(q, k, v, cu_seqlens, max_seqlen, P, window, n_sink=0, scale=None,
+                                order="contiguous", out=None, lse=None, dev_status=None,
+                                stream=None):
+    """``ring_attn_fwd_window`` of packed sequences: q [total,H_q,D], k/v
+    [total,H_kv,D], cu_seqlens int32 [n+1] (CUDA); windows and first tokens
+    are each sequence's own. Returns (out [total,H_q,D], lse [H_q,total])."""
+    import torch
+    lib = load()
+    total, H_q, H_kv, D, n, mx = _varlen_args(q, k, v, cu_seqlens, max_seqlen)
+    _like(out, "out", q.shape, q.dtype)
+    _like(lse, "lse", (H_q, total), torch.float32)
+    _int_buffer(dev_status, "dev_status", 1)
+    code = _dtype_code(q.dtype)
+    _on_device(((q, "q"), (k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens"), (out, "out"),
+                (lse, "lse"), (dev_status, "dev_status")))
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(H_q, total, device=q.device, dtype=torch.float32)
+    sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
+    st = lib.ring_attn_fwd_window_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                         _ptr(cu_seqlens), n, total, mx, H_q, H_kv, D, P,
+                                         int(window), int(n_sink), sc, code, ORDERS[order],
+                                         _ptr(dev_status), _stream(stream))
+    _check(st, "ring_attn_fwd_window_varlen")
+    return out, lse
+
+
+def bwd_window_workspace_bytes(B, H_q, H_kv, S, D, P, window, n_sink=0, order="contiguous",
+                               varlen=False):
+    """Bytes of device workspace ``ring_attn_bwd_window`` needs (packed: B
+    sequences of at most S tokens, ``varlen``)."""
+    lib = load()
+    n = ctypes.c_size_t()
+    _check(lib.ring_attn_bwd_window_workspace(B, H_q, H_kv, S, D, P, int(window), int(n_sink),
+                                              ORDERS[order], int(bool(varlen)), ctypes.byref(n)),
+           "ring_attn_bwd_window_workspace")
+    return n.value
+
+
+def ring_attn_bwd_window(q, k, v, out, lse, dout, P, window, n_sink=0, scale=None,
+                         order="contiguous", dq=None, dk=None, dv=None, workspace=None,
+                         dev_status=None, stream=None):
+    """Gradients (dq, dk, dv) of ``ring_attn_fwd_window`` (bf16) for the
+    upstream dout; ``workspace`` (uint8, ``bwd_window_workspace_bytes``) is
+    allocated here when not given."""
+    import torch
+    lib = load()
+    B, S, H_q, D = q.shape
+    H_kv = k.shape[2]
+    for t, n in ((k, "k"), (v, "v"), (dk, "dk"), (dv, "dv")):
+        _like(t, n, (B, S, H_kv, D), q.dtype)
+    for t, n in ((out, "out"), (dout, "dout"), (dq, "dq")):
+        _like(t, n, q.shape, q.dtype)
+    _like(lse, "lse", (B, H_q, S), torch.float32)
+    _int_buffer(dev_status, "dev_status", 1)
+    if workspace is not None and workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a uint8 tensor")
+    code = _dtype_code(q.dtype)
+    _on_device(((q, "q"), (k, "k"), (v, "v"), (out, "out"), (lse, "lse"), (dout, "dout"),
+                (dq, "dq"), (dk, "dk"), (dv, "dv"), (workspace, "workspace"),
+                (dev_status, "dev_status")))
+    with _on_stream(stream):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None:
+            need = bwd_window_workspace_bytes(B, H_q, H_kv, S, D, P, window, n_sink, order)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
+    st = lib.ring_attn_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+                                  _ptr(dq), _ptr(dk), _ptr(dv), B, H_q, H_kv, S, D, P,
+                                  int(window), int(n_sink), sc, code, ORDERS[order],
+                                  _ptr(workspace), workspace.numel(), _ptr(dev_status),
+                                  _stream(stream))
+    _check(st, "ring_attn_bwd_window")
+    return dq, dk, dv
+
+
+def ring_attn_bwd_window_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, P, window,
+                                n_sink=0, scale=None, order="contiguous", dq=None, dk=None,
+                                dv=None, workspace=None, dev_status=None, stream=None):
+    """Gradients (dq, dk, dv) of ``ring_attn_fwd_window_varlen`` for the
+    upstream dout."""
+    import torch
+    lib = load()
+    total, H_q, H_kv, D, n, mx = _varlen_args(q, k, v, cu_seqlens, max_seqlen)
+    for t, name in ((out, "out"), (dout, "dout"), (dq, "dq")):
+        _like(t, name, q.shape, q.dtype)
+    for t, name in ((dk, "dk"), (dv, "dv")):
+        _like(t, name, k.shape, q.dtype)
+    _like(lse, "lse", (H_q, total), torch.float32)
+    _int_buffer(dev_status, "dev_status", 1)
+    if workspace is not None and workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a uint8 tensor")
+    code = _dtype_code(q.dtype)
+    _on_device(((q, "q"), (k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens"), (out, "out"),
+                (lse, "lse"), (dout, "dout"), (dq, "dq"), (dk, "dk"), (dv, "dv"),
+                (workspace, "workspace"), (dev_status, "dev_status")))
+    with _on_stream(stream):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None:
+            need = bwd_window_workspace_bytes(n, H_q, H_kv, mx, D, P, window, n_sink, order, True)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
+    st = lib.ring_attn_bwd_window_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                         _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
+                                         _ptr(cu_seqlens), n, total, mx, H_q, H_kv, D, P,
+                                         int(window), int(n_sink), sc, code, ORDERS[order],
+                                         _ptr(workspace), workspace.numel(), _ptr(dev_status),
+                                         _stream(stream))
+    _check(st, "ring_attn_bwd_window_varlen")
+    return dq, dk, dv
+
+
 def attn_lse_merge(o_a, lse_a, o_b, lse_b, out=None, lse=None, stream=None):
     """Pairwise merge; o_* [B,S,H,D], lse_* [B,H,S] float32."""
     import torch
@@ -618,12 +790,6 @@ def _ints(t, name, n):
     """A contiguous int32 [n] tensor (None: not given)."""
     import torch
     _like(t, name, (n,), torch.int32)
-
-
-def _on_stream(stream):
-    """Memory handed out inside belongs to the stream the call runs on."""
-    import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def kv4_append(cache, k, v, start, n_new=None, dev_status=None, stream=None):

@@ -16,6 +16,19 @@ bool aligned(const void* p, uintptr_t a) {
 
 constexpr long long kMaxElems = 0x7fffffffLL;   // 32-bit element indexing
 
+// Geometry of a windowed call over sequences of at most S tokens.
+ra_status make_window_geometry(int B, int H_q, int H_kv, int S, int D, int P, int window,
+                               int n_sink, float scale, int order, int tile, WinGeometry* g) {
+  *g = WinGeometry();
+  const ra_status st = make_geometry(B, H_q, H_kv, S, D, P, 1, scale, order, -1, tile, g);
+  if (st != RA_OK) return st;
+  if (window <= 0 || n_sink < 0) return RA_ERR_RANGE;
+  g->window = window < S ? window : S;
+  g->n_sink = n_sink < S ? n_sink : S;
+  g->sink_splits = 1;
+  return RA_OK;
+}
+
 ra_status check_attn_args(const void* q, const void* k, const void* v,
                           const void* out, const float* lse, int B, int H_q,
                           int H_kv, int S, int D, int dtype, int step,
@@ -273,6 +286,142 @@ ra_status ring_attn_bwd_varlen(const void* q, const void* k, const void* v, cons
   return launch_attn_bwd(g, q, k, v, out, lse, dout, dq, dk, dv,
                          static_cast<float*>(workspace), RA_BWD_ALL, dev_status,
                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+ra_status ring_attn_fwd_window(const void* q, const void* k, const void* v, void* out,
+                               float* lse, int B, int H_q, int H_kv, int S, int D, int P,
+                               int window, int n_sink, float scale, int dtype, int order,
+                               int* dev_status, void* stream) {
+  ra_status st = check_attn_args(q, k, v, out, lse, B, H_q, H_kv, S, D, dtype, -1, nullptr,
+                                 dev_status);
+  if (st != RA_OK) return st;
+  WinGeometry g;
+  st = make_window_geometry(B, H_q, H_kv, S, D, P, window, n_sink, scale, order,
+                            tile_rows_for(dtype, D), &g);
+  if (st != RA_OK) return st;
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != RA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == RA_F32)
+    return launch_attn_simt_window(g, static_cast<const float*>(q),
+                                   static_cast<const float*>(k), static_cast<const float*>(v),
+                                   static_cast<float*>(out), lse, dev_status, s);
+  return launch_attn_tc_window(g, q, k, v, out, lse, dev_status, s);
+}
+
+ra_status ring_attn_fwd_window_varlen(const void* q, const void* k, const void* v, void* out,
+                                      float* lse, const int* cu_seqlens, int n_seq, int total,
+                                      int max_seqlen, int H_q, int H_kv, int D, int P,
+                                      int window, int n_sink, float scale, int dtype, int order,
+                                      int* dev_status, void* stream) {
+  if (!cu_seqlens) return RA_ERR_NULL;
+  if (n_seq <= 0 || total <= 0 || max_seqlen <= 0) return RA_ERR_SHAPE;
+  if (!aligned(cu_seqlens, 4)) return RA_ERR_ALIGN;
+  ra_status st = check_attn_args(q, k, v, out, lse, 1, H_q, H_kv, total, D, dtype, -1, nullptr,
+                                 dev_status);
+  if (st != RA_OK) return st;
+  if ((long long)n_seq * max_seqlen * H_q > kMaxElems) return RA_ERR_RANGE;
+  WinGeometry g;
+  st = make_window_geometry(n_seq, H_q, H_kv, max_seqlen, D, P, window, n_sink, scale, order,
+                            tile_rows_for(dtype, D), &g);
+  if (st != RA_OK) return st;
+  g.cu_seqlens = cu_seqlens;
+  g.total = total;
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != RA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == RA_F32)
+    return launch_attn_simt_window(g, static_cast<const float*>(q),
+                                   static_cast<const float*>(k), static_cast<const float*>(v),
+                                   static_cast<float*>(out), lse, dev_status, s);
+  return launch_attn_tc_window(g, q, k, v, out, lse, dev_status, s);
+}
+
+ra_status ring_attn_bwd_window_workspace(int B, int H_q, int H_kv, int S, int D, int P,
+                                         int window, int n_sink, int order, int varlen,
+                                         size_t* bytes) {
+  if (!bytes) return RA_ERR_NULL;
+  if (D != 64 && D != 128) return RA_ERR_HEADDIM;
+  WinGeometry g;
+  ra_status st = make_window_geometry(B, H_q, H_kv, S, D, P, window, n_sink, 0.f, order,
+                                      tile_rows_for(RA_BF16, D), &g);
+  if (st != RA_OK) return st;
+  static const int kPacked = 0;
+  if (varlen) g.cu_seqlens = &kPacked;      // only whether it is set matters here
+  const long long n = bwd_workspace_floats(g);
+  if (n / 2 > kMaxElems) return RA_ERR_RANGE;
+  *bytes = (size_t)(n + plan_window_bwd(&g)) * sizeof(float);
+  return RA_OK;
+}
+
+ra_status ring_attn_bwd_window(const void* q, const void* k, const void* v, const void* out,
+                               const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                               int B, int H_q, int H_kv, int S, int D, int P, int window,
+                               int n_sink, float scale, int dtype, int order, void* workspace,
+                               size_t workspace_bytes, int* dev_status, void* stream) {
+  if (!lse || !dout || !dq || !dk || !dv || !workspace) return RA_ERR_NULL;
+  ra_status st = check_attn_args(q, k, v, out, lse, B, H_q, H_kv, S, D, dtype, -1, nullptr,
+                                 dev_status);
+  if (st != RA_OK) return st;
+  if (dtype != RA_BF16) return RA_ERR_DTYPE;
+  if (!aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) ||
+      !aligned(workspace, 16))
+    return RA_ERR_ALIGN;
+  WinGeometry g;
+  st = make_window_geometry(B, H_q, H_kv, S, D, P, window, n_sink, scale, order,
+                            tile_rows_for(dtype, D), &g);
+  if (st != RA_OK) return st;
+  size_t need = 0;
+  st = ring_attn_bwd_window_workspace(B, H_q, H_kv, S, D, P, window, n_sink, order, 0, &need);
+  if (st != RA_OK) return st;
+  if (workspace_bytes < need) return RA_ERR_BUFFER;
+  plan_window_bwd(&g);
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != RA_OK) return st;
+  return launch_attn_bwd_window(g, q, k, v, out, lse, dout, dq, dk, dv,
+                                static_cast<float*>(workspace), dev_status,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+ra_status ring_attn_bwd_window_varlen(const void* q, const void* k, const void* v,
+                                      const void* out, const float* lse, const void* dout,
+                                      void* dq, void* dk, void* dv, const int* cu_seqlens,
+                                      int n_seq, int total, int max_seqlen, int H_q, int H_kv,
+                                      int D, int P, int window, int n_sink, float scale,
+                                      int dtype, int order, void* workspace,
+                                      size_t workspace_bytes, int* dev_status, void* stream) {
+  if (!cu_seqlens || !lse || !dout || !dq || !dk || !dv || !workspace) return RA_ERR_NULL;
+  if (n_seq <= 0 || total <= 0 || max_seqlen <= 0) return RA_ERR_SHAPE;
+  if (!aligned(cu_seqlens, 4)) return RA_ERR_ALIGN;
+  ra_status st = check_attn_args(q, k, v, out, lse, 1, H_q, H_kv, total, D, dtype, -1, nullptr,
+                                 dev_status);
+  if (st != RA_OK) return st;
+  if (dtype != RA_BF16) return RA_ERR_DTYPE;
+  if (!aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) ||
+      !aligned(workspace, 16))
+    return RA_ERR_ALIGN;
+  if ((long long)n_seq * max_seqlen * H_q > kMaxElems) return RA_ERR_RANGE;
+  WinGeometry g;
+  st = make_window_geometry(n_seq, H_q, H_kv, max_seqlen, D, P, window, n_sink, scale, order,
+                            tile_rows_for(dtype, D), &g);
+  if (st != RA_OK) return st;
+  g.cu_seqlens = cu_seqlens;
+  g.total = total;
+  size_t need = 0;
+  st = ring_attn_bwd_window_workspace(n_seq, H_q, H_kv, max_seqlen, D, P, window, n_sink, order,
+                                      1, &need);
+  if (st != RA_OK) return st;
+  if (workspace_bytes < need) return RA_ERR_BUFFER;
+  plan_window_bwd(&g);
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != RA_OK) return st;
+  return launch_attn_bwd_window(g, q, k, v, out, lse, dout, dq, dk, dv,
+                                static_cast<float*>(workspace), dev_status,
+                                reinterpret_cast<cudaStream_t>(stream));
 }
 
 ra_status attn_lse_merge_n(const void* const* o, const float* const* lse,

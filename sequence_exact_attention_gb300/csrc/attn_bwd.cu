@@ -23,6 +23,13 @@
 //       dV += P^T dO, dK += dS^T Q      tensor cores, A operand from TMEM
 //  3. bwd_dq_kernel: one CTA per query tile, walking the key tiles in the
 //     forward's ring order: S = Q K^T, dP = dO V^T, dS, dQ += dS K.
+// With a sliding window and first tokens that stay visible (WinGeometry) the
+// same kernels walk only the tiles that see each other, and a pair is also
+// masked where its key lies between the first tokens and the query's window.
+// The key tiles that hold a first token are seen from the whole sequence:
+// their walks would outlast all others, so each is cut into shares of the
+// query positions, one CTA each, whose float32 dV and dK meet in
+// bwd_sink_join_kernel (in a fixed order: no atomics here either).
 // The two gradient kernels both recompute S and dP; in exchange neither needs
 // atomics, and each gradient is accumulated on chip and written once.
 //
@@ -34,12 +41,15 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "checks.cuh"
 #include "fastmath.cuh"
 #include "q_iter.cuh"
 #include "ra_internal.h"
 #include "ring_iter.cuh"
 #include "sm100.cuh"
+#include "window_iter.cuh"
 
 namespace ra {
 namespace {
@@ -264,12 +274,12 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (
 // Warp w covers key rows 32 (w mod 4) .. +31 and query columns 64 (w / 4)
 // .. +63; its bf16 P^T and dS^T go into the first 32 columns of its own
 // S^T and dP^T column ranges, so no warp writes columns another one reads.
-template <int D, bool kVarlen>
+template <int D, bool kVarlen, class G = Geometry>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v,
-                const __grid_constant__ CUtensorMap tm_do, const Geometry gp,
+                const __grid_constant__ CUtensorMap tm_do, const G gp,
                 const float* __restrict__ lse2, const float* __restrict__ delta,
                 __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
                 int* __restrict__ status) {
@@ -287,23 +297,57 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
   // work item: key tile kt of kv head hk; (batch, kv head) outermost so that
   // the CTAs resident together read the queries of one group from L2; key
   // tiles in position order (most causal work first).
+  constexpr bool kWin = std::is_same<G, WinGeometry>::value;
+  using Walk = typename std::conditional<kWin, WinQIterT<kT>, QIter>::type;
   const int grp = gp.H_q / gp.H_kv;
   const int n_kt = gp.n_seg * gp.nt;
-  const int kt = (int)(blockIdx.x % n_kt);
-  const int bhk = (int)(blockIdx.x / n_kt);
+  int kt = (int)(blockIdx.x % n_kt);
+  int bhk = (int)(blockIdx.x / n_kt);
+  // the shares of the key tiles with first tokens come first: the longest walks
+  int share = -1, ordinal = 0;
+  if constexpr (kWin) {
+    const int n_share = gp.B * gp.H_kv * gp.sink_tiles * gp.sink_splits;
+    int block = (int)blockIdx.x;
+    if (block < n_share) {
+      share = block % gp.sink_splits;
+      block /= gp.sink_splits;
+      ordinal = block % gp.sink_tiles;
+      bhk = block / gp.sink_tiles;
+    } else {
+      kt = (block - n_share) % n_kt;
+      bhk = (block - n_share) / n_kt;
+    }
+  }
   const int b = bhk / gp.H_kv, hk = bhk % gp.H_kv;
-  const int kseg = kt / gp.nt, kti = kt % gp.nt;
+  int kseg = kt / gp.nt, kti = kt % gp.nt;
   // packed variable-length sequences: b is the sequence, `g` its geometry
-  Geometry gv;
+  G gv;
   int row0 = 0;
-  if constexpr (kVarlen) varlen_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
-  const Geometry& g = kVarlen ? gv : gp;
+  if constexpr (kVarlen && kWin)
+    varlen_window_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
+  else if constexpr (kVarlen)
+    varlen_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
+  const G& g = kVarlen ? gv : gp;
+  if constexpr (kWin) {
+    if (share >= 0) {
+      if (!sink_tile(g, ordinal, kseg, kti)) return;
+    } else if (kseg * g.seg_len + kti * kT < g.n_sink) {
+      return;                        // its shares do the work
+    }
+  }
   const SegRows kr = seg_rows(gp, b, kseg, row0, kVarlen);   // the key tile's rows
   const int src = seg_owner(g, kseg);
   const int kv_lo = kseg * g.seg_len + kti * kT;
   const int kv_valid = tile_tokens(g, kseg, kti);   // <= 0: padding only
   const int h0 = hk * grp;
   if (kv_valid <= 0) return;     // no key, no gradient row: the CTA leaves at once
+  auto start = [&](Walk& it) {
+    if constexpr (kWin)
+      it.init(g, src, kv_lo, kv_valid, h0, h0 + grp, share > 0 ? share * gp.sink_span : 0,
+              share >= 0 && share + 1 < gp.sink_splits ? (share + 1) * gp.sink_span : g.S);
+    else
+      it.init(g, src, kv_lo, kv_valid, h0, h0 + grp);
+  };
 
   init_barriers<C>(bar, abort_flag, never);
   if (warp == kMmaWarp) {
@@ -324,8 +368,8 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
         tma_load_4d(base + C::kFixB + bx * kBoxBytes, &tm_v, bar(C::bFix), bx * 64, hk,
                     kr.trow + kv_lo, kr.tbat);
       }
-      QIter it;
-      it.init(g, src, kv_lo, kv_valid, h0, h0 + grp);
+      Walk it;
+      start(it);
       QTile qt;
       int j = 0;
       while (it.next(g, qt)) {
@@ -374,8 +418,8 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
       const uint64_t q_mn = sw128_desc(base + C::kStage0, kBoxBytes, 1024);
       const uint64_t do_mn = sw128_desc(base + C::kStage0 + C::kTileBytes, kBoxBytes, 1024);
       bool ok = mbar_wait_warp(bar(C::bFix), 0, abort_flag, kTimeoutNs);
-      QIter it;
-      it.init(g, src, kv_lo, kv_valid, h0, h0 + grp);
+      Walk it;
+      start(it);
       QTile qt;
       // S^T(j+1) is issued as soon as dV(j) has read P^T(j) (they share
       // columns), before dK(j): the next P^T pass then overlaps dK(j) and
@@ -466,8 +510,8 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
     const uint32_t c0 = (uint32_t)(hf * 64);          // this warp's first column
     const int kpos = kv_lo + row;
     const uint64_t sl2x2 = pack2(g.scale_log2, g.scale_log2);
-    QIter it;
-    it.init(g, src, kv_lo, kv_valid, h0, h0 + grp);
+    Walk it;
+    start(it);
     QTile qt;
     int j = 0;
     bool ok = true;
@@ -506,6 +550,13 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             if (i < lim) p[i] = 0.f;
+          if constexpr (kWin) {
+            // queries that have left the key behind
+            const int end = kpos < g.n_sink ? 64 : lim + g.window;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= end) p[i] = 0.f;
+          }
         }
         uint32_t pk[32];
 #pragma unroll
@@ -564,6 +615,24 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
             for (int i = 0; i < 32; ++i) u[i] = 0u;
           }
+          if constexpr (kWin) {
+            if (share >= 0 && gp.sink_splits > 1) {
+              // a share's float32 part: [bhk][ordinal][share][dV, dK][row][D]
+              const long long part =
+                  ((((long long)bhk * gp.sink_tiles + ordinal) * gp.sink_splits + share) * 2 +
+                   which) * kT + row;
+              if (in_range(part, 1, (long long)gp.B * gp.H_kv * gp.sink_tiles * gp.sink_splits *
+                                        2 * kT, status)) {
+                float4* dst4 = reinterpret_cast<float4*>(gp.sink_part + part * D + col);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  dst4[i] = make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                                        __uint_as_float(u[4 * i + 2]),
+                                        __uint_as_float(u[4 * i + 3]));
+              }
+              continue;
+            }
+          }
           if (row_ok) store_row32(dst + col, u, mul);
         }
       }
@@ -578,6 +647,45 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
     atomicExch(status, (int)RA_ERR_TIMEOUT);
 }
 
+// Joins the shares of the key tiles with first tokens: one block a (batch, kv
+// head, tile, 16 rows); shares are added in order.
+constexpr int kJoinRows = 16;
+template <int D, bool kVarlen>
+__global__ void __launch_bounds__(256)
+bwd_sink_join_kernel(const WinGeometry gp, __nv_bfloat16* __restrict__ dk,
+                     __nv_bfloat16* __restrict__ dv, int* __restrict__ status) {
+  int block = (int)blockIdx.x;
+  const int r0 = block % (kT / kJoinRows) * kJoinRows;
+  block /= kT / kJoinRows;
+  const int ordinal = block % gp.sink_tiles;
+  const int bhk = block / gp.sink_tiles, b = bhk / gp.H_kv, hk = bhk % gp.H_kv;
+  WinGeometry gv;
+  int row0 = 0;
+  if constexpr (kVarlen) varlen_window_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
+  const WinGeometry& g = kVarlen ? gv : gp;
+  int seg, ti;
+  if (!sink_tile(g, ordinal, seg, ti)) return;
+  const int valid = tile_tokens(g, seg, ti);
+  const size_t grow = seg_rows(gp, b, seg, row0, kVarlen).grow + (size_t)seg * g.seg_len + ti * kT;
+  const float4* part = reinterpret_cast<const float4*>(gp.sink_part) +
+                       ((long long)bhk * gp.sink_tiles + ordinal) * gp.sink_splits * 2 * kT * (D / 4);
+  for (int i = threadIdx.x; i < 2 * kJoinRows * (D / 4); i += 256) {
+    const int which = i / (kJoinRows * (D / 4));
+    const int row = r0 + i / (D / 4) % kJoinRows, c = i % (D / 4);
+    if (row >= valid) continue;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < gp.sink_splits; ++s) {
+      const float4 x = part[((long long)(s * 2 + which) * kT + row) * (D / 4) + c];
+      y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+    }
+    const float mul = which ? g.scale : 1.f;
+    const size_t off = ((grow + row) * g.H_kv + hk) * D + 4 * c;
+    if (in_range((long long)off, 4, extent_kv(gp), status))
+      *reinterpret_cast<uint2*>((which ? dk : dv) + off) =
+          make_uint2(pack_bf16x2(y.x * mul, y.y * mul), pack_bf16x2(y.z * mul, y.w * mul));
+  }
+}
+
 // ------------------------------------------------------------------ dQ
 // Per visit j the tensor cores run S(j), dP(j), dQ(j); the compute warps read
 // S (pass 1, P kept in registers) and then dP (pass 2), writing bf16 dS into
@@ -585,12 +693,12 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
 // as soon as pass 1 has read S(j), and dP(j+1) right after pass 2, ahead of
 // dQ(j), so both passes of the next visit find their product done. K_j stays
 // in its slot until dQ(j), V_j only until dP(j).
-template <int D, bool kVarlen>
+template <int D, bool kVarlen, class G = Geometry>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
               const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v,
-              const __grid_constant__ CUtensorMap tm_do, const Geometry gp,
+              const __grid_constant__ CUtensorMap tm_do, const G gp,
               const float* __restrict__ lse2, const float* __restrict__ delta,
               __nv_bfloat16* __restrict__ dq, int* __restrict__ status) {
   using C = CfgQ<D>;
@@ -618,10 +726,15 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int seg = qt / gp.nt;
   const int ti = qt % gp.nt;
   // packed variable-length sequences: b is the sequence, `g` its geometry
-  Geometry gv;
+  constexpr bool kWin = std::is_same<G, WinGeometry>::value;
+  using Walk = typename std::conditional<kWin, WinKvIter, KvIter>::type;
+  G gv;
   int row0 = 0;
-  if constexpr (kVarlen) varlen_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
-  const Geometry& g = kVarlen ? gv : gp;
+  if constexpr (kVarlen && kWin)
+    varlen_window_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
+  else if constexpr (kVarlen)
+    varlen_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
+  const G& g = kVarlen ? gv : gp;
   const SegRows qr = seg_rows(gp, b, seg, row0, kVarlen);    // the query tile's rows
   const int r = seg_owner(g, seg);
   const int q_lo = seg * g.seg_len + ti * kT;
@@ -667,7 +780,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
         tma_load_4d(base + C::kFixB + bx * kBoxBytes, &tm_do, bar(C::bFix), bx * 64, h,
                     qr.trow + q_lo, qr.tbat);
       }
-      KvIter it;
+      Walk it;
       it.init(g, r, q_lo, q_valid);
       KvTile kv;
       int nk = 0, nv = 0;                  // K and V tiles loaded
@@ -743,7 +856,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
         __syncwarp();
       };
       bool ok = mbar_wait_warp(bar(C::bFix), 0, abort_flag, kTimeoutNs);
-      KvIter it;
+      Walk it;
       it.init(g, r, q_lo, q_valid);
       KvTile kv;
       bool have = ok && it.next(g, kv);
@@ -821,7 +934,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
     const float nl2_row = wi_ok ? lse2[wi] : -INFINITY;
     const float ndl_row = wi_ok ? delta[wi] : 0.f;
     const uint64_t nl2x2 = pack2(nl2_row, nl2_row), ndlx2 = pack2(ndl_row, ndl_row);
-    KvIter it;
+    Walk it;
     it.init(g, r, q_lo, q_valid);
     KvTile kv;
     int j = 0;
@@ -855,6 +968,14 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             if (i >= lim) p[i] = 0.f;
+          if constexpr (kWin) {
+            // keys between the first tokens and the row's window
+            const int w_lo = q_pos - g.window + 1 - kv.lo - (int)c0;
+            const int s_hi = g.n_sink - kv.lo - (int)c0;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= s_hi && i < w_lo) p[i] = 0.f;
+          }
         }
       }
       tc_fence_before();
@@ -925,8 +1046,8 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
     atomicExch(status, (int)RA_ERR_TIMEOUT);
 }
 
-template <int D, bool kVarlen>
-ra_status launch_d(const Geometry& g, const CUtensorMap& mq, const CUtensorMap& mk,
+template <int D, bool kVarlen, class G = Geometry>
+ra_status launch_d(const G& g, const CUtensorMap& mq, const CUtensorMap& mk,
                    const CUtensorMap& mv, const CUtensorMap& mdo, const void* out,
                    const float* lse, const void* dout, void* dq, void* dk, void* dv,
                    float* ws, int phases, int* status, cudaStream_t stream) {
@@ -936,9 +1057,12 @@ ra_status launch_d(const Geometry& g, const CUtensorMap& mq, const CUtensorMap& 
   float* delta = ws + rows;
   const long long prep_blocks = rows / 32;
   const long long n_tiles = (long long)g.n_seg * g.nt;
-  const long long grid_kv = n_tiles * g.B * g.H_kv;
+  constexpr bool kWin = std::is_same<G, WinGeometry>::value;
+  long long grid_kv = n_tiles * g.B * g.H_kv;
+  if constexpr (kWin) grid_kv += (long long)g.B * g.H_kv * g.sink_tiles * g.sink_splits;
   const long long grid_q = n_tiles * g.B * g.H_q;
-  if (prep_blocks > 0x7fffffffLL || grid_q > 0x7fffffffLL) return RA_ERR_RANGE;
+  if (prep_blocks > 0x7fffffffLL || grid_q > 0x7fffffffLL || grid_kv > 0x7fffffffLL)
+    return RA_ERR_RANGE;
   if (phases & RA_BWD_PREP) {
     bwd_prep_kernel<D, kVarlen><<<(unsigned)prep_blocks, 256, 0, stream>>>(
         g, static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout),
@@ -946,20 +1070,29 @@ ra_status launch_d(const Geometry& g, const CUtensorMap& mq, const CUtensorMap& 
     if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
   }
   if (phases & RA_BWD_DKDV) {
-    if (cudaFuncSetAttribute(bwd_dkdv_kernel<D, kVarlen>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(bwd_dkdv_kernel<D, kVarlen, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmemBytes) != cudaSuccess)
       return RA_ERR_LAUNCH;
-    bwd_dkdv_kernel<D, kVarlen><<<(unsigned)grid_kv, kThreads, C::kSmemBytes, stream>>>(
+    bwd_dkdv_kernel<D, kVarlen, G><<<(unsigned)grid_kv, kThreads, C::kSmemBytes, stream>>>(
         mq, mk, mv, mdo, g, lse2, delta, static_cast<__nv_bfloat16*>(dk),
         static_cast<__nv_bfloat16*>(dv), status);
     if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
+    if constexpr (kWin) {
+      if (g.sink_tiles > 0 && g.sink_splits > 1) {
+        const long long blocks = (long long)g.B * g.H_kv * g.sink_tiles * (kT / kJoinRows);
+        if (blocks > 0x7fffffffLL) return RA_ERR_RANGE;
+        bwd_sink_join_kernel<D, kVarlen><<<(unsigned)blocks, 256, 0, stream>>>(
+            g, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), status);
+        if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
+      }
+    }
   }
   if (phases & RA_BWD_DQ) {
     using CQ = CfgQ<D>;
-    if (cudaFuncSetAttribute(bwd_dq_kernel<D, kVarlen>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(bwd_dq_kernel<D, kVarlen, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              CQ::kSmemBytes) != cudaSuccess)
       return RA_ERR_LAUNCH;
-    bwd_dq_kernel<D, kVarlen><<<(unsigned)grid_q, kThreads, CQ::kSmemBytes, stream>>>(
+    bwd_dq_kernel<D, kVarlen, G><<<(unsigned)grid_q, kThreads, CQ::kSmemBytes, stream>>>(
         mq, mk, mv, mdo, g, lse2, delta, static_cast<__nv_bfloat16*>(dq), status);
     if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
   }
@@ -999,6 +1132,71 @@ ra_status launch_attn_bwd(const Geometry& g, const void* q, const void* k, const
                                phases, dev_status, stream);
   return launch_d<128, false>(g, mq, mk, mv, mdo, out, lse, dout, dq, dk, dv, workspace,
                               phases, dev_status, stream);
+}
+
+// The tiles with first tokens, and how many shares each is cut into: a share
+// spans as many query positions as an ordinary key tile is seen from, and at
+// least kMinVisits tiles of queries; no more shares than keep the
+// multiprocessors busy four times over (a share costs 2 * 128 * D floats).
+long long plan_window_bwd(WinGeometry* g) {
+  constexpr long long kMaxCtas = 4 * 152;
+  constexpr int kMinVisits = 16;
+  const int grp = g->H_q / g->H_kv;
+  const long long n_kt = (long long)g->n_seg * g->nt;
+  // sequences of a packed batch cut their tiles by their own segment length:
+  // at most one ragged tile a segment more than whole tiles
+  const long long most = (g->n_sink + kT - 1) / kT + g->n_seg + 1;
+  long long tiles = g->n_sink == 0 ? 0 : (n_kt < most ? n_kt : most);
+  if (!g->cu_seqlens) {
+    tiles = 0;
+    for (int seg = 0; seg < g->n_seg; ++seg)
+      for (int ti = 0; ti < g->nt; ++ti) {
+        if ((long long)seg * g->seg_len + (long long)ti * kT >= g->n_sink) break;
+        ++tiles;
+      }
+  }
+  g->sink_tiles = (int)tiles;
+  g->sink_splits = 1;
+  g->sink_span = g->S;
+  g->sink_part = nullptr;
+  if (tiles == 0) return 0;
+  long long span = ((long long)g->window + kT - 1 + kT - 1) / kT * kT;
+  const long long least = (long long)((kMinVisits + grp - 1) / grp) * kT;
+  if (span < least) span = least;
+  long long splits = (g->S + span - 1) / span;
+  const long long one = tiles * g->B * g->H_kv;
+  const long long cap = (kMaxCtas + one - 1) / one;
+  if (splits > cap) {
+    splits = cap;
+    span = ((g->S + splits - 1) / splits + kT - 1) / kT * kT;
+    splits = (g->S + span - 1) / span;
+  }
+  g->sink_splits = (int)splits;
+  g->sink_span = (int)span;
+  return splits > 1 ? one * splits * 2 * kT * g->D : 0;
+}
+
+ra_status launch_attn_bwd_window(const WinGeometry& g, const void* q, const void* k,
+                                 const void* v, const void* out, const float* lse,
+                                 const void* dout, void* dq, void* dk, void* dv,
+                                 float* workspace, int* dev_status, cudaStream_t stream) {
+  const bool varlen = g.cu_seqlens != nullptr;
+  const int mb = varlen ? 1 : g.B, ms = varlen ? g.total : g.S;
+  CUtensorMap mq, mk, mv, mdo;
+  if (!make_bshd_map(&mq, q, mb, ms, g.H_q, g.D, kT) ||
+      !make_bshd_map(&mk, k, mb, ms, g.H_kv, g.D, kT) ||
+      !make_bshd_map(&mv, v, mb, ms, g.H_kv, g.D, kT) ||
+      !make_bshd_map(&mdo, dout, mb, ms, g.H_q, g.D, kT))
+    return RA_ERR_LAUNCH;
+  WinGeometry gl = g;
+  gl.sink_part = workspace + bwd_workspace_floats(g);
+  auto launch = [&](auto fn) {
+    return fn(gl, mq, mk, mv, mdo, out, lse, dout, dq, dk, dv, workspace, RA_BWD_ALL, dev_status,
+              stream);
+  };
+  if (g.D == 64)
+    return varlen ? launch(launch_d<64, true, WinGeometry>) : launch(launch_d<64, false, WinGeometry>);
+  return varlen ? launch(launch_d<128, true, WinGeometry>) : launch(launch_d<128, false, WinGeometry>);
 }
 
 }  // namespace ra

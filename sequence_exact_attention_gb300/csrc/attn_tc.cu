@@ -73,12 +73,14 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "checks.cuh"
 #include "fastmath.cuh"
 #include "ra_internal.h"
 #include "ring_iter.cuh"
 #include "sm100.cuh"
+#include "window_iter.cuh"
 
 namespace ra {
 namespace {
@@ -311,17 +313,23 @@ __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint6
             v_desc + (uint64_t)((kk * 2048) >> 4), idesc, (accumulate || kk > 0) ? 1u : 0u);
 }
 
-template <int D, bool kOutF32, bool kVarlen, bool kWithholdV0>
+// G = WinGeometry: attention with a sliding window and a few first tokens that
+// stay visible. The walk then covers only the key tiles that some row of the
+// block sees, and a score is also masked where its key lies between the first
+// tokens and the row's window.
+template <int D, bool kOutF32, bool kVarlen, bool kWithholdV0, class G = Geometry>
 __global__ void __launch_bounds__(Roles<D>::kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v,
-               const __grid_constant__ CUtensorMap tm_o, const Geometry gp,
+               const __grid_constant__ CUtensorMap tm_o, const G gp,
                void* __restrict__ out, float* __restrict__ lse,
                int* __restrict__ vlog, int log_stride, int* __restrict__ status,
                int tma_out) {
   using C = Cfg<D>;
   using R = Roles<D>;
+  constexpr bool kWin = std::is_same<G, WinGeometry>::value;
+  using Iter = typename std::conditional<kWin, WinKvIter, KvIter>::type;
   // Full bf16 output tiles go out through TMA stores at D = 128 (a row part
   // is 128 bytes); at D = 64 the per-row stores measured faster.
   constexpr bool kTmaOut = !kOutF32 && D == 128;
@@ -358,10 +366,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int bh = b * gp.H_q + h;
   const int seg = qb / nb;
   const int blk = qb - seg * nb;
-  Geometry gv;
+  G gv;
   int row0 = 0;
-  if constexpr (kVarlen) varlen_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
-  const Geometry& g = kVarlen ? gv : gp;
+  if constexpr (kVarlen && kWin)
+    varlen_window_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
+  else if constexpr (kVarlen)
+    varlen_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
+  const G& g = kVarlen ? gv : gp;
   const int r = seg_owner(g, seg);
   const int q_lo = seg * g.seg_len + blk * kBlockRows;
   // rows of the block holding tokens (<= 0: padding only); Q1 takes part
@@ -449,7 +460,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
         return mbar_wait(bar(C::bDone + x % C::kKBuf), (uint32_t)(x / C::kKBuf) & 1, abort_flag,
                          kTimeoutNs);
       };
-      KvIter it;
+      Iter it;
       it.init(g, r, q_lo, q_valid);
       KvTile kv;
       int j = 0;
@@ -535,7 +546,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
       const uint32_t tS0 = tmem, tS1 = tmem + kTile;
       const uint32_t tO0 = tmem + kOCol, tO1 = tmem + kOCol + D;
       // the walk's length, counted while Q lands
-      const int n = kv_walk_length(g, r, q_lo, q_valid);
+      int n;
+      if constexpr (kWin) n = win_walk_length(g, r, q_lo, q_valid);
+      else n = kv_walk_length(g, r, q_lo, q_valid);
       bool ok = mbar_wait_warp(bar(C::bQFull), 0, abort_flag, kTimeoutNs) &&
                 (!two || mbar_wait_warp(bar(C::bQFull + 1), 0, abort_flag, kTimeoutNs));
       if (ok && n > 0) {
@@ -644,7 +657,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
         int* log = (vlog && warp == qi * R::kTileWarps && lane == 0) ? vlog + log_off(qi) : nullptr;
         int n_log = 0;
         const int q_last = q_lo + min(kTile * (qi + 1), q_valid) - 1;
-        KvIter it;
+        Iter it;
         it.init(g, r, q_lo, q_valid);
         KvTile kv;
         bool have = it.next(g, kv);
@@ -671,7 +684,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
           tc_fence_after();
           // tiles the causal rule cuts for this query tile, and ragged tails:
           // columns from lim on (of this part's 64) are masked
-          const bool all_allowed = !g.causal || kv.lo + kv.valid - 1 <= qt_lo;
+          bool all_allowed = !g.causal || kv.lo + kv.valid - 1 <= qt_lo;
+          int w_lo = 0, s_hi = 0;      // window: columns [s_hi, w_lo) are masked too
+          if constexpr (kWin) {
+            all_allowed = all_allowed && (kv.lo > qt_lo + kTile - 1 - g.window ||
+                                          kv.lo + kTile <= g.n_sink);
+            w_lo = q_pos - g.window + 1 - kv.lo - part * 64;
+            s_hi = g.n_sink - kv.lo - part * 64;
+          }
           const bool cut = !(all_allowed && kv.valid == kTile);
           const int lim = (g.causal ? min(kv.valid, q_pos - kv.lo + 1) : kv.valid) - part * 64;
           float m8[8];
@@ -690,7 +710,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (cut) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (c * 32 + i >= lim) u[i] = __float_as_uint(-INFINITY);
+                if (c * 32 + i >= lim || (kWin && c * 32 + i >= s_hi && c * 32 + i < w_lo))
+                  u[i] = __float_as_uint(-INFINITY);
             }
             max_chunk(u, m8);
           }
@@ -720,7 +741,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (cut) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (c * 32 + i >= lim) u[i] = __float_as_uint(-INFINITY);
+                if (c * 32 + i >= lim || (kWin && c * 32 + i >= s_hi && c * 32 + i < w_lo))
+                  u[i] = __float_as_uint(-INFINITY);
             }
             exp_chunk(u, sl2x2, neg_m2, sum2a, sum2b, tS + part * 64 + c * 16);
           }
@@ -796,7 +818,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
       float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
       int j = 0;               // key tiles done
       bool ok = true;
-      KvIter it;
+      Iter it;
       it.init(g, r, q_lo, q_valid);
       KvTile kv;
       bool have = it.next(g, kv);
@@ -841,12 +863,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
           reg_fence(uu[0]);
           reg_fence(uu[1]);
           // tiles the causal rule cuts for this query tile, and ragged tails
-          const bool all_allowed = !g.causal || kv.lo + kv.valid - 1 <= qt_lo;
+          bool all_allowed = !g.causal || kv.lo + kv.valid - 1 <= qt_lo;
+          if constexpr (kWin)
+            all_allowed = all_allowed && (kv.lo > qt_lo + kTile - 1 - g.window ||
+                                          kv.lo + kTile <= g.n_sink);
           if (!(all_allowed && kv.valid == kTile)) {
             const int lim = (g.causal ? min(kv.valid, q_pos - kv.lo + 1) : kv.valid) - part * 64;
+            int w_lo = 0, s_hi = 0;    // window: columns [s_hi, w_lo) are masked too
+            if constexpr (kWin) {
+              w_lo = q_pos - g.window + 1 - kv.lo - part * 64;
+              s_hi = g.n_sink - kv.lo - part * 64;
+            }
 #pragma unroll
             for (int c = 0; c < 64; ++c)
-              if (c >= lim) uu[c / 32][c % 32] = __float_as_uint(-INFINITY);
+              if (c >= lim || (kWin && c >= s_hi && c < w_lo))
+                uu[c / 32][c % 32] = __float_as_uint(-INFINITY);
           }
           float m8[8];
 #pragma unroll
@@ -945,15 +976,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
 }
 
 // ------------------------------------------------------------------ host
-template <int D, bool kOutF32, bool kVarlen = false, bool kWithholdV0 = false>
-ra_status launch_typed(const Geometry& g, const CUtensorMap& mq, const CUtensorMap& mk,
+template <int D, bool kOutF32, bool kVarlen = false, bool kWithholdV0 = false, class G = Geometry>
+ra_status launch_typed(const G& g, const CUtensorMap& mq, const CUtensorMap& mk,
                        const CUtensorMap& mv, const CUtensorMap& mo, bool tma_out, void* out,
                        float* lse, int* vlog, int log_stride, int* status, cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kern = attn_tc_kernel<D, kOutF32, kVarlen, kWithholdV0>;
+  auto kern = attn_tc_kernel<D, kOutF32, kVarlen, kWithholdV0, G>;
   // keys and values of every head within half of the 126 MB L2: order the
   // grid longest block first across all heads
-  Geometry gl = g;
+  G gl = g;
   const long long kv_rows = g.cu_seqlens ? g.total
                             : (g.shard_rows > 0 ? (long long)g.P * g.B * g.shard_rows
                                                 : (long long)g.B * g.S);
@@ -1015,6 +1046,24 @@ ra_status launch_attn_tc_varlen(const Geometry& g, const void* q, const void* k,
                                          dev_status, stream);
   return launch_typed<128, false, true>(g, mq, mk, mv, mo, tma_out, out, lse, nullptr, 0,
                                         dev_status, stream);
+}
+
+ra_status launch_attn_tc_window(const WinGeometry& g, const void* q, const void* k,
+                                const void* v, void* out, float* lse, int* dev_status,
+                                cudaStream_t stream) {
+  const bool varlen = g.cu_seqlens != nullptr;
+  const int nb = varlen ? 1 : g.B, rows = varlen ? g.total : g.S;
+  CUtensorMap mq, mk, mv, mo;
+  if (!make_maps(&mq, &mk, &mv, g, q, k, v, nb, rows)) return RA_ERR_LAUNCH;
+  const bool tma_out = make_out_map(&mo, g, out, nb, rows);
+  auto launch = [&](auto fn) {
+    return fn(g, mq, mk, mv, mo, tma_out, out, lse, nullptr, 0, dev_status, stream);
+  };
+  if (g.D == 64)
+    return varlen ? launch(launch_typed<64, false, true, false, WinGeometry>)
+                  : launch(launch_typed<64, false, false, false, WinGeometry>);
+  return varlen ? launch(launch_typed<128, false, true, false, WinGeometry>)
+                : launch(launch_typed<128, false, false, false, WinGeometry>);
 }
 
 ra_status launch_attn_tc_sharded(const Geometry& g, const void* q, const void* k,

@@ -43,6 +43,20 @@ struct Geometry {
   int qb_major;
 };
 
+// Geometry of attention with a sliding window: query i sees key j <= i when
+// j > i - window or j < n_sink (causal is set, 1 <= window <= S, n_sink <= S).
+// In the dK/dV kernel the key tiles that hold a first token are seen from the
+// whole sequence: their work is cut into `sink_splits` shares of `sink_span`
+// query positions (tiles counted by their first position), joined through
+// `sink_part` when there are more than one.
+struct WinGeometry : Geometry {
+  int window, n_sink;
+  int sink_tiles;      // at most so many key tiles of a sequence hold one
+  int sink_splits;
+  int sink_span;
+  float* sink_part;    // [B * H_kv][sink_tiles][sink_splits][dV, dK][tile][D]
+};
+
 // Host-side planning helpers (plan.cpp).
 ra_status make_geometry(int B, int H_q, int H_kv, int S, int D, int P,
                         int causal, float scale, int order, int step, int tile,
@@ -79,6 +93,15 @@ ra_status launch_attn_tc(const Geometry& g, const void* q, const void* k,
                          const void* v, void* out, float* lse, int* visit_log,
                          int log_stride, int* dev_status, cudaStream_t stream);
 
+// Windowed launches: fixed-length, or packed when g.cu_seqlens is set (no visit
+// log, all steps).
+ra_status launch_attn_tc_window(const WinGeometry& g, const void* q, const void* k,
+                                const void* v, void* out, float* lse, int* dev_status,
+                                cudaStream_t stream);
+ra_status launch_attn_simt_window(const WinGeometry& g, const float* q, const float* k,
+                                  const float* v, float* out, float* lse, int* dev_status,
+                                  cudaStream_t stream);
+
 // TMA map of a [B, S, H, D] bf16 tensor: box = 64 columns x 1 head x
 // `box_rows` rows x 1 batch, 128-byte swizzle (tensor_map.cpp).
 bool make_bshd_map(CUtensorMap* m, const void* ptr, int B, int S, int H, int D,
@@ -91,6 +114,15 @@ ra_status launch_attn_bwd(const Geometry& g, const void* q, const void* k, const
                           const void* out, const float* lse, const void* dout, void* dq,
                           void* dk, void* dv, float* workspace, int phases,
                           int* dev_status, cudaStream_t stream);
+
+// The windowed backward: plan_window_bwd fills the sink fields of g (but for
+// sink_part) and returns the floats of partial sums the launch wants after
+// bwd_workspace_floats(g).
+long long plan_window_bwd(WinGeometry* g);
+ra_status launch_attn_bwd_window(const WinGeometry& g, const void* q, const void* k,
+                                 const void* v, const void* out, const float* lse,
+                                 const void* dout, void* dq, void* dk, void* dv,
+                                 float* workspace, int* dev_status, cudaStream_t stream);
 
 struct MergeArgs {
   const void* o[RA_MERGE_MAX_N];
