@@ -14,7 +14,6 @@ import contextlib
 import ctypes
 import math
 import os
-from typing import NamedTuple
 
 import numpy as np
 
@@ -185,21 +184,24 @@ def visit_log_layout(B, H_q, S, D, P, dtype, order="contiguous"):
 
 def _dtype_code(dt):
     import torch
-    if dt in (torch.bfloat16, "bf16"):
+    if dt is torch.bfloat16 or dt == "bf16":
         return RA_BF16
-    if dt in (torch.float32, "f32"):
+    if dt is torch.float32 or dt == "f32":
         return RA_F32
     raise ValueError(f"unsupported dtype {dt}")
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None
 
 
 def _stream(stream):
+    """The handle of ``stream``, or of torch's current one (asked for without
+    the Stream object that torch.cuda.current_stream() builds: 3 us a call)."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dev(t, name):
@@ -214,7 +216,7 @@ def _like(t, name, shape, dtype):
     exactly the shape and dtype the call implies (None: not given)."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -236,11 +238,13 @@ def _on_device(named):
     devs = set()
     for t, n in named:
         if t is not None:
-            _dev(t, n)
-            devs.add(t.device)
+            if not (t.is_cuda and t.is_contiguous()):
+                _dev(t, n)
+            devs.add(t.get_device())
     if len(devs) > 1:
-        raise ValueError(f"the call's tensors are on several devices: {sorted(map(str, devs))}")
-    if devs and next(iter(devs)).index != torch.cuda.current_device():
+        raise ValueError("the call's tensors are on several devices: "
+                         f"{[f'cuda:{d}' for d in sorted(devs)]}")
+    if devs and next(iter(devs)) != torch.cuda.current_device():
         raise ValueError("the call's tensors must be on the current CUDA device")
 
 
@@ -540,10 +544,15 @@ def ring_attn_bwd_ulysses(q, k, v, out, lse, dout, S, causal, scale=None, worksp
     return dq, dk, dv
 
 
+_NULL_CONTEXT = contextlib.nullcontext()
+
+
 def _on_stream(stream):
     """Memory handed out inside belongs to the stream the call runs on."""
+    if stream is None:
+        return _NULL_CONTEXT
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return torch.cuda.stream(stream)
 
 
 def ring_attn_fwd_window(q, k, v, P, window, n_sink=0, scale=None, order="contiguous", out=None,
@@ -746,13 +755,43 @@ def attn_lse_merge_n(os_, lses, out=None, lse=None, stream=None):
 
 # ------------------------------------------------------------------ 4-bit key/value cache
 
-class KV4Cache(NamedTuple):
+class KV4Cache(tuple):
     """A key/value cache held in 4 bits (format: ``include/ring_attn.h``):
-    codes uint8 [B, H_kv, C, D/2], meta bfloat16 [B, H_kv, C, D/64, 2]."""
-    k_codes: "torch.Tensor"   # noqa: F821
-    k_meta: "torch.Tensor"    # noqa: F821
-    v_codes: "torch.Tensor"   # noqa: F821
-    v_meta: "torch.Tensor"    # noqa: F821
+    codes uint8 [B, H_kv, C, D/2], meta bfloat16 [B, H_kv, C, D/64, 2].
+
+    A tuple of its four tensors, whose shapes, dtypes and layout are checked
+    here, once, and not again by the calls that take the cache.
+    """
+    fields = ("k_codes", "k_meta", "v_codes", "v_meta")
+
+    def __new__(cls, k_codes, k_meta, v_codes, v_meta):
+        import torch
+        self = super().__new__(cls, (k_codes, k_meta, v_codes, v_meta))
+        shape = k_codes.shape
+        if len(shape) != 4:
+            raise ValueError("k_codes must be [B, H_kv, C, D/2]")
+        B, H_kv, C, half = shape
+        meta = (B, H_kv, C, half // 32, 2)
+        _like(k_codes, "k_codes", shape, torch.uint8)
+        _like(v_codes, "v_codes", shape, torch.uint8)
+        _like(k_meta, "k_meta", meta, torch.bfloat16)
+        _like(v_meta, "v_meta", meta, torch.bfloat16)
+        self.dims = (B, H_kv, C, 2 * half)
+        self.device = dev = k_codes.get_device()
+        for t, n in zip(self, cls.fields):
+            if not t.is_contiguous():
+                raise ValueError(f"{n} must be contiguous")
+            if t.get_device() != dev:
+                raise ValueError("the cache's tensors are on several devices")
+        return self
+
+    k_codes = property(lambda self: self[0])
+    k_meta = property(lambda self: self[1])
+    v_codes = property(lambda self: self[2])
+    v_meta = property(lambda self: self[3])
+
+    def pointers(self):
+        return self[0].data_ptr(), self[1].data_ptr(), self[2].data_ptr(), self[3].data_ptr()
 
 
 def kv4_cache(B, H_kv, C, D, device="cuda"):
@@ -767,29 +806,26 @@ def kv4_cache(B, H_kv, C, D, device="cuda"):
     return KV4Cache(*parts)
 
 
-def _kv4_dims(cache):
-    """(B, H_kv, C, D) of a cache whose tensors agree."""
+def _with_cache(cache, named):
+    """The call's other tensors (None: not given) contiguous and on the
+    cache's device, and that device current."""
     import torch
-    codes = cache.k_codes
-    if codes.dim() != 4:
-        raise ValueError("k_codes must be [B, H_kv, C, D/2]")
-    B, H_kv, C, half = codes.shape
-    _like(cache.k_codes, "k_codes", codes.shape, torch.uint8)
-    _like(cache.v_codes, "v_codes", codes.shape, torch.uint8)
-    meta = (B, H_kv, C, half // 32, 2)
-    _like(cache.k_meta, "k_meta", meta, torch.bfloat16)
-    _like(cache.v_meta, "v_meta", meta, torch.bfloat16)
-    return B, H_kv, C, 2 * half
-
-
-def _kv4_named(cache, what=""):
-    return tuple((t, what + n) for t, n in zip(cache, KV4Cache._fields))
+    dev = cache.device
+    if dev < 0:
+        raise ValueError("the cache must be of CUDA tensors")
+    for t, n in named:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            _dev(t, n)
+            raise ValueError(f"{n} and the cache are on different devices")
+    if dev != torch.cuda.current_device():
+        raise ValueError("the call's tensors must be on the current CUDA device")
 
 
 def _ints(t, name, n):
     """A contiguous int32 [n] tensor (None: not given)."""
     import torch
-    _like(t, name, (n,), torch.int32)
+    if t is not None:
+        _like(t, name, (n,), torch.int32)
 
 
 def kv4_append(cache, k, v, start, n_new=None, dev_status=None, stream=None):
@@ -797,19 +833,20 @@ def kv4_append(cache, k, v, start, n_new=None, dev_status=None, stream=None):
     start[b] + 1, ... of ``cache``; with ``n_new`` int32 [B] only the first
     n_new[b] tokens of a padded batch. start: int32 [B] (CUDA)."""
     lib = load()
-    B, H_kv, C, D = _kv4_dims(cache)
+    B, H_kv, C, D = cache.dims
     if k.dim() != 4:
         raise ValueError("k must be [B, T, H_kv, D]")
     T = k.shape[1]
-    _like(k, "k", (B, T, H_kv, D), k.dtype)
-    _like(v, "v", k.shape, k.dtype)
+    shape = (B, T, H_kv, D)
+    _like(k, "k", shape, k.dtype)
+    _like(v, "v", shape, k.dtype)
     _ints(start, "start", B)
     _ints(n_new, "n_new", B)
     _int_buffer(dev_status, "dev_status", 1)
     code = _dtype_code(k.dtype)
-    _on_device(_kv4_named(cache) + ((k, "k"), (v, "v"), (start, "start"), (n_new, "n_new"),
-                                    (dev_status, "dev_status")))
-    st = lib.kv4_append(_ptr(k), _ptr(v), *map(_ptr, cache), _ptr(start), _ptr(n_new), B, T, H_kv,
+    _with_cache(cache, ((k, "k"), (v, "v"), (start, "start"), (n_new, "n_new"),
+                        (dev_status, "dev_status")))
+    st = lib.kv4_append(_ptr(k), _ptr(v), *cache.pointers(), _ptr(start), _ptr(n_new), B, T, H_kv,
                         D, C, code, _ptr(dev_status), _stream(stream))
     _check(st, "kv4_append")
 
@@ -820,24 +857,25 @@ def kv4_read(cache, start, T, dtype=None, k=None, v=None, dev_status=None, strea
     float32."""
     import torch
     lib = load()
-    B, H_kv, C, D = _kv4_dims(cache)
-    dtype = dtype if dtype is not None else (torch.bfloat16 if k is None else k.dtype)
+    B, H_kv, C, D = cache.dims
+    if dtype is None:
+        dtype = torch.bfloat16 if k is None else k.dtype
     code = _dtype_code(dtype)
     T = int(T)
     if T <= 0:
         raise ValueError("T must be positive")
-    _like(k, "k", (B, T, H_kv, D), dtype)
-    _like(v, "v", (B, T, H_kv, D), dtype)
+    shape = (B, T, H_kv, D)
+    _like(k, "k", shape, dtype)
+    _like(v, "v", shape, dtype)
     _ints(start, "start", B)
     _int_buffer(dev_status, "dev_status", 1)
-    _on_device(_kv4_named(cache) + ((k, "k"), (v, "v"), (start, "start"),
-                                    (dev_status, "dev_status")))
+    _with_cache(cache, ((k, "k"), (v, "v"), (start, "start"), (dev_status, "dev_status")))
     with _on_stream(stream):
         if k is None:
-            k = torch.empty(B, T, H_kv, D, dtype=dtype, device=cache.k_codes.device)
+            k = torch.empty(shape, dtype=dtype, device=cache[0].device)
         if v is None:
             v = torch.empty_like(k)
-    st = lib.kv4_read(*map(_ptr, cache), _ptr(start), _ptr(k), _ptr(v), B, T, H_kv, D, C, code,
+    st = lib.kv4_read(*cache.pointers(), _ptr(start), _ptr(k), _ptr(v), B, T, H_kv, D, C, code,
                       _ptr(dev_status), _stream(stream))
     _check(st, "kv4_read")
     return k, v
@@ -846,11 +884,10 @@ def kv4_read(cache, start, T, dtype=None, k=None, v=None, dev_status=None, strea
 def kv4_attn_workspace_bytes(B, S_q, H_q, H_kv, D, C, max_len=None, window=0, n_sink=0,
                              with_score=False):
     """Bytes of device workspace ``kv4_attn`` needs for these sizes."""
-    lib = load()
     n = ctypes.c_size_t()
-    _check(lib.kv4_attn_workspace(B, S_q, H_q, H_kv, D, C, C if max_len is None else int(max_len),
-                                  int(window), int(n_sink), int(bool(with_score)),
-                                  ctypes.byref(n)), "kv4_attn_workspace")
+    _check(load().kv4_attn_workspace(B, S_q, H_q, H_kv, D, C, C if max_len is None else max_len,
+                                     window, n_sink, 1 if with_score else 0, ctypes.byref(n)),
+           "kv4_attn_workspace")
     return n.value
 
 
@@ -868,12 +905,14 @@ def kv4_attn(q, cache, lens, max_len=None, window=0, n_sink=0, scale=None, out=N
     """
     import torch
     lib = load()
-    B, H_kv, C, D = _kv4_dims(cache)
-    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
+    B, H_kv, C, D = cache.dims
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != D:
         raise ValueError("q must be [B, S_q, H_q, D] matching the cache")
-    _, S_q, H_q, _ = q.shape
+    _, S_q, H_q, _ = shape
     max_len = C if max_len is None else int(max_len)
-    _like(out, "out", q.shape, q.dtype)
+    window, n_sink = int(window), int(n_sink)
+    _like(out, "out", shape, q.dtype)
     _like(lse, "lse", (B, H_q, S_q), torch.float32)
     _like(score, "score", (B, H_kv, C), torch.float32)
     _ints(lens, "lens", B)
@@ -881,24 +920,23 @@ def kv4_attn(q, cache, lens, max_len=None, window=0, n_sink=0, scale=None, out=N
     if workspace is not None and workspace.dtype != torch.uint8:
         raise ValueError("workspace must be a uint8 tensor")
     code = _dtype_code(q.dtype)
-    _on_device(_kv4_named(cache) + ((q, "q"), (lens, "lens"), (out, "out"), (lse, "lse"),
-                                    (score, "score"), (workspace, "workspace"),
-                                    (dev_status, "dev_status")))
+    _with_cache(cache, ((q, "q"), (lens, "lens"), (out, "out"), (lse, "lse"), (score, "score"),
+                        (workspace, "workspace"), (dev_status, "dev_status")))
     with _on_stream(stream):
         if out is None:
             out = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty(B, H_q, S_q, dtype=torch.float32, device=q.device)
+            lse = torch.empty((B, H_q, S_q), dtype=torch.float32, device=q.device)
         if workspace is None:
             need = kv4_attn_workspace_bytes(B, S_q, H_q, H_kv, D, C, max_len, window, n_sink,
                                             score is not None)
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    sc = float(scale) if scale is not None else 0.0
-    st = lib.kv4_attn(_ptr(q), *map(_ptr, cache), _ptr(lens), _ptr(out), _ptr(lse), _ptr(score), B,
-                      S_q, H_q, H_kv, D, C, max_len, int(window), int(n_sink), sc, code,
-                      _ptr(workspace), workspace.numel() if workspace is not None else 0,
-                      _ptr(dev_status), _stream(stream))
+    st = lib.kv4_attn(_ptr(q), *cache.pointers(), _ptr(lens), _ptr(out), _ptr(lse), _ptr(score), B,
+                      S_q, H_q, H_kv, D, C, max_len, window, n_sink,
+                      0.0 if scale is None else float(scale), code, _ptr(workspace),
+                      0 if workspace is None else workspace.numel(), _ptr(dev_status),
+                      _stream(stream))
     _check(st, "kv4_attn")
     return out, lse
 
@@ -917,14 +955,13 @@ def kv4_evict(cache, score, lens, budget, n_sink=0, n_recent=0, dst=None, dst_sc
     """
     import torch
     lib = load()
-    B, H_kv, C, D = _kv4_dims(cache)
+    B, H_kv, C, D = cache.dims
     budget, n_sink, n_recent = int(budget), int(n_sink), int(n_recent)
     if budget <= 0:
         raise ValueError("budget must be positive")
-    dev = cache.k_codes.device
     C_dst = -(-budget // 16) * 16
     if dst is not None:
-        dB, dH, C_dst, dD = _kv4_dims(dst)
+        dB, dH, C_dst, dD = dst.dims
         if (dB, dH, dD) != (B, H_kv, D):
             raise ValueError("dst must have the cache's B, H_kv and D")
     _like(score, "score", (B, H_kv, C), torch.float32)
@@ -933,19 +970,21 @@ def kv4_evict(cache, score, lens, budget, n_sink=0, n_recent=0, dst=None, dst_sc
     _ints(lens, "lens", B)
     _ints(dst_lens, "dst_lens", B)
     _int_buffer(dev_status, "dev_status", 1)
-    _on_device(_kv4_named(cache) + (_kv4_named(dst, "dst ") if dst is not None else ()) +
-               ((score, "score"), (lens, "lens"), (dst_score, "dst_score"),
-                (dst_lens, "dst_lens"), (kept, "kept"), (dev_status, "dev_status")))
+    _with_cache(cache, ((score, "score"), (lens, "lens"), (dst_score, "dst_score"),
+                        (dst_lens, "dst_lens"), (kept, "kept"), (dev_status, "dev_status")))
+    if dst is not None and dst.device != cache.device:
+        raise ValueError("dst and the cache are on different devices")
+    dev = cache[0].device
     with _on_stream(stream):
         if dst is None:
             dst = kv4_cache(B, H_kv, C_dst, D, dev)
         if dst_score is None:
-            dst_score = torch.zeros(B, H_kv, C_dst, dtype=torch.float32, device=dev)
+            dst_score = torch.zeros((B, H_kv, C_dst), dtype=torch.float32, device=dev)
         if dst_lens is None:
-            dst_lens = torch.empty(B, dtype=torch.int32, device=dev)
+            dst_lens = torch.empty_like(lens)
         if kept is None:
-            kept = torch.empty(B, H_kv, budget, dtype=torch.int32, device=dev)
-    st = lib.kv4_evict(*map(_ptr, cache), _ptr(score), _ptr(lens), *map(_ptr, dst),
+            kept = torch.empty((B, H_kv, budget), dtype=torch.int32, device=dev)
+    st = lib.kv4_evict(*cache.pointers(), _ptr(score), _ptr(lens), *dst.pointers(),
                        _ptr(dst_score), _ptr(dst_lens), _ptr(kept), B, H_kv, D, C, C_dst, budget,
                        n_sink, n_recent, _ptr(dev_status), _stream(stream))
     _check(st, "kv4_evict")

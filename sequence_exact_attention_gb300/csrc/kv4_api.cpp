@@ -148,15 +148,16 @@ ra_status kv4_attn(const void* q, const void* k_codes, const void* k_meta, const
   a.lse = lse;
   a.score = score;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / __builtin_sqrtf((float)D)) * 1.4426950408889634f;
-  // partial outputs, their (maximum, sum), the logits: in this order, each a
+  // partial outputs, their (maximum, sum), the logits, the rows' log-sums: each a
   // multiple of 16 bytes
   float* ws = static_cast<float*>(workspace);
   const size_t parts = (size_t)B * H_kv * a.n_rb * a.n_split * a.rows;
   a.part_o = ws;
   if (a.n_split > 1) ws += parts * D;
   a.part_ml = ws;
-  if (a.n_split > 1 || score) ws += parts * 2;
+  if (a.n_split > 1) ws += parts * 2;
   a.logits = ws;
+  a.row_lse2 = ws + (size_t)B * H_kv * a.n_rb * a.slots * a.log_rows;
   a.status = dev_status;
   return launch_kv4_attn(a, reinterpret_cast<cudaStream_t>(stream));
 }

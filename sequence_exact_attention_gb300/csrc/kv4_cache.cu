@@ -57,47 +57,35 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[kVals]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// One group of the token rows [B, T, H_kv, D]: its token's sequence and slot.
+// One group of the token rows [B, T, H_kv, D]. Token tensors hold fewer than
+// 2^31 elements, so 32 bits count their groups.
 struct Group {
-  long long elem;      // first element of the group in the token tensor
   long long word;      // the group's word in meta: ((b H_kv + h) C + slot) (D / 64) + group
-  int b, t, slot;
+  bool counts;         // not padding (append)
+  bool in_cache;       // its slot exists
 };
 
-__device__ __forceinline__ Group locate(const Kv4RowArgs& a, long long i) {
-  Group r;
-  const int ng = a.D / kKv4Group;
-  r.elem = i * kKv4Group;
-  const int gr = (int)(i % ng);
-  i /= ng;
-  const int h = (int)(i % a.H_kv);
-  i /= a.H_kv;
-  r.t = (int)(i % a.T);
-  r.b = (int)(i / a.T);
-  // a start so large that slot overflows is out of range in any case
-  const long long slot = (long long)(a.start ? __ldg(a.start + r.b) : 0) + r.t;
-  r.slot = slot >= 0 && slot < a.C ? (int)slot : -1;
-  r.word = (((long long)r.b * a.H_kv + h) * a.C + slot) * ng + gr;
-  return r;
+__device__ __forceinline__ Group locate(const Kv4RowArgs& a, uint32_t i) {
+  const uint32_t two = a.D == 128;                   // groups a row: 1 or 2
+  const uint32_t gr = i & two;
+  uint32_t r = i >> two;
+  const uint32_t h = r % (uint32_t)a.H_kv;
+  r /= (uint32_t)a.H_kv;
+  const uint32_t t = r % (uint32_t)a.T, b = r / (uint32_t)a.T;
+  Group x;
+  const long long slot = (long long)(a.start ? __ldg(a.start + b) : 0) + t;
+  x.counts = !a.n_new || (int)t < __ldg(a.n_new + b);
+  x.in_cache = slot >= 0 && slot < a.C;
+  x.word = ((((long long)b * a.H_kv + h) * a.C + slot) << two) + gr;
+  if (x.in_cache)
+    x.in_cache = in_range(x.word, 1, (long long)a.B * a.H_kv * a.C << two, a.status);
+  return x;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-kv4_append_kernel(const Kv4RowArgs a, long long groups) {
-  const long long i = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const int lane = threadIdx.x % kLanes;
-  // eight lanes leave or stay together: the shuffles below name only them
-  const uint32_t mask = 0xffu << (threadIdx.x & 24);
-  if (i >= groups) return;
-  const Group r = locate(a, i);
-  if (a.n_new && r.t >= __ldg(a.n_new + r.b)) return;    // padding of this sequence
-  if (r.slot < 0) {
-    if (lane == 0 && a.status) atomicExch(a.status, (int)RA_ERR_RANGE);
-    return;
-  }
-  const bool is_v = blockIdx.y != 0;
-  float x[kVals];
-  load8(static_cast<const T*>(is_v ? a.v : a.k) + r.elem + lane * kVals, x);
+// Eight values of a group whose other lanes are the mask's: its codes as one
+// word, its scale and zero point.
+__device__ __forceinline__ uint32_t encode(const float (&x)[kVals], uint32_t mask,
+                                           uint32_t& meta) {
   float lo = x[0], hi = x[0], bad = 0.f;
 #pragma unroll
   for (int e = 0; e < kVals; ++e) {
@@ -116,6 +104,7 @@ kv4_append_kernel(const Kv4RowArgs a, long long groups) {
   const float scale = __bfloat162float(sb);
   const __nv_bfloat16 zb = __float2bfloat16_rn(__fadd_rn(__fadd_rn(lo, __fmul_rn(8.f, scale)), bad));
   const float zero = __bfloat162float(zb);
+  meta = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(zb) << 16);
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < kVals; ++e) {
@@ -123,42 +112,68 @@ kv4_append_kernel(const Kv4RowArgs a, long long groups) {
     const int c = (int)fminf(fmaxf(n, -8.f), 7.f) + 8;
     w |= (uint32_t)c << (4 * e);
   }
-  const long long word = r.word;
-  const long long n_words = (long long)a.B * a.H_kv * a.C * (a.D / kKv4Group);
-  if (!in_range(word, 1, n_words, a.status)) return;
-  reinterpret_cast<uint32_t*>(is_v ? a.c.vc : a.c.kc)[word * kLanes + lane] = w;
-  if (lane == 0)
-    (is_v ? a.c.vm : a.c.km)[word] =
-        (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(zb) << 16);
+  return w;
+}
+
+__device__ __forceinline__ void decode(uint32_t w, uint32_t meta, float (&x)[kVals]) {
+  const float scale = __uint_as_float(meta << 16), zero = __uint_as_float(meta & 0xffff0000u);
+#pragma unroll
+  for (int e = 0; e < kVals; ++e)      // the product is exact in float32
+    x[e] = fmaf(scale, (float)((int)((w >> (4 * e)) & 15u) - 8), zero);
+}
+
+// Both kernels: eight lanes a group, of the keys and of the values.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+kv4_append_kernel(const Kv4RowArgs a, uint32_t groups) {
+  const uint32_t i = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  // eight lanes leave or stay together: the shuffles name only them
+  const uint32_t mask = 0xffu << (threadIdx.x & 24);
+  if (i >= groups) return;
+  const Group r = locate(a, i);
+  if (!r.counts) return;
+  if (!r.in_cache) {
+    if (lane == 0 && a.status) atomicExch(a.status, (int)RA_ERR_RANGE);
+    return;
+  }
+  const size_t elem = (size_t)i * kKv4Group + lane * kVals;
+  float k[kVals], v[kVals];
+  load8(static_cast<const T*>(a.k) + elem, k);
+  load8(static_cast<const T*>(a.v) + elem, v);
+  uint32_t mk, mv;
+  const uint32_t wk = encode(k, mask, mk), wv = encode(v, mask, mv);
+  reinterpret_cast<uint32_t*>(a.c.kc)[r.word * kLanes + lane] = wk;
+  reinterpret_cast<uint32_t*>(a.c.vc)[r.word * kLanes + lane] = wv;
+  if (lane == 0) {
+    a.c.km[r.word] = mk;
+    a.c.vm[r.word] = mv;
+  }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-kv4_read_kernel(const Kv4RowArgs a, long long groups) {
-  const long long i = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+kv4_read_kernel(const Kv4RowArgs a, uint32_t groups) {
+  const uint32_t i = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes;
   if (i >= groups) return;
-  const bool is_v = blockIdx.y != 0;
-  T* dst = static_cast<T*>(is_v ? a.v : a.k);
-  if (!dst) return;
   const Group r = locate(a, i);
-  float x[kVals];
-  const long long n_words = (long long)a.B * a.H_kv * a.C * (a.D / kKv4Group);
-  if (r.slot < 0 || !in_range(r.word, 1, n_words, a.status)) {
+  float k[kVals], v[kVals];
+  if (!r.in_cache) {
     // no such slot: zeros, and the status says so
     if (lane == 0 && a.status) atomicExch(a.status, (int)RA_ERR_RANGE);
 #pragma unroll
-    for (int e = 0; e < kVals; ++e) x[e] = 0.f;
+    for (int e = 0; e < kVals; ++e) k[e] = v[e] = 0.f;
   } else {
-    const uint32_t m = __ldg((is_v ? a.c.vm : a.c.km) + r.word);
-    const uint32_t w =
-        __ldg(reinterpret_cast<const uint32_t*>(is_v ? a.c.vc : a.c.kc) + r.word * kLanes + lane);
-    const float scale = __uint_as_float(m << 16), zero = __uint_as_float(m & 0xffff0000u);
-#pragma unroll
-    for (int e = 0; e < kVals; ++e)      // the product is exact in float32
-      x[e] = fmaf(scale, (float)((int)((w >> (4 * e)) & 15u) - 8), zero);
+    const uint32_t wk = __ldg(reinterpret_cast<const uint32_t*>(a.c.kc) + r.word * kLanes + lane);
+    const uint32_t wv = __ldg(reinterpret_cast<const uint32_t*>(a.c.vc) + r.word * kLanes + lane);
+    const uint32_t mk = __ldg(a.c.km + r.word), mv = __ldg(a.c.vm + r.word);
+    decode(wk, mk, k);
+    decode(wv, mv, v);
   }
-  store8(dst + r.elem + lane * kVals, x);
+  const size_t elem = (size_t)i * kKv4Group + lane * kVals;
+  if (a.k) store8(static_cast<T*>(a.k) + elem, k);
+  if (a.v) store8(static_cast<T*>(a.v) + elem, v);
 }
 
 template <typename Kernel>
@@ -166,8 +181,7 @@ ra_status launch_rows(Kernel kern, const Kv4RowArgs& a, cudaStream_t stream) {
   const long long groups = (long long)a.B * a.T * a.H_kv * (a.D / kKv4Group);
   const int per = kThreads / kLanes;
   const long long blocks = (groups + per - 1) / per;
-  if (blocks > 0x7fffffffLL) return RA_ERR_RANGE;
-  kern<<<dim3((unsigned)blocks, 2), kThreads, 0, stream>>>(a, groups);
+  kern<<<(unsigned)blocks, kThreads, 0, stream>>>(a, (uint32_t)groups);
   return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_LAUNCH;
 }
 

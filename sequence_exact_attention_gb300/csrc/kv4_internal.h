@@ -2,6 +2,7 @@
 // arguments of its kernels and their launchers.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -22,6 +23,21 @@ struct Kv4Cache {
   uint8_t* vc;
   uint32_t* vm;
 };
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device;
+// asked for once a device (`done` has a bit for each, the first 64).
+template <class Kernel>
+bool allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
 
 constexpr int kKv4Group = 64;
 constexpr int kKv4SlotAlign = 16;    // capacities are multiples of it
@@ -56,13 +72,15 @@ struct Kv4AttnArgs {
   // `rows`; each block's visible tiles of kKv4Tile slots are cut into
   // n_split chunks of `chunk` tiles.
   int rows, n_rb, n_split, chunk;
-  int slots;              // max_len rounded up to a tile: the logits' stride
+  int slots;              // max_len rounded up to a tile: the logits' slots
+  int log_rows;           // rows a slot's logits take: those in use, in fours
   float* part_o;          // [B * H_kv * n_rb][n_split][rows][D]
   float* part_ml;         // [B * H_kv * n_rb][n_split][rows][2]
-  float* logits;          // [B * H_kv * n_rb][slots][rows], with score
+  float* logits;          // [B * H_kv * n_rb][slots][log_rows], with score
+  float* row_lse2;        // [B * H_kv * n_rb][rows] log-sums, base 2, with score
   int* status;
 };
-constexpr int kKv4Tile = 32;         // slots a warp works on at a time
+constexpr int kKv4Tile = 128;        // slots a CTA works on at a time
 
 // Fills the plan fields for the sizes in `a`; bytes: the workspace needed
 // (0 when one chunk a block suffices and no score is kept).

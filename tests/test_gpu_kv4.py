@@ -6,11 +6,12 @@ codes, scales, zero points and evicted rows are equal. A read value is one
 float32 operation on exact inputs, rounded to the output type. A logit's error
 E is at most (D + 8) 2^-23 of the sum of its absolute terms (products exact,
 sums float32, the tensor core may drop the last bit of a term) and what small
-query values lose in half precision: 2^-25 of the row's largest, at most
-doubled by the power-of-two scaling, times the sum of the codes' values. A
-weight is then off by 2 E + 2^-21 (two exponentials' errors) of itself, and
-its half-precision product with the value scale by 2^-11 more; the output is
-rounded to bf16 (2^-8).
+query values lose in half precision: with the row's largest brought to 2^14 or
+more and divided by at most 16, 2^-25 2^-10 of it, far less than the 2^-22
+below, times the codes' values. A weight is then off by 2 E + 2^-21 (two
+exponentials' errors) of itself, and its half-precision product with the value
+scale by 2^-11 more, times the code's value less 8, that is |v - zero|; the
+output is rounded to bf16 (2^-8).
 """
 
 import numpy as np
@@ -58,7 +59,7 @@ def bounds(q, k, v, lens, window, n_sink, out, scale):
                 continue
             for h in range(H_q):
                 kk, vv, qq = k[b, h // grp, see], v[b, h // grp, see], q[b, t, h]
-                # |sk (c - 8)| + |zk| is at most 8 steps and the zero point, far below 8
+                # |sk (c - 8)| + |zk| is at most 8 steps of 0.5 and a zero point below 1.5
                 terms = 8.0 * np.abs(qq).sum()
                 e = scale * ((D + 8) * 2.0 ** -23 * terms + 2.0 ** -24 * np.abs(qq).max() * D * 4.0)
                 s = scale * (kk @ qq)
@@ -66,7 +67,7 @@ def bounds(q, k, v, lens, window, n_sink, out, scale):
                 p /= p.sum()
                 t_lse[b, h, t] = e + 2.0 ** -20 * (1 + np.abs(s).max())
                 t_out[b, t, h] = (np.abs(out[b, t, h]) * 2.0 ** -8 +
-                                  (2 * e + 2.0 ** -20 * (1 + np.abs(s).max()) + 2.0 ** -11) * (p @ (np.abs(vv) + 1.0)))
+                                  (2 * e + 2.0 ** -20 * (1 + np.abs(s).max()) + 2.0 ** -11) * (p @ (np.abs(vv) + 1.5)))
     return t_out, t_lse
 
 
@@ -160,7 +161,7 @@ def test_magnitudes(v_scale, q_scale):
     cache, k, v = random_cache(B, H_kv, C, D, seed=11)
     f = float(torch.tensor(v_scale).to(torch.bfloat16))
     new = (cache.v_meta.float() * f).to(torch.bfloat16)
-    cache = cache._replace(v_meta=new)
+    cache = binding.KV4Cache(*cache[:3], new)
     v = kv4.values(kv4.unpack(cache.v_codes.cpu().numpy()), *(new.float().cpu().numpy()[..., i] for i in (0, 1)))
     q = (torch.randn(B, 1, H_q, D, generator=torch.Generator().manual_seed(2)) * q_scale).to(torch.bfloat16)
     scale = 1 / np.sqrt(D) / max(q_scale, 1.0)
@@ -178,7 +179,7 @@ def test_value_scales_that_grow_along_the_cache():
     cache, k, v = random_cache(B, H, C, D, seed=12)
     growth = torch.exp2(torch.linspace(-30, 30, C).floor()).to(DEV)
     new = (cache.v_meta.float() * growth[None, None, :, None, None]).to(torch.bfloat16)
-    cache = cache._replace(v_meta=new)
+    cache = binding.KV4Cache(*cache[:3], new)
     v = kv4.values(kv4.unpack(cache.v_codes.cpu().numpy()), *(new.float().cpu().numpy()[..., i] for i in (0, 1)))
     q = torch.randn(B, 1, 2 * H, D, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
     for n in (512, 300, 40):

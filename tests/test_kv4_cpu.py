@@ -124,7 +124,10 @@ def test_binding_refuses_wrong_tensors():
         (lambda: binding.kv4_append(cache, k, k, lens.long()), "start must be"),
         (lambda: binding.kv4_append(cache, k, k, lens[:1]), "start must have shape"),
         (lambda: binding.kv4_append(cache, k.half(), k.half(), lens), "unsupported dtype"),
-        (lambda: binding.kv4_append(cache._replace(v_meta=cache.v_meta.float()), k, k, lens), "v_meta must be"),
+        (lambda: binding.KV4Cache(*cache[:3], cache.v_meta.float()), "v_meta must be"),
+        (lambda: binding.KV4Cache(cache.k_codes[..., :16], *cache[1:]), "v_codes must have shape"),
+        (lambda: binding.KV4Cache(cache.k_codes[0], *cache[1:]), "k_codes must be"),
+        (lambda: binding.KV4Cache(cache.k_codes.transpose(0, 1), *cache[1:]), "k_codes must be contiguous"),
         (lambda: binding.kv4_read(cache, lens, 0), "T must be"),
         (lambda: binding.kv4_read(cache, lens, 2, k=torch.zeros(2, 3, 2, 64)), "k must have shape"),
         (lambda: binding.kv4_attn(q[:1], cache, lens), "q must be"),
@@ -136,10 +139,10 @@ def test_binding_refuses_wrong_tensors():
         (lambda: binding.kv4_evict(cache, torch.zeros(2, 2, 32), lens, 8,
                                    dst=binding.kv4_cache(2, 1, 16, 64, "cpu")), "dst must have"),
         # right shapes, but host tensors: no CPU path
-        (lambda: binding.kv4_append(cache, k, k, lens), "CUDA tensor"),
-        (lambda: binding.kv4_read(cache, lens, 2), "CUDA tensor"),
-        (lambda: binding.kv4_attn(q, cache, lens), "CUDA tensor"),
-        (lambda: binding.kv4_evict(cache, torch.zeros(2, 2, 32), lens, 8), "CUDA tensor"),
+        (lambda: binding.kv4_append(cache, k, k, lens), "CUDA tensors"),
+        (lambda: binding.kv4_read(cache, lens, 2), "CUDA tensors"),
+        (lambda: binding.kv4_attn(q, cache, lens), "CUDA tensors"),
+        (lambda: binding.kv4_evict(cache, torch.zeros(2, 2, 32), lens, 8), "CUDA tensors"),
     ]
     for call, text in cases:
         with pytest.raises(ValueError, match=text):
