@@ -246,6 +246,90 @@ bwd_prep_kernel(const Geometry gp, const __nv_bfloat16* __restrict__ out,
   }
 }
 
+// The same for narrow windows, where a row sees at most kNarrow keys: delta_i =
+// sum_j p_ij <dO_i, v_j> from the probabilities themselves. The forward's out
+// is rounded to bf16, and a row of few keys cannot average that rounding away:
+// dq and dk came out 2.2 times the rounding of bf16 off at a window of 2 (the
+// products' own roundings leave 1.4), 1.5 times at 16. The sum costs less than
+// one tile product of the same rows. 8 threads a row, as above.
+constexpr int kNarrow = 16;
+template <int D, bool kVarlen>
+__global__ void __launch_bounds__(256)
+bwd_prep_narrow_kernel(const WinGeometry gp, const __nv_bfloat16* __restrict__ dout,
+                       const float* __restrict__ lse, float* __restrict__ lse2,
+                       float* __restrict__ delta, long long rows, int* __restrict__ status) {
+  const long long gid = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);
+  const int sub = threadIdx.x & 7;
+  if (gid >= rows) return;               // rows is a multiple of 32: whole blocks
+  const int row = (int)(gid % kT);
+  long long rest = gid / kT;
+  const int ti = (int)(rest % gp.nt);
+  rest /= gp.nt;
+  const int seg = (int)(rest % gp.n_seg);
+  const int bh = (int)(rest / gp.n_seg);
+  const int b = bh / gp.H_q, h = bh % gp.H_q, hk = h / (gp.H_q / gp.H_kv);
+  WinGeometry gv;
+  int row0 = 0;
+  if constexpr (kVarlen) varlen_window_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
+  const WinGeometry& g = kVarlen ? gv : gp;
+  const size_t srow = seg_rows(gp, b, seg, row0, kVarlen).grow;
+  const size_t lrow = lse_base(gp, b, h, seg, row0, kVarlen);
+  const int in_seg = ti * kT + row;
+  const int pos = seg * g.seg_len + in_seg;
+  constexpr int E = D / 8;
+  const size_t off = ((srow + pos) * g.H_q + h) * D + (size_t)sub * E;
+  const bool valid = in_seg < seg_tokens(g, seg) && in_range((long long)off, E, extent_q(gp), status) &&
+                     in_range((long long)(lrow + pos), 1, extent_lse(gp), status);
+  float q[E], d[E];
+  auto load = [](const __nv_bfloat16* p, float (&x)[E]) {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) {
+      const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[8 * i + 2 * e] = bf_lo(w[e]);
+        x[8 * i + 2 * e + 1] = bf_hi(w[e]);
+      }
+    }
+  };
+  float nl2 = -INFINITY, acc = 0.f;
+  if (valid) {
+    load(gp.q + off, q);
+    load(dout + off, d);
+    nl2 = -(lse[lrow + pos] * kLog2e);
+  }
+  const int lo = max(pos - g.window + 1, 0), first = valid ? min(g.n_sink, lo) : 0;
+  const int n = valid ? first + pos - lo + 1 : 0;
+  // the warp's four rows go together: their shuffles need every lane
+  const int n_all = __reduce_max_sync(0xffffffffu, n);
+  for (int i = 0; i < n_all; ++i) {
+    float s = 0.f, dp = 0.f;
+    const int j = i < first ? i : lo + i - first;
+    const size_t koff = ((srow + j) * g.H_kv + hk) * D + (size_t)sub * E;
+    if (i < n && in_range((long long)koff, E, extent_kv(gp), status)) {
+      float k[E], v[E];
+      load(gp.k + koff, k);
+      load(gp.v + koff, v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        s = fmaf(q[e], k[e], s);
+        dp = fmaf(d[e], v[e], dp);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      dp += __shfl_xor_sync(0xffffffffu, dp, o);
+    }
+    if (i < n) acc = fmaf(ex2_approx(fmaf(s, g.scale_log2, nl2)), dp, acc);
+  }
+  if (sub == 0) {
+    lse2[gid] = nl2;
+    delta[gid] = valid ? -acc : 0.f;
+  }
+}
+
 // ------------------------------------------------------------------ query walk
 using QIter = QIterT<kT>;     // csrc/q_iter.cuh
 
@@ -1064,9 +1148,17 @@ ra_status launch_d(const G& g, const CUtensorMap& mq, const CUtensorMap& mk,
   if (prep_blocks > 0x7fffffffLL || grid_q > 0x7fffffffLL || grid_kv > 0x7fffffffLL)
     return RA_ERR_RANGE;
   if (phases & RA_BWD_PREP) {
-    bwd_prep_kernel<D, kVarlen><<<(unsigned)prep_blocks, 256, 0, stream>>>(
-        g, static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout),
-        lse, lse2, delta, rows, status);
+    bool narrow = false;
+    if constexpr (kWin) {
+      narrow = (long long)g.window + g.n_sink <= kNarrow || g.S <= kNarrow;
+      if (narrow)
+        bwd_prep_narrow_kernel<D, kVarlen><<<(unsigned)prep_blocks, 256, 0, stream>>>(
+            g, static_cast<const __nv_bfloat16*>(dout), lse, lse2, delta, rows, status);
+    }
+    if (!narrow)
+      bwd_prep_kernel<D, kVarlen><<<(unsigned)prep_blocks, 256, 0, stream>>>(
+          g, static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout),
+          lse, lse2, delta, rows, status);
     if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
   }
   if (phases & RA_BWD_DKDV) {
@@ -1190,6 +1282,9 @@ ra_status launch_attn_bwd_window(const WinGeometry& g, const void* q, const void
     return RA_ERR_LAUNCH;
   WinGeometry gl = g;
   gl.sink_part = workspace + bwd_workspace_floats(g);
+  gl.q = static_cast<const __nv_bfloat16*>(q);
+  gl.k = static_cast<const __nv_bfloat16*>(k);
+  gl.v = static_cast<const __nv_bfloat16*>(v);
   auto launch = [&](auto fn) {
     return fn(gl, mq, mk, mv, mdo, out, lse, dout, dq, dk, dv, workspace, RA_BWD_ALL, dev_status,
               stream);

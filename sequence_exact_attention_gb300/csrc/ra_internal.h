@@ -3,6 +3,7 @@
 
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "ring_attn.h"
@@ -55,6 +56,7 @@ struct WinGeometry : Geometry {
   int sink_splits;
   int sink_span;
   float* sink_part;    // [B * H_kv][sink_tiles][sink_splits][dV, dK][tile][D]
+  const __nv_bfloat16 *q, *k, *v;    // the backward's, for narrow windows
 };
 
 // Host-side planning helpers (plan.cpp).

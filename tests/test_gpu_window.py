@@ -76,6 +76,41 @@ def test_matches_oracle(case, dtype):
     assert int(status.item()) == 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,n_sink", [(2, 0), (3, 1), (1, 1), (7, 4), (16, 0), (300, 0)])
+def test_gradients_lose_no_more_than_two_roundings(D, window, n_sink):
+    """dq and dk come from dS in bf16 and are rounded to it: two roundings of
+    one size, sqrt(2) times the error of rounding the exact gradient, and a
+    tenth for everything else. Rows of few keys lose no more (they would, with
+    delta from the rounded output)."""
+    q, k, v, do = draw((1, 1000), 4, 2, D, torch.bfloat16, 77)
+    qd, kd, vd, dd = (t.to(DEV) for t in (q, k, v, do))
+    out, lse = binding.ring_attn_fwd_window(qd, kd, vd, 1, window, n_sink)
+    got = binding.ring_attn_bwd_window(qd, kd, vd, out, lse, dd, 1, window, n_sink)
+    want = oracle.window_backward(q, k, v, do, window, n_sink, 1 / np.sqrt(D))
+    for name, g, w in zip(("dq", "dk", "dv"), got, want):
+        rounded = torch.from_numpy(w).to(torch.bfloat16).double().numpy()
+        err = np.linalg.norm(g.double().cpu().numpy() - w)
+        assert err <= 1.1 * np.sqrt(2) * np.linalg.norm(rounded - w), (name, err / np.linalg.norm(w))
+
+
+def test_packed_sequences_of_few_tokens():
+    """No row sees more than its short sequence: the same holds."""
+    lengths, D = [5, 2, 16, 1, 9, 12] * 20, 64
+    total, longest = sum(lengths), max(lengths)
+    q, k, v, do = draw((total,), 4, 2, D, torch.bfloat16, 78)
+    cu = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    cud = torch.from_numpy(cu).to(DEV)
+    qd, kd, vd, dd = (t.to(DEV) for t in (q, k, v, do))
+    out, lse = binding.ring_attn_fwd_window_varlen(qd, kd, vd, cud, longest, 1, 100, 4)
+    got = binding.ring_attn_bwd_window_varlen(qd, kd, vd, out, lse, dd, cud, longest, 1, 100, 4)
+    want = oracle.window_backward_varlen(q, k, v, do, cu, 100, 4, 1 / np.sqrt(D))
+    for name, g, w in zip(("dq", "dk", "dv"), got, want):
+        rounded = torch.from_numpy(w).to(torch.bfloat16).double().numpy()
+        err = np.linalg.norm(g.double().cpu().numpy() - w)
+        assert err <= 1.1 * np.sqrt(2) * np.linalg.norm(rounded - w), (name, err / np.linalg.norm(w))
+
+
 PACKED = [
     # lengths, H_q, H_kv, D, P, order, window, n_sink
     ("mixed", [300, 0, 1, 777, 128, 1000], 4, 2, 128, 1, "contiguous", 100, 4),
