@@ -52,10 +52,10 @@ MERGE_METRIC = "LSE merge GB/s (algorithmic bytes)"
 # stored with it (see _kernel_digest). window_iter.cuh, which attn_tc.cu
 # includes too, is not among them: only the windowed instantiations use it.
 # The forward's bytes were captured at digest c97b3fa27a2b7d1b; ra_internal.h
-# has since grown a field of the windowed backward's arguments, and the timed
+# has since changed in the windowed kernels' declarations, and the timed
 # kernels' machine code is the same.
 TRAFFIC = {
-    "attn_tc": {"sha256_16": "b8c8e8a39463d259", "bytes_per_launch": {
+    "attn_tc": {"sha256_16": "2d464422b83c8d31", "bytes_per_launch": {
         "bf16_s32k_causal_zigzag": 844294912 + 255832320,
         "bf16_s16k_d64": 402742784 + 119375616,
         "bf16_s128k_gqa_causal": 2729346048 + 1058723840,
@@ -67,7 +67,7 @@ TRAFFIC = {
     # the merge was captured on S = 8192 (1.15 GiB on the device) and scaled by
     # 65536 / 8192 = 8: a streaming kernel whose bytes grow with the rows
     # (ra_internal.h has since changed in other kernels' declarations alone)
-    "merge": {"sha256_16": "be8ecba9a06c2dfa", "bytes_per_launch": {
+    "merge": {"sha256_16": "a38b296695778538", "bytes_per_launch": {
         "merge_p8_s64k": 8 * (1082154240 + 112507904),
     }},
 }

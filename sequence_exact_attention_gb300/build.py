@@ -28,8 +28,8 @@ VARIANTS = {"release": (LIB, OUT, []),
             "debug": (LIB_DEBUG, os.path.join(OUT, "debug"), ["-DRA_DEBUG_CHECKS"])}
 
 SOURCES = ["plan.cpp", "api.cpp", "tensor_map.cpp", "merge.cu", "attn_simt.cu", "attn_tc.cu",
-           "attn_bwd.cu", "bwd_noalloc.cu", "kv4_api.cpp", "kv4_cache.cu", "kv4_attn.cu",
-           "kv4_evict.cu"]
+           "attn_f32_window.cu", "attn_bwd.cu", "bwd_noalloc.cu", "kv4_api.cpp", "kv4_cache.cu",
+           "kv4_attn.cu", "kv4_evict.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC",

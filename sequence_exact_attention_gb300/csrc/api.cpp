@@ -304,7 +304,7 @@ ra_status ring_attn_fwd_window(const void* q, const void* k, const void* v, void
   if (st != RA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == RA_F32)
-    return launch_attn_simt_window(g, static_cast<const float*>(q),
+    return launch_attn_f32_window(g, static_cast<const float*>(q),
                                    static_cast<const float*>(k), static_cast<const float*>(v),
                                    static_cast<float*>(out), lse, dev_status, s);
   return launch_attn_tc_window(g, q, k, v, out, lse, dev_status, s);
@@ -333,7 +333,7 @@ ra_status ring_attn_fwd_window_varlen(const void* q, const void* k, const void* 
   if (st != RA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == RA_F32)
-    return launch_attn_simt_window(g, static_cast<const float*>(q),
+    return launch_attn_f32_window(g, static_cast<const float*>(q),
                                    static_cast<const float*>(k), static_cast<const float*>(v),
                                    static_cast<float*>(out), lse, dev_status, s);
   return launch_attn_tc_window(g, q, k, v, out, lse, dev_status, s);

@@ -19,12 +19,10 @@
 // row group; partial dot products are combined with two xor-shuffles.
 #include <cmath>
 #include <cstdint>
-#include <type_traits>
 
 #include "checks.cuh"
 #include "ra_internal.h"
 #include "ring_iter.cuh"
-#include "window_iter.cuh"
 
 namespace ra {
 namespace {
@@ -39,14 +37,12 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float acc) {
   return fmaf(a.w, b.w, acc);
 }
 
-// G = WinGeometry: with a sliding window and first tokens that stay visible.
-template <int D, bool kVarlen, class G = Geometry>
+template <int D, bool kVarlen>
 __global__ void __launch_bounds__(kThreads)
-attn_simt_kernel(const G gp, const float* __restrict__ q,
+attn_simt_kernel(const Geometry gp, const float* __restrict__ q,
                  const float* __restrict__ k, const float* __restrict__ v,
                  float* __restrict__ out, float* __restrict__ lse,
                  int* __restrict__ vlog, int log_stride, int* __restrict__ status) {
-  constexpr bool kWin = std::is_same<G, WinGeometry>::value;
   constexpr int V4 = D / 4;          // float4 per row
   constexpr int NV = V4 / 4;         // float4 per thread
   extern __shared__ float4 smem[];
@@ -61,13 +57,10 @@ attn_simt_kernel(const G gp, const float* __restrict__ q,
   const int qid = n_qt - 1 - blockIdx.x / BH;    // later positions first
   const int seg = qid / gp.nt, ti = qid % gp.nt;
   const int b = bh / gp.H_q, h = bh % gp.H_q;
-  G gv;
+  Geometry gv;
   int row0 = 0;
-  if constexpr (kVarlen && kWin)
-    varlen_window_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
-  else if constexpr (kVarlen)
-    varlen_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
-  const G& g = kVarlen ? gv : gp;
+  if constexpr (kVarlen) varlen_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
+  const Geometry& g = kVarlen ? gv : gp;
   const int q_lo = seg * g.seg_len + ti * kRows;
   const int q_valid = tile_tokens(g, seg, ti);     // <= 0: a tile of padding only
   const int r = seg_owner(g, seg);
@@ -112,7 +105,7 @@ attn_simt_kernel(const G gp, const float* __restrict__ q,
   int* log_base = vlog ? vlog + log_off : nullptr;
   int n_vis = 0;
 
-  typename std::conditional<kWin, WinKvIter, KvIter>::type it;
+  KvIter it;
   it.init(g, r, q_lo, q_valid);
   KvTile kv;
   while (it.next(g, kv)) {
@@ -151,11 +144,6 @@ attn_simt_kernel(const G gp, const float* __restrict__ q,
 #pragma unroll
       for (int j = 0; j < kRows; ++j)
         if (j >= kv.valid || (g.causal && kv.lo + j > q_pos)) s[j] = -INFINITY;
-      if constexpr (kWin) {
-#pragma unroll
-        for (int j = 0; j < kRows; ++j)
-          if (kv.lo + j >= g.n_sink && kv.lo + j <= q_pos - g.window) s[j] = -INFINITY;
-      }
     }
     float mx = -INFINITY;
 #pragma unroll
@@ -199,18 +187,18 @@ attn_simt_kernel(const G gp, const float* __restrict__ q,
   if (log_base && threadIdx.x == 0 && in_range(log_off, 1, log_len, status)) log_base[0] = n_vis;
 }
 
-template <int D, bool kVarlen = false, class G = Geometry>
-ra_status launch_d(const G& g, const float* q, const float* k,
+template <int D, bool kVarlen = false>
+ra_status launch_d(const Geometry& g, const float* q, const float* k,
                    const float* v, float* out, float* lse, int* vlog,
                    int log_stride, int* status, cudaStream_t stream) {
   const int smem = 2 * kRows * D * (int)sizeof(float);
-  if (cudaFuncSetAttribute(attn_simt_kernel<D, kVarlen, G>,
+  if (cudaFuncSetAttribute(attn_simt_kernel<D, kVarlen>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            smem) != cudaSuccess)
     return RA_ERR_LAUNCH;
   const long long grid = (long long)g.n_seg * g.nt * g.B * g.H_q;
   if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
-  attn_simt_kernel<D, kVarlen, G><<<(unsigned)grid, kThreads, smem, stream>>>(
+  attn_simt_kernel<D, kVarlen><<<(unsigned)grid, kThreads, smem, stream>>>(
       g, q, k, v, out, lse, vlog, log_stride, status);
   return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_LAUNCH;
 }
@@ -222,16 +210,6 @@ ra_status launch_attn_simt_varlen(const Geometry& g, const float* q, const float
                                   cudaStream_t stream) {
   if (g.D == 64) return launch_d<64, true>(g, q, k, v, out, lse, nullptr, 0, dev_status, stream);
   return launch_d<128, true>(g, q, k, v, out, lse, nullptr, 0, dev_status, stream);
-}
-
-ra_status launch_attn_simt_window(const WinGeometry& g, const float* q, const float* k,
-                                  const float* v, float* out, float* lse, int* dev_status,
-                                  cudaStream_t stream) {
-  auto launch = [&](auto fn) { return fn(g, q, k, v, out, lse, nullptr, 0, dev_status, stream); };
-  const bool varlen = g.cu_seqlens != nullptr;
-  if (g.D == 64)
-    return varlen ? launch(launch_d<64, true, WinGeometry>) : launch(launch_d<64, false, WinGeometry>);
-  return varlen ? launch(launch_d<128, true, WinGeometry>) : launch(launch_d<128, false, WinGeometry>);
 }
 
 ra_status launch_attn_simt_sharded(const Geometry& g, const float* q, const float* k,

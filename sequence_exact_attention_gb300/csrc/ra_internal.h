@@ -100,7 +100,7 @@ ra_status launch_attn_tc(const Geometry& g, const void* q, const void* k,
 ra_status launch_attn_tc_window(const WinGeometry& g, const void* q, const void* k,
                                 const void* v, void* out, float* lse, int* dev_status,
                                 cudaStream_t stream);
-ra_status launch_attn_simt_window(const WinGeometry& g, const float* q, const float* k,
+ra_status launch_attn_f32_window(const WinGeometry& g, const float* q, const float* k,
                                   const float* v, float* out, float* lse, int* dev_status,
                                   cudaStream_t stream);
 

