@@ -43,6 +43,14 @@ EXPORTS = ("ring_attn_fwd", "ring_attn_fwd_ex", "ring_attn_visit_log_len",
 
 _lib = None
 _lib_path = LIB_PATH
+_T = None           # torch, imported by the first call that takes tensors
+
+
+def _import_torch():
+    global _T
+    import torch
+    _T = torch
+    return torch
 
 
 class RingAttnError(RuntimeError):
@@ -183,7 +191,7 @@ def visit_log_layout(B, H_q, S, D, P, dtype, order="contiguous"):
 # ------------------------------------------------------------------ tensors
 
 def _dtype_code(dt):
-    import torch
+    torch = _T or _import_torch()
     if dt is torch.bfloat16 or dt == "bf16":
         return RA_BF16
     if dt is torch.float32 or dt == "f32":
@@ -198,9 +206,9 @@ def _ptr(t):
 def _stream(stream):
     """The handle of ``stream``, or of torch's current one (asked for without
     the Stream object that torch.cuda.current_stream() builds: 3 us a call)."""
-    import torch
     if stream is not None:
         return stream.cuda_stream
+    torch = _T or _import_torch()
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
@@ -224,9 +232,9 @@ def _like(t, name, shape, dtype):
 
 def _int_buffer(t, name, n):
     """An int32 buffer of at least n elements (None: not given)."""
-    import torch
     if t is None:
         return
+    torch = _T or _import_torch()
     if t.dtype != torch.int32 or t.numel() < n:
         raise ValueError(f"{name} must be int32 with at least {n} elements")
 
@@ -234,7 +242,7 @@ def _int_buffer(t, name, n):
 def _on_device(named):
     """Every tensor on one CUDA device, contiguous, and that device current
     (the library launches on the current device)."""
-    import torch
+    torch = _T or _import_torch()
     devs = set()
     for t, n in named:
         if t is not None:
@@ -257,7 +265,7 @@ def ring_attn_fwd(q, k, v, P, causal, scale=None, order="contiguous", step=-1,
     the exact CUDA-core kernel. With ``step`` = t >= 0 only ring step t runs
     and (out, lse) are that step's float32 partial result.
     """
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     B, S, H_q, D = q.shape
     H_kv = k.shape[2]
@@ -290,7 +298,7 @@ def ring_attn_fwd(q, k, v, P, causal, scale=None, order="contiguous", step=-1,
 
 def ring_attn_fwd_plain(q, k, v, out, lse, P, causal, scale=None, stream=None):
     """The plain ``ring_attn_fwd`` entry point (bf16, contiguous order)."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     B, S, H_q, D = q.shape
     H_kv = k.shape[2]
@@ -331,7 +339,7 @@ def ring_attn_bwd(q, k, v, out, lse, dout, P, causal, scale=None, order="contigu
     ``phases`` other than BWD_ALL selects kernels (ring_attn_bwd_ex); a split
     call must reuse the workspace the prep phase filled.
     """
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     B, S, H_q, D = q.shape
     H_kv = k.shape[2]
@@ -385,7 +393,7 @@ def ring_attn_bwd_noalloc(q, k, v, out, lse, dout, P, causal, scale=None, order=
     A problem needing more than ``BWD_NOALLOC_MAX_BYTES`` of workspace raises
     ``RingAttnError`` with status ``RA_ERR_SCRATCH``.
     """
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     B, S, H_q, D = q.shape
     H_kv = k.shape[2]
@@ -414,7 +422,7 @@ def ring_attn_bwd_noalloc(q, k, v, out, lse, dout, P, causal, scale=None, order=
 
 
 def _varlen_args(q, k, v, cu_seqlens, max_seqlen):
-    import torch
+    torch = _T or _import_torch()
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens must be a 1-D int32 CUDA tensor")
     total, H_q, D = q.shape
@@ -429,7 +437,7 @@ def ring_attn_fwd_varlen(q, k, v, cu_seqlens, max_seqlen, P, causal, scale=None,
                          stream=None):
     """Ring attention of packed sequences: q [total,H_q,D], k/v [total,H_kv,D],
     cu_seqlens int32 [n+1] (CUDA). Returns (out [total,H_q,D], lse [H_q,total])."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     total, H_q, H_kv, D, n, mx = _varlen_args(q, k, v, cu_seqlens, max_seqlen)
     _like(out, "out", q.shape, q.dtype)
@@ -454,7 +462,7 @@ def ring_attn_bwd_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, P, cau
                          scale=None, order="contiguous", workspace=None, dev_status=None,
                          stream=None):
     """Gradients (dq, dk, dv) of ``ring_attn_fwd_varlen`` for the upstream dout."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     total, H_q, H_kv, D, n, mx = _varlen_args(q, k, v, cu_seqlens, max_seqlen)
     _like(out, "out", q.shape, q.dtype)
@@ -485,7 +493,7 @@ def ring_attn_fwd_ulysses(q, k, v, S, causal, scale=None, out=None, lse=None,
                           dev_status=None, stream=None):
     """Attention of sequence-sharded tensors q [P,B,C,H_q,D], k/v [P,B,C,H_kv,D]
     (C = ceil(S/P)). Returns (out [P,B,C,H_q,D], lse [P,B,H_q,C])."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     P, B, C, H_q, D = q.shape
     H_kv = k.shape[3]
@@ -514,7 +522,7 @@ def ring_attn_bwd_ulysses(q, k, v, out, lse, dout, S, causal, scale=None, worksp
                           dev_status=None, stream=None):
     """Gradients (dq, dk, dv) of ``ring_attn_fwd_ulysses``, all in the
     sequence-parallel layout [P, B, C, H, D]."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     P, B, C, H_q, D = q.shape
     H_kv = k.shape[3]
@@ -551,7 +559,7 @@ def _on_stream(stream):
     """Memory handed out inside belongs to the stream the call runs on."""
     if stream is None:
         return _NULL_CONTEXT
-    import torch
+    torch = _T or _import_torch()
     return torch.cuda.stream(stream)
 
 
@@ -560,7 +568,7 @@ def ring_attn_fwd_window(q, k, v, P, window, n_sink=0, scale=None, order="contig
     """Causal ring attention in which query i sees the ``window`` tokens up to
     itself and the first ``n_sink`` tokens; q [B,S,H_q,D], k/v [B,S,H_kv,D],
     bf16 or float32. Returns (out, lse)."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     B, S, H_q, D = q.shape
     H_kv = k.shape[2]
@@ -591,7 +599,7 @@ def ring_attn_fwd_window_varlen(q, k, v, cu_seqlens, max_seqlen, P, window, n_si
     """``ring_attn_fwd_window`` of packed sequences: q [total,H_q,D], k/v
     [total,H_kv,D], cu_seqlens int32 [n+1] (CUDA); windows and first tokens
     are each sequence's own. Returns (out [total,H_q,D], lse [H_q,total])."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     total, H_q, H_kv, D, n, mx = _varlen_args(q, k, v, cu_seqlens, max_seqlen)
     _like(out, "out", q.shape, q.dtype)
@@ -632,7 +640,7 @@ def ring_attn_bwd_window(q, k, v, out, lse, dout, P, window, n_sink=0, scale=Non
     """Gradients (dq, dk, dv) of ``ring_attn_fwd_window`` (bf16) for the
     upstream dout; ``workspace`` (uint8, ``bwd_window_workspace_bytes``) is
     allocated here when not given."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     B, S, H_q, D = q.shape
     H_kv = k.shape[2]
@@ -670,7 +678,7 @@ def ring_attn_bwd_window_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen,
                                 dv=None, workspace=None, dev_status=None, stream=None):
     """Gradients (dq, dk, dv) of ``ring_attn_fwd_window_varlen`` for the
     upstream dout."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     total, H_q, H_kv, D, n, mx = _varlen_args(q, k, v, cu_seqlens, max_seqlen)
     for t, name in ((out, "out"), (dout, "dout"), (dq, "dq")):
@@ -705,7 +713,7 @@ def ring_attn_bwd_window_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen,
 
 def attn_lse_merge(o_a, lse_a, o_b, lse_b, out=None, lse=None, stream=None):
     """Pairwise merge; o_* [B,S,H,D], lse_* [B,H,S] float32."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     B, S, H, D = o_a.shape
     for t, n in ((o_b, "o_b"), (out, "out")):
@@ -727,7 +735,7 @@ def attn_lse_merge(o_a, lse_a, o_b, lse_b, out=None, lse=None, stream=None):
 
 def attn_lse_merge_n(os_, lses, out=None, lse=None, stream=None):
     """N-way merge of lists of partials (one pass)."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     n = len(os_)
     if n < 1 or len(lses) != n:
@@ -765,7 +773,7 @@ class KV4Cache(tuple):
     fields = ("k_codes", "k_meta", "v_codes", "v_meta")
 
     def __new__(cls, k_codes, k_meta, v_codes, v_meta):
-        import torch
+        torch = _T or _import_torch()
         self = super().__new__(cls, (k_codes, k_meta, v_codes, v_meta))
         shape = k_codes.shape
         if len(shape) != 4:
@@ -796,7 +804,7 @@ class KV4Cache(tuple):
 
 def kv4_cache(B, H_kv, C, D, device="cuda"):
     """A zeroed cache of capacity C (a multiple of 16) slots a sequence."""
-    import torch
+    torch = _T or _import_torch()
     if D not in (64, 128) or C <= 0 or C % 16:
         raise ValueError("D must be 64 or 128 and C a positive multiple of 16")
     parts = []
@@ -806,26 +814,24 @@ def kv4_cache(B, H_kv, C, D, device="cuda"):
     return KV4Cache(*parts)
 
 
-def _with_cache(cache, named):
+def _with_cache(cache, tensors, names):
     """The call's other tensors (None: not given) contiguous and on the
     cache's device, and that device current."""
-    import torch
     dev = cache.device
     if dev < 0:
         raise ValueError("the cache must be of CUDA tensors")
-    for t, n in named:
+    for i, t in enumerate(tensors):
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            _dev(t, n)
-            raise ValueError(f"{n} and the cache are on different devices")
-    if dev != torch.cuda.current_device():
+            _dev(t, names[i])
+            raise ValueError(f"{names[i]} and the cache are on different devices")
+    if dev != _T.cuda.current_device():
         raise ValueError("the call's tensors must be on the current CUDA device")
 
 
 def _ints(t, name, n):
     """A contiguous int32 [n] tensor (None: not given)."""
-    import torch
     if t is not None:
-        _like(t, name, (n,), torch.int32)
+        _like(t, name, (n,), (_T or _import_torch()).int32)
 
 
 def kv4_append(cache, k, v, start, n_new=None, dev_status=None, stream=None):
@@ -844,9 +850,8 @@ def kv4_append(cache, k, v, start, n_new=None, dev_status=None, stream=None):
     _ints(n_new, "n_new", B)
     _int_buffer(dev_status, "dev_status", 1)
     code = _dtype_code(k.dtype)
-    _with_cache(cache, ((k, "k"), (v, "v"), (start, "start"), (n_new, "n_new"),
-                        (dev_status, "dev_status")))
-    st = lib.kv4_append(_ptr(k), _ptr(v), *cache.pointers(), _ptr(start), _ptr(n_new), B, T, H_kv,
+    _with_cache(cache, (k, v, start, n_new, dev_status), ("k", "v", "start", "n_new", "dev_status"))
+    st = lib.kv4_append(k.data_ptr(), v.data_ptr(), *cache.pointers(), start.data_ptr(), _ptr(n_new), B, T, H_kv,
                         D, C, code, _ptr(dev_status), _stream(stream))
     _check(st, "kv4_append")
 
@@ -855,7 +860,7 @@ def kv4_read(cache, start, T, dtype=None, k=None, v=None, dev_status=None, strea
     """The values (k, v) [B, T, H_kv, D] of slots start[b] ... start[b] + T - 1
     (start None: from slot 0), bf16 unless ``dtype`` or given tensors say
     float32."""
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     B, H_kv, C, D = cache.dims
     if dtype is None:
@@ -869,13 +874,13 @@ def kv4_read(cache, start, T, dtype=None, k=None, v=None, dev_status=None, strea
     _like(v, "v", shape, dtype)
     _ints(start, "start", B)
     _int_buffer(dev_status, "dev_status", 1)
-    _with_cache(cache, ((k, "k"), (v, "v"), (start, "start"), (dev_status, "dev_status")))
+    _with_cache(cache, (k, v, start, dev_status), ("k", "v", "start", "dev_status"))
     with _on_stream(stream):
         if k is None:
             k = torch.empty(shape, dtype=dtype, device=cache[0].device)
         if v is None:
             v = torch.empty_like(k)
-    st = lib.kv4_read(*cache.pointers(), _ptr(start), _ptr(k), _ptr(v), B, T, H_kv, D, C, code,
+    st = lib.kv4_read(*cache.pointers(), _ptr(start), k.data_ptr(), v.data_ptr(), B, T, H_kv, D, C, code,
                       _ptr(dev_status), _stream(stream))
     _check(st, "kv4_read")
     return k, v
@@ -903,7 +908,7 @@ def kv4_attn(q, cache, lens, max_len=None, window=0, n_sink=0, scale=None, out=N
     ``workspace`` (uint8, ``kv4_attn_workspace_bytes``) is allocated here when
     not given; calls that may overlap need their own.
     """
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     B, H_kv, C, D = cache.dims
     shape = q.shape
@@ -920,8 +925,8 @@ def kv4_attn(q, cache, lens, max_len=None, window=0, n_sink=0, scale=None, out=N
     if workspace is not None and workspace.dtype != torch.uint8:
         raise ValueError("workspace must be a uint8 tensor")
     code = _dtype_code(q.dtype)
-    _with_cache(cache, ((q, "q"), (lens, "lens"), (out, "out"), (lse, "lse"), (score, "score"),
-                        (workspace, "workspace"), (dev_status, "dev_status")))
+    _with_cache(cache, (q, lens, out, lse, score, workspace, dev_status),
+                ("q", "lens", "out", "lse", "score", "workspace", "dev_status"))
     with _on_stream(stream):
         if out is None:
             out = torch.empty_like(q)
@@ -932,8 +937,8 @@ def kv4_attn(q, cache, lens, max_len=None, window=0, n_sink=0, scale=None, out=N
                                             score is not None)
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    st = lib.kv4_attn(_ptr(q), *cache.pointers(), _ptr(lens), _ptr(out), _ptr(lse), _ptr(score), B,
-                      S_q, H_q, H_kv, D, C, max_len, window, n_sink,
+    st = lib.kv4_attn(q.data_ptr(), *cache.pointers(), lens.data_ptr(), out.data_ptr(),
+                      lse.data_ptr(), _ptr(score), B, S_q, H_q, H_kv, D, C, max_len, window, n_sink,
                       0.0 if scale is None else float(scale), code, _ptr(workspace),
                       0 if workspace is None else workspace.numel(), _ptr(dev_status),
                       _stream(stream))
@@ -953,7 +958,7 @@ def kv4_evict(cache, score, lens, budget, n_sink=0, n_recent=0, dst=None, dst_sc
     [B, H_kv, budget], every kept slot's place in ``cache`` (-1 past the last).
     Slots of ``dst`` past the last are left as they were.
     """
-    import torch
+    torch = _T or _import_torch()
     lib = load()
     B, H_kv, C, D = cache.dims
     budget, n_sink, n_recent = int(budget), int(n_sink), int(n_recent)
@@ -970,8 +975,8 @@ def kv4_evict(cache, score, lens, budget, n_sink=0, n_recent=0, dst=None, dst_sc
     _ints(lens, "lens", B)
     _ints(dst_lens, "dst_lens", B)
     _int_buffer(dev_status, "dev_status", 1)
-    _with_cache(cache, ((score, "score"), (lens, "lens"), (dst_score, "dst_score"),
-                        (dst_lens, "dst_lens"), (kept, "kept"), (dev_status, "dev_status")))
+    _with_cache(cache, (score, lens, dst_score, dst_lens, kept, dev_status),
+                ("score", "lens", "dst_score", "dst_lens", "kept", "dev_status"))
     if dst is not None and dst.device != cache.device:
         raise ValueError("dst and the cache are on different devices")
     dev = cache[0].device
