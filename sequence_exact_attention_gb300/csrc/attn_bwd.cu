@@ -30,6 +30,11 @@
 // their walks would outlast all others, so each is cut into shares of the
 // query positions, one CTA each, whose float32 dV and dK meet in
 // bwd_sink_join_kernel (in a fixed order: no atomics here either).
+// The two gradient kernels do not depend on each other: the windowed dQ grid
+// is launched as a programmatic dependent of the dK/dV grid and fills its last
+// wave's idle multiprocessors. (Windows make both grids many equal, short
+// CTAs, whose last waves are mostly idle.) It waits for that grid at its own
+// end only, so that what follows on the stream finds both done.
 // The two gradient kernels both recompute S and dP; in exchange neither needs
 // atomics, and each gradient is accumulated on chip and written once.
 //
@@ -44,6 +49,7 @@
 #include <type_traits>
 
 #include "checks.cuh"
+#include "early_launch.cuh"
 #include "fastmath.cuh"
 #include "q_iter.cuh"
 #include "ra_internal.h"
@@ -425,6 +431,7 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int kv_valid = tile_tokens(g, kseg, kti);   // <= 0: padding only
   const int h0 = hk * grp;
   if (kv_valid <= 0) return;     // no key, no gradient row: the CTA leaves at once
+  if constexpr (kWin) let_dependents_start();
   auto start = [&](Walk& it) {
     if constexpr (kWin)
       it.init(g, src, kv_lo, kv_valid, h0, h0 + grp, share > 0 ? share * gp.sink_span : 0,
@@ -1128,6 +1135,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
   if (threadIdx.x == 0 && (*abort_flag || *never) && status)
     atomicExch(status, (int)RA_ERR_TIMEOUT);
+  if constexpr (kWin) wait_for_prior_grid();
 }
 
 template <int D, bool kVarlen, class G = Geometry>
@@ -1169,23 +1177,26 @@ ra_status launch_d(const G& g, const CUtensorMap& mq, const CUtensorMap& mk,
         mq, mk, mv, mdo, g, lse2, delta, static_cast<__nv_bfloat16*>(dk),
         static_cast<__nv_bfloat16*>(dv), status);
     if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
-    if constexpr (kWin) {
-      if (g.sink_tiles > 0 && g.sink_splits > 1) {
-        const long long blocks = (long long)g.B * g.H_kv * g.sink_tiles * (kT / kJoinRows);
-        if (blocks > 0x7fffffffLL) return RA_ERR_RANGE;
-        bwd_sink_join_kernel<D, kVarlen><<<(unsigned)blocks, 256, 0, stream>>>(
-            g, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), status);
-        if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
-      }
-    }
   }
   if (phases & RA_BWD_DQ) {
     using CQ = CfgQ<D>;
     if (cudaFuncSetAttribute(bwd_dq_kernel<D, kVarlen, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              CQ::kSmemBytes) != cudaSuccess)
       return RA_ERR_LAUNCH;
-    bwd_dq_kernel<D, kVarlen, G><<<(unsigned)grid_q, kThreads, CQ::kSmemBytes, stream>>>(
-        mq, mk, mv, mdo, g, lse2, delta, static_cast<__nv_bfloat16*>(dq), status);
+    if constexpr (kWin) {
+      if (!launch_early(bwd_dq_kernel<D, kVarlen, G>, grid_q, kThreads, CQ::kSmemBytes, stream, mq,
+                        mk, mv, mdo, g, lse2, delta, static_cast<__nv_bfloat16*>(dq), status))
+        return RA_ERR_LAUNCH;
+      if (g.sink_tiles > 0 && g.sink_splits > 1) {
+        const long long blocks = (long long)g.B * g.H_kv * g.sink_tiles * (kT / kJoinRows);
+        if (blocks > 0x7fffffffLL) return RA_ERR_RANGE;
+        bwd_sink_join_kernel<D, kVarlen><<<(unsigned)blocks, 256, 0, stream>>>(
+            g, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), status);
+      }
+    } else {
+      bwd_dq_kernel<D, kVarlen, G><<<(unsigned)grid_q, kThreads, CQ::kSmemBytes, stream>>>(
+          mq, mk, mv, mdo, g, lse2, delta, static_cast<__nv_bfloat16*>(dq), status);
+    }
     if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
   }
   return RA_OK;

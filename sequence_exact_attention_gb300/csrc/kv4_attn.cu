@@ -40,7 +40,8 @@
 // and metadata are four contiguous pieces, which one lane asks for with bulk
 // copies that land on the stage's barrier, once all warps have read the stage.
 // (A ring for each warp cost 60 of 420 instructions on 16 slots.) Chunks of a
-// long axis are joined by kv4_join_kernel. Everything is summed in a fixed
+// long axis are joined by kv4_join_kernel (launched early: its CTAs are there
+// when the last chunk ends). Everything is summed in a fixed
 // order: results repeat bit for bit.
 //
 // Measured, 8 sequences x 8 key/value heads x 131072 slots, D = 128, 32 query
@@ -61,6 +62,7 @@
 #include <type_traits>
 
 #include "checks.cuh"
+#include "early_launch.cuh"
 #include "fastmath.cuh"
 #include "kv4_internal.h"
 #include "sm100.cuh"
@@ -192,6 +194,7 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
   const int v_begin = split * a.chunk;
   const int v_end = min(sp.n, v_begin + a.chunk);
   if (v_begin >= v_end && a.n_split > 1) return;      // the join knows how many chunks there are
+  let_dependents_start();
 
   // ---- the ring of tiles; lane 0 of warp 0 fills it
   const uint32_t ring = sm100::smem_u32(smem);
@@ -683,6 +686,8 @@ kv4_join_kernel(const Kv4AttnArgs a) {
   const int rb = row / a.rows, r = row % a.rows;
   const Span sp = span_of(a, b, rb);
   const int n = (sp.n + a.chunk - 1) / a.chunk;       // chunks that hold a visible tile
+  let_dependents_start();
+  wait_for_prior_grid();
   const long long base = ((long long)bh * a.n_rb + rb) * a.n_split;
   float y[V], m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -737,6 +742,7 @@ kv4_score_kernel(const Kv4AttnArgs a, int blocks_per_head) {
   const int j0 = (blockIdx.x % blocks_per_head) * (kScoreThreads * kScorePer) + threadIdx.x;
   const int b = bh / a.H_kv;
   const int grp = a.H_q / a.H_kv, R = a.S_q * grp;
+  wait_for_prior_grid();
   float sum[kScorePer] = {};
   bool seen[kScorePer] = {};
   for (int rb = 0; rb < a.n_rb; ++rb) {
@@ -789,15 +795,14 @@ ra_status launch_nt(const Kv4AttnArgs& a, cudaStream_t stream) {
   if (a.n_split > 1) {
     const long long rows = (long long)a.B * a.H_q * a.S_q;
     if (rows > 0x7fffffffLL) return RA_ERR_RANGE;
-    kv4_join_kernel<D><<<(unsigned)rows, 32 * kJoinWarps, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
+    if (!launch_early(kv4_join_kernel<D>, rows, 32 * kJoinWarps, 0, stream, a)) return RA_ERR_LAUNCH;
   }
   if (a.score) {
     const int per = (a.max_len + kScoreThreads * kScorePer - 1) / (kScoreThreads * kScorePer);
     const long long blocks = (long long)a.B * a.H_kv * per;
     if (blocks > 0x7fffffffLL) return RA_ERR_RANGE;
-    kv4_score_kernel<<<(unsigned)blocks, kScoreThreads, 0, stream>>>(a, per);
-    if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
+    if (!launch_early(kv4_score_kernel, blocks, kScoreThreads, 0, stream, a, per))
+      return RA_ERR_LAUNCH;
   }
   return RA_OK;
 }
