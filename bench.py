@@ -51,11 +51,10 @@ MERGE_METRIC = "LSE merge GB/s (algorithmic bytes)"
 # workload; an entry holds only while the kernel's sources have the digest
 # stored with it (see _kernel_digest). window_iter.cuh, which attn_tc.cu
 # includes too, is not among them: only the windowed instantiations use it.
-# The forward's bytes were captured at digest c97b3fa27a2b7d1b; ra_internal.h
-# has since changed in the windowed kernels' declarations, and the timed
-# kernels' machine code is the same.
+# The forward's bytes were captured at digest c97b3fa27a2b7d1b; the sources
+# have since changed in the windowed kernels' parts only.
 TRAFFIC = {
-    "attn_tc": {"sha256_16": "2d464422b83c8d31", "bytes_per_launch": {
+    "attn_tc": {"sha256_16": "96a8ea810a5fcb91", "bytes_per_launch": {
         "bf16_s32k_causal_zigzag": 844294912 + 255832320,
         "bf16_s16k_d64": 402742784 + 119375616,
         "bf16_s128k_gqa_causal": 2729346048 + 1058723840,

@@ -649,6 +649,17 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
               if (i >= end) p[i] = 0.f;
           }
         }
+        if constexpr (kWin && kVarlen)
+          if (qt.valid < kT) {
+            // the rows that follow the sequence: weight 0, which NaN would survive
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= qt.valid - (int)c0) p[i] = 0.f;
+            ok = mbar_wait_warp(bar(C::bFullDO + st), (uint32_t)(j >> 1) & 1, abort_flag,
+                                kTimeoutNs);
+            zero_rows(base + C::kStage0 + st * C::kStageBytes + C::kTileBytes, C::kBoxes, qt.valid,
+                      threadIdx.x);
+          }
         uint32_t pk[32];
 #pragma unroll
         for (int i = 0; i < 64; i += 2) pk[i >> 1] = pack_bf16x2(p[i], p[i + 1]);
@@ -668,6 +679,13 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
         tmem_ld_wait();
         reg_fence(u0);
         reg_fence(u1);
+        if constexpr (kWin && kVarlen)
+          if (qt.valid < kT) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= qt.valid - (int)c0) (i < 32 ? u0[i & 31] : u1[i & 31]) = 0u;
+            zero_rows(base + C::kStage0 + st * C::kStageBytes, C::kBoxes, qt.valid, threadIdx.x);
+          }
         uint32_t pk[32];
 #pragma unroll
         for (int i = 0; i < 64; i += 2) {
@@ -1082,6 +1100,13 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
         tmem_ld_wait();
         reg_fence(u0);
         reg_fence(u1);
+        if constexpr (kWin && kVarlen)
+          if (kv.valid < kT) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= kv.valid - (int)c0) (i < 32 ? u0[i & 31] : u1[i & 31]) = 0u;
+            zero_rows(base + C::kK0 + j % C::kKBuf * C::kTileBytes, C::kBoxes, kv.valid, threadIdx.x);
+          }
         uint32_t pk[32];
 #pragma unroll
         for (int i = 0; i < 64; i += 2) {

@@ -755,6 +755,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
           // is done (S_i(j)'s completion covers it). Both parts take the same
           // decision for a row.
           if (__any_sync(0xffffffffu, resc) && j > 0) scale_cols<D / 2>(tOp, alpha);
+          // what follows the sequence has weight 0 here, which NaN would survive
+          if constexpr (kWin && kVarlen)
+            if (qi == 0 && kv.valid < kTile) {
+              const int vs = j % C::kVBuf;
+              ok = mbar_wait_warp(bar(C::bVFull + vs), (uint32_t)(j / C::kVBuf) & 1, abort_flag,
+                                  kTimeoutNs);
+              zero_rows(base + C::kVOff + vs * C::kTileBytes, C::kBoxes, kv.valid, threadIdx.x);
+            }
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(bar(C::bPFull + qi));
@@ -913,6 +921,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
           // decision for a row.
           if (__any_sync(0xffffffffu, resc) && j > 0)
             scale_cols<D / 2>(tmem + t_lane + kOCol + (uint32_t)(qi * D + part * (D / 2)), alpha);
+          // what follows the sequence has weight 0 here, which NaN would survive
+          if constexpr (kWin && kVarlen)
+            if (qi == 0 && kv.valid < kTile) {
+              const int vs = j % C::kVBuf;
+              ok = mbar_wait_warp(bar(C::bVFull + vs), (uint32_t)(j / C::kVBuf) & 1, abort_flag,
+                                  kTimeoutNs);
+              zero_rows(base + C::kVOff + vs * C::kTileBytes, C::kBoxes, kv.valid, threadIdx.x);
+            }
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(bar(C::bPFull + qi));

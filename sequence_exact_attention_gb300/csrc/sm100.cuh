@@ -130,9 +130,21 @@ __device__ __forceinline__ void bulk_wait_read_all() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 // Orders this thread's generic-proxy shared-memory writes before later
-// async-proxy (TMA) reads of them.
+// async-proxy (TMA, tensor-core) reads of them.
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Rows [valid, 128) of a tile of 64-column bf16 boxes (128 rows of 128 bytes
+// each), as 0, by 256 threads that the next reader of the tile waits for.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int valid, int thread) {
+  for (int bx = 0; bx < boxes; ++bx)
+    for (int i = thread; i < (128 - valid) * 8; i += 256)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                       tile + (uint32_t)(bx * 128 * 128 + valid * 128 + i * 16)),
+                   "r"(0)
+                   : "memory");
+  fence_proxy_async_smem();
 }
 
 // Untiled bulk copy global -> shared, completing on `bar` (transaction

@@ -51,6 +51,11 @@ CASES = [
     ("s900_w300_sink400", 1, 2, 1, 900, 128, 1, "contiguous", 300, 400),
     ("s5_mostly_empty", 1, 2, 1, 5, 64, 4, "contiguous", 2, 1),
     ("s3000_w500_sink16_gqa4", 1, 8, 2, 3000, 64, 1, "contiguous", 500, 16),
+    ("s1100_w40_sink32", 1, 2, 1, 1100, 128, 1, "contiguous", 40, 32),
+    ("s1100_w200_sink33", 1, 2, 1, 1100, 64, 2, "zigzag", 200, 33),
+    ("s1300_w130_sink160", 1, 2, 2, 1300, 64, 1, "contiguous", 130, 160),
+    ("s1301_w256_sink161_p2", 1, 2, 2, 1301, 128, 2, "contiguous", 256, 161),
+    ("s1300_w600_sink20_p5", 1, 2, 2, 1300, 128, 5, "zigzag", 600, 20),
     ("window_past_the_end", 1, 2, 2, 300, 128, 1, "contiguous", 1 << 30, 1 << 30),
 ]
 
@@ -169,6 +174,37 @@ def test_a_window_over_everything_is_the_causal_call(D, dtype):
         for x, y in zip(binding.ring_attn_bwd(q, k, v, a, la, do, 2, True, order="zigzag"),
                         binding.ring_attn_bwd_window(q, k, v, b, lb, do, 2, 700, 0, order="zigzag")):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P,order", [(1, "contiguous"), (2, "zigzag")])
+def test_packed_sequences_do_not_leak(D, dtype, P, order):
+    """NaN and infinities in one sequence, and in the rows behind the last one,
+    stay there: the others' results keep their bits."""
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    lengths, pad, W, K = [300, 130, 77, 5], 140, 60, 6
+    cu = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    cud, rows = torch.from_numpy(cu).to(DEV), int(cu[-1]) + pad
+    clean = [t.to(DEV) for t in draw((rows,), 4, 2, D, tdt, 71)]
+    res = []
+    for junk in (False, True):
+        q, k, v, do = (t.clone() for t in clean)
+        if junk:
+            for t, x, y in ((q, np.nan, -np.inf), (k, np.inf, np.nan), (v, np.nan, np.inf), (do, np.inf, np.nan)):
+                t[cu[1]:cu[2]] = x
+                t[cu[-1]:] = y
+        out, lse = torch.zeros_like(q), torch.zeros(4, rows, device=DEV)
+        binding.ring_attn_fwd_window_varlen(q, k, v, cud, 300, P, W, K, order=order, out=out, lse=lse)
+        got = [out, lse.t()]
+        if dtype == "bf16":
+            grads = [torch.zeros_like(t) for t in (q, k, v)]
+            got += binding.ring_attn_bwd_window_varlen(q, k, v, out, lse, do, cud, 300, P, W, K, order=order,
+                                                       dq=grads[0], dk=grads[1], dv=grads[2])
+        res.append(got)
+    for a, b in zip(*res):
+        for lo, hi in ((cu[0], cu[1]), (cu[2], cu[3]), (cu[3], cu[4]), (cu[4], rows)):
+            assert torch.equal(a[lo:hi], b[lo:hi])
 
 
 @pytest.mark.parametrize("n_sink", [4, 200])
