@@ -78,7 +78,8 @@ typedef enum {
   RA_ERR_DEVICE = 6,   /* current device is not compute capability 10.3            */
   RA_ERR_LAUNCH = 7,   /* CUDA runtime error while preparing or launching          */
   RA_ERR_TIMEOUT = 8,  /* a device-side bounded wait expired (dev_status only)     */
-  RA_ERR_BUFFER = 9,   /* a caller buffer is too small or overlaps an input        */
+  RA_ERR_BUFFER = 9,   /* a caller buffer is too small; 4-bit cache: one that a
+                          call writes overlaps another of its buffers            */
   RA_ERR_RANGE = 10,   /* a size overflows 32-bit indexing, or step out of range;
                           in dev_status (checked build only): a device index out
                           of its tensor's range                                   */
@@ -370,8 +371,13 @@ ra_status ring_attn_bwd_ulysses(const void* q, const void* k, const void* v,
  * meets only the key tiles that some row of it sees, so the work grows with
  * S * window. dtype RA_BF16 or RA_F32; no visit log. Errors as
  * ring_attn_fwd_ex.
+ * Keys and values must be finite where a query does not see them, too: a
+ * hidden key has weight 0, and 0 times an infinity is not a number.
  * ring_attn_fwd_window_varlen - the same for packed sequences (conventions of
- * ring_attn_fwd_varlen): windows and first tokens are each sequence's own.
+ * ring_attn_fwd_varlen): windows and first tokens are each sequence's own. A
+ * sequence's results depend on its own rows only, whatever the others hold;
+ * cu_seqlens[n_seq] may be less than `total`: rows behind the last sequence
+ * are not written and may hold anything (also in the backward).
  */
 ra_status ring_attn_fwd_window(const void* q, const void* k, const void* v,
                                void* out, float* lse, int B, int H_q, int H_kv,
@@ -495,7 +501,9 @@ ra_status ring_attn_expiry_test(const void* q, const void* k, const void* v,
  * 128; the four tensors are 16-byte aligned. How many slots a sequence uses
  * is the caller's `lens` (device int32 [B]); slots past it may hold anything,
  * including NaN. Nothing here reads lens on the host, so a step can be
- * captured into a graph and replayed while lens grows.
+ * captured into a graph and replayed while lens grows. A tensor that a call
+ * writes (its workspace too) may not overlap any other of the call's
+ * (RA_ERR_BUFFER).
  *
  * kv4_append - quantises T tokens a sequence, k and v [B, T, H_kv, D] of
  * `dtype` (RA_BF16 or RA_F32), into slots start[b], start[b] + 1, ...
@@ -566,8 +574,8 @@ ra_status kv4_attn(const void* q, const void* k_codes, const void* k_meta,
  * [B, H_kv, C_dst] likewise (may be NULL), dst_lens [B] = min(n, budget), and
  * kept int32 [B, H_kv, budget], each kept slot's place in the source, -1 past
  * the last. Slots past the last stay as they were. n_sink + n_recent <=
- * budget (else RA_ERR_RANGE). Nothing written may overlap anything read
- * (RA_ERR_BUFFER): evict into a spare cache and swap the two.
+ * budget (else RA_ERR_RANGE). Source and destination are two caches: evict
+ * into a spare one and swap the two.
  */
 ra_status kv4_evict(const void* k_codes, const void* k_meta, const void* v_codes,
                     const void* v_meta, const float* score, const int* lens,

@@ -879,7 +879,7 @@ def kv4_read(cache, start, T, dtype=None, k=None, v=None, dev_status=None, strea
         if k is None:
             k = torch.empty(shape, dtype=dtype, device=cache[0].device)
         if v is None:
-            v = torch.empty_like(k)
+            v = torch.empty(shape, dtype=dtype, device=cache[0].device)
     st = lib.kv4_read(*cache.pointers(), _ptr(start), k.data_ptr(), v.data_ptr(), B, T, H_kv, D, C, code,
                       _ptr(dev_status), _stream(stream))
     _check(st, "kv4_read")
@@ -929,7 +929,7 @@ def kv4_attn(q, cache, lens, max_len=None, window=0, n_sink=0, scale=None, out=N
                 ("q", "lens", "out", "lse", "score", "workspace", "dev_status"))
     with _on_stream(stream):
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
         if lse is None:
             lse = torch.empty((B, H_q, S_q), dtype=torch.float32, device=q.device)
         if workspace is None:

@@ -15,10 +15,39 @@ bool aligned(const void* p, uintptr_t a) {
 
 constexpr long long kMaxElems = 0x7fffffffLL;   // 32-bit sizes of token tensors
 
-// Whether [p, p + n) and [q, q + m) share a byte.
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + m && b < a + n;
+// The bytes of one of a call's tensors (none where it is not given).
+struct Bytes {
+  const void* p;
+  size_t n;
+};
+// Whether two tensors that a call writes, or one that it writes and one that it
+// reads, share a byte.
+template <size_t kOuts, size_t kIns>
+bool overlap(const Bytes (&outs)[kOuts], const Bytes (&ins)[kIns]) {
+  auto meet = [](const Bytes& x, const Bytes& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return x.p && y.p && x.n && y.n && a < b + y.n && b < a + x.n;
+  };
+  for (size_t i = 0; i < kOuts; ++i) {
+    for (const Bytes& x : ins)
+      if (meet(outs[i], x)) return true;
+    for (size_t k = 0; k < i; ++k)
+      if (meet(outs[i], outs[k])) return true;
+  }
+  return false;
+}
+
+// Bytes of one of a call's two token tensors, code tensors, meta tensors.
+size_t token_bytes(const Kv4RowArgs& a, int dtype) {
+  return (size_t)a.B * a.T * a.H_kv * a.D * (dtype == RA_F32 ? 4 : 2);
+}
+template <class Args>
+size_t code_bytes(const Args& a) {
+  return (size_t)a.B * a.H_kv * a.C * (a.D / 2);
+}
+template <class Args>
+size_t meta_bytes(const Args& a) {
+  return (size_t)a.B * a.H_kv * a.C * (a.D / kKv4Group) * 4;
 }
 
 ra_status check_cache(const Kv4Cache& c, int B, int H_kv, int D, int C) {
@@ -52,7 +81,7 @@ ra_status check_rows(const Kv4RowArgs& a, int dtype) {
   if ((long long)a.B * a.T > kMaxElems || (long long)a.B * a.T * a.H_kv > kMaxElems ||
       (long long)a.B * a.T * a.H_kv * a.D > kMaxElems)
     return RA_ERR_RANGE;
-  return check_device(nullptr);
+  return RA_OK;
 }
 
 // Sizes of an attention call, brought to the form the plan wants.
@@ -89,7 +118,14 @@ ra_status kv4_append(const void* k, const void* v, void* k_codes, void* k_meta, 
   a.n_new = n_new;
   a.B = B; a.T = T; a.H_kv = H_kv; a.D = D; a.C = C;
   a.status = dev_status;
-  const ra_status st = check_rows(a, dtype);
+  ra_status st = check_rows(a, dtype);
+  if (st != RA_OK) return st;
+  const Bytes ins[] = {{k, token_bytes(a, dtype)}, {v, token_bytes(a, dtype)},
+                       {start, (size_t)B * 4}, {n_new, (size_t)B * 4}};
+  const Bytes outs[] = {{k_codes, code_bytes(a)}, {k_meta, meta_bytes(a)},
+                        {v_codes, code_bytes(a)}, {v_meta, meta_bytes(a)}};
+  if (overlap(outs, ins)) return RA_ERR_BUFFER;
+  st = check_device(nullptr);
   if (st != RA_OK) return st;
   return launch_kv4_append(a, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -105,7 +141,13 @@ ra_status kv4_read(const void* k_codes, const void* k_meta, const void* v_codes,
   a.start = start;
   a.B = B; a.T = T; a.H_kv = H_kv; a.D = D; a.C = C;
   a.status = dev_status;
-  const ra_status st = check_rows(a, dtype);
+  ra_status st = check_rows(a, dtype);
+  if (st != RA_OK) return st;
+  const Bytes ins[] = {{k_codes, code_bytes(a)}, {k_meta, meta_bytes(a)}, {v_codes, code_bytes(a)},
+                       {v_meta, meta_bytes(a)}, {start, (size_t)B * 4}};
+  const Bytes outs[] = {{k, token_bytes(a, dtype)}, {v, token_bytes(a, dtype)}};
+  if (overlap(outs, ins)) return RA_ERR_BUFFER;
+  st = check_device(nullptr);
   if (st != RA_OK) return st;
   return launch_kv4_read(a, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -140,6 +182,12 @@ ra_status kv4_attn(const void* q, const void* k_codes, const void* k_meta, const
   if (st != RA_OK) return st;
   if (need > 0 && !workspace) return RA_ERR_NULL;
   if (workspace_bytes < need) return RA_ERR_BUFFER;
+  const size_t rows = (size_t)B * S_q * H_q;
+  const Bytes ins[] = {{q, rows * D * 2}, {k_codes, code_bytes(a)}, {k_meta, meta_bytes(a)},
+                       {v_codes, code_bytes(a)}, {v_meta, meta_bytes(a)}, {lens, (size_t)B * 4}};
+  const Bytes outs[] = {{out, rows * D * 2}, {lse, rows * 4},
+                        {score, (size_t)B * H_kv * C * 4}, {workspace, need}};
+  if (overlap(outs, ins)) return RA_ERR_BUFFER;
   st = check_device(nullptr);
   if (st != RA_OK) return st;
   a.q = q;
@@ -181,19 +229,18 @@ ra_status kv4_evict(const void* k_codes, const void* k_meta, const void* v_codes
   if (!aligned(score, 4) || !aligned(lens, 4) || !aligned(dst_score, 4) ||
       !aligned(dst_lens, 4) || !aligned(kept, 4) || !aligned(dev_status, 4))
     return RA_ERR_ALIGN;
+  a.B = B; a.H_kv = H_kv; a.D = D; a.C = C; a.C_dst = C_dst;
+  a.budget = budget; a.n_sink = n_sink; a.n_recent = n_recent;
   // nothing that is written may be part of what is read
-  const size_t src_rows = (size_t)B * H_kv * C, dst_rows = (size_t)B * H_kv * C_dst;
-  const size_t code = (size_t)D / 2, meta = (size_t)D / kKv4Group * 4;
-  const struct { const void* p; size_t n; } in[] = {
-      {k_codes, src_rows * code}, {k_meta, src_rows * meta}, {v_codes, src_rows * code},
-      {v_meta, src_rows * meta}, {score, src_rows * 4}, {lens, (size_t)B * 4}};
-  const struct { const void* p; size_t n; } outs[] = {
-      {dst_k_codes, dst_rows * code}, {dst_k_meta, dst_rows * meta}, {dst_v_codes, dst_rows * code},
-      {dst_v_meta, dst_rows * meta}, {dst_score, dst_score ? dst_rows * 4 : 0},
-      {dst_lens, (size_t)B * 4}, {kept, (size_t)B * H_kv * budget * 4}};
-  for (const auto& o : outs)
-    for (const auto& i : in)
-      if (o.n && overlap(o.p, o.n, i.p, i.n)) return RA_ERR_BUFFER;
+  const size_t dst_rows = (size_t)B * H_kv * C_dst;
+  const size_t code = dst_rows * (D / 2), meta = dst_rows * (D / kKv4Group) * 4;
+  const Bytes ins[] = {{k_codes, code_bytes(a)}, {k_meta, meta_bytes(a)}, {v_codes, code_bytes(a)},
+                       {v_meta, meta_bytes(a)}, {score, (size_t)B * H_kv * C * 4},
+                       {lens, (size_t)B * 4}};
+  const Bytes outs[] = {{dst_k_codes, code}, {dst_k_meta, meta}, {dst_v_codes, code},
+                        {dst_v_meta, meta}, {dst_score, dst_rows * 4},
+                        {dst_lens, (size_t)B * 4}, {kept, (size_t)B * H_kv * budget * 4}};
+  if (overlap(outs, ins)) return RA_ERR_BUFFER;
   st = check_device(nullptr);
   if (st != RA_OK) return st;
   a.score = score;
@@ -201,8 +248,6 @@ ra_status kv4_evict(const void* k_codes, const void* k_meta, const void* v_codes
   a.lens = lens;
   a.dst_lens = dst_lens;
   a.kept = kept;
-  a.B = B; a.H_kv = H_kv; a.D = D; a.C = C; a.C_dst = C_dst;
-  a.budget = budget; a.n_sink = n_sink; a.n_recent = n_recent;
   a.status = dev_status;
   return launch_kv4_evict(a, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -179,7 +179,7 @@ const char* ring_attn_strerror(int status) {
     case RA_ERR_DEVICE: return "no usable CUDA device of compute capability 10.3 (GB300)";
     case RA_ERR_LAUNCH: return "CUDA error while preparing or launching a kernel";
     case RA_ERR_TIMEOUT: return "a device-side bounded wait expired";
-    case RA_ERR_BUFFER: return "caller buffer too small, or it overlaps an input";
+    case RA_ERR_BUFFER: return "caller buffer too small, or it overlaps another of the call's";
     case RA_ERR_RANGE: return "size or index out of range (32-bit indexing; ring step outside [-1, P); window; cache slots)";
     case RA_ERR_SCRATCH:
       return "problem too large for the library's built-in backward scratch "

@@ -77,6 +77,18 @@ def test_attn_refusals(lib):
     assert attn(lib, score=11, ws_bytes=m - 1) == BUFFER
 
 
+def test_buffers_that_overlap_are_refused(lib):
+    for bad in (dict(k=3), dict(v=6), dict(start=4), dict(n_new=5), dict(c=(3, 4, 3, 6))):
+        assert append(lib, **bad) == BUFFER, bad
+    for bad in (dict(k=3), dict(v=6), dict(k=7, v=7)):
+        assert read(lib, **bad) == BUFFER, bad
+    for bad in (dict(out=1), dict(out=5), dict(lse=7), dict(score=4), dict(score=8), dict(ws=1), dict(ws=8),
+                dict(ws=11, score=11)):
+        assert attn(lib, **bad) == BUFFER, bad
+    for bad in (dict(dst=(7, 8, 7, 10)), dict(dscore=13), dict(dlens=13)):
+        assert evict(lib, **bad) == BUFFER, bad
+
+
 def test_attn_workspace(lib):
     assert lib.kv4_attn_workspace(2, 1, 4, 2, 64, 4096, 4096, 0, 0, 0, None) == NULL
     assert need(lib, 1, 1, 8, 2, 64, 256, 201, 0, 0, 0) == (OK, 0)       # one chunk, nothing to join
