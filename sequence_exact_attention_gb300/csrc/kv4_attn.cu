@@ -742,11 +742,19 @@ kv4_score_kernel(const Kv4AttnArgs a, int blocks_per_head) {
   const int j0 = (blockIdx.x % blocks_per_head) * (kScoreThreads * kScorePer) + threadIdx.x;
   const int b = bh / a.H_kv;
   const int grp = a.H_q / a.H_kv, R = a.S_q * grp;
+  // what this call does not write is read while the grid before still runs
+  const Span first = span_of(a, b, 0);
+  float old[kScorePer];
+#pragma unroll
+  for (int e = 0; e < kScorePer; ++e) {
+    const int j = j0 + e * kScoreThreads;
+    old[e] = j < a.max_len ? a.score[(long long)bh * a.C + j] : 0.f;
+  }
   wait_for_prior_grid();
   float sum[kScorePer] = {};
   bool seen[kScorePer] = {};
   for (int rb = 0; rb < a.n_rb; ++rb) {
-    const Span sp = span_of(a, b, rb);
+    const Span sp = rb == 0 ? first : span_of(a, b, rb);
     if (j0 >= sp.hi) continue;
     const long long blk = (long long)bh * a.n_rb + rb;
     const float* lse2 = a.row_lse2 + blk * a.rows;
@@ -778,7 +786,7 @@ kv4_score_kernel(const Kv4AttnArgs a, int blocks_per_head) {
 #pragma unroll
   for (int e = 0; e < kScorePer; ++e) {
     const long long at = (long long)bh * a.C + j0 + e * kScoreThreads;
-    if (seen[e] && in_range(at, 1, (long long)a.B * a.H_kv * a.C, a.status)) a.score[at] += sum[e];
+    if (seen[e] && in_range(at, 1, (long long)a.B * a.H_kv * a.C, a.status)) a.score[at] = old[e] + sum[e];
   }
 }
 
