@@ -43,35 +43,41 @@ __device__ __forceinline__ void load8(const float* p, float (&x)[kVals]) {
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[kVals]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+// Quotients by a fixed d of n < 2^25: mul = ceil(2^(25 + l) / d) with
+// 2^(l - 1) < d <= 2^l is off by less than d / d, so n * mul / 2^(25 + l) is off
+// by less than n 2^l / d / 2^(25 + l) < 1 / d and has the quotient's floor. (Two
+// runtime divisions a thread were a third of the instructions.)
+struct Divisor {
+  uint32_t d, mul;
+  int shift;
+  explicit Divisor(uint32_t d_) : d(d_) {
+    int l = 0;
+    while ((1ull << l) < d) ++l;
+    shift = 25 + l;
+    mul = (uint32_t)(((1ull << shift) + d - 1) / d);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float* p, const float (&x)[kVals]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
+  __device__ __forceinline__ uint32_t of(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * mul) >> shift);
+  }
+};
 
 // One group of the token rows [B, T, H_kv, D]. Token tensors hold fewer than
-// 2^31 elements, so 32 bits count their groups.
+// 2^31 elements, and so fewer than 2^25 groups.
 struct Group {
   long long word;      // the group's word in meta: ((b H_kv + h) C + slot) (D / 64) + group
   bool counts;         // not padding (append)
   bool in_cache;       // its slot exists
 };
 
-__device__ __forceinline__ Group locate(const Kv4RowArgs& a, uint32_t i) {
+struct Divisors {
+  Divisor heads, tokens;
+};
+
+__device__ __forceinline__ Group locate(const Kv4RowArgs& a, const Divisors& by, uint32_t i) {
   const uint32_t two = a.D == 128;                   // groups a row: 1 or 2
-  const uint32_t gr = i & two;
-  uint32_t r = i >> two;
-  const uint32_t h = r % (uint32_t)a.H_kv;
-  r /= (uint32_t)a.H_kv;
-  const uint32_t t = r % (uint32_t)a.T, b = r / (uint32_t)a.T;
+  const uint32_t gr = i & two, row = i >> two;
+  const uint32_t bt = by.heads.of(row), h = row - bt * by.heads.d;
+  const uint32_t b = by.tokens.of(bt), t = bt - b * by.tokens.d;
   Group x;
   const long long slot = (long long)(a.start ? __ldg(a.start + b) : 0) + t;
   x.counts = !a.n_new || (int)t < __ldg(a.n_new + b);
@@ -115,23 +121,44 @@ __device__ __forceinline__ uint32_t encode(const float (&x)[kVals], uint32_t mas
   return w;
 }
 
-__device__ __forceinline__ void decode(uint32_t w, uint32_t meta, float (&x)[kVals]) {
+// The eight values of a word of codes, stored as float32 (one rounding) ...
+__device__ __forceinline__ void store_values(float* p, uint32_t w, uint32_t meta) {
   const float scale = __uint_as_float(meta << 16), zero = __uint_as_float(meta & 0xffff0000u);
+  float x[kVals];
 #pragma unroll
-  for (int e = 0; e < kVals; ++e)      // the product is exact in float32
-    x[e] = fmaf(scale, (float)((int)((w >> (4 * e)) & 15u) - 8), zero);
+  for (int e = 0; e < kVals; ++e)      // 2^23 + c, exact as everything up to the sum
+    x[e] = fmaf(scale, __uint_as_float(((w >> (4 * e)) & 15u) | 0x4b000000u) - 8388616.f, zero);
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+// ... or as bfloat16 (one rounding, two values an operation: 128 + c and c - 8
+// are bfloat16 numbers).
+__device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t w, uint32_t meta) {
+  auto pair = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+  const __nv_bfloat162 scale = pair(__byte_perm(meta, 0, 0x1010));
+  const __nv_bfloat162 zero = pair(__byte_perm(meta, 0, 0x3232));
+  uint32_t r[4];                       // values e and e + 4
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t u = ((w >> (4 * e)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 x = __hfma2(scale, __hsub2(pair(u), pair(0x43084308u)), zero);
+    r[e] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
+                 __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
 }
 
 // Both kernels: eight lanes a group, of the keys and of the values.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-kv4_append_kernel(const Kv4RowArgs a, uint32_t groups) {
+kv4_append_kernel(const Kv4RowArgs a, const Divisors by, uint32_t groups) {
   const uint32_t i = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes;
   // eight lanes leave or stay together: the shuffles name only them
   const uint32_t mask = 0xffu << (threadIdx.x & 24);
   if (i >= groups) return;
-  const Group r = locate(a, i);
+  const Group r = locate(a, by, i);
   if (!r.counts) return;
   if (!r.in_cache) {
     if (lane == 0 && a.status) atomicExch(a.status, (int)RA_ERR_RANGE);
@@ -153,27 +180,23 @@ kv4_append_kernel(const Kv4RowArgs a, uint32_t groups) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-kv4_read_kernel(const Kv4RowArgs a, uint32_t groups) {
+kv4_read_kernel(const Kv4RowArgs a, const Divisors by, uint32_t groups) {
   const uint32_t i = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes;
   if (i >= groups) return;
-  const Group r = locate(a, i);
-  float k[kVals], v[kVals];
-  if (!r.in_cache) {
-    // no such slot: zeros, and the status says so
-    if (lane == 0 && a.status) atomicExch(a.status, (int)RA_ERR_RANGE);
-#pragma unroll
-    for (int e = 0; e < kVals; ++e) k[e] = v[e] = 0.f;
-  } else {
-    const uint32_t wk = __ldg(reinterpret_cast<const uint32_t*>(a.c.kc) + r.word * kLanes + lane);
-    const uint32_t wv = __ldg(reinterpret_cast<const uint32_t*>(a.c.vc) + r.word * kLanes + lane);
-    const uint32_t mk = __ldg(a.c.km + r.word), mv = __ldg(a.c.vm + r.word);
-    decode(wk, mk, k);
-    decode(wv, mv, v);
+  const Group r = locate(a, by, i);
+  uint32_t wk = 0, wv = 0, mk = 0, mv = 0;           // no such slot: zeros
+  if (r.in_cache) {
+    wk = __ldg(reinterpret_cast<const uint32_t*>(a.c.kc) + r.word * kLanes + lane);
+    wv = __ldg(reinterpret_cast<const uint32_t*>(a.c.vc) + r.word * kLanes + lane);
+    mk = __ldg(a.c.km + r.word);
+    mv = __ldg(a.c.vm + r.word);
+  } else if (lane == 0 && a.status) {
+    atomicExch(a.status, (int)RA_ERR_RANGE);
   }
   const size_t elem = (size_t)i * kKv4Group + lane * kVals;
-  if (a.k) store8(static_cast<T*>(a.k) + elem, k);
-  if (a.v) store8(static_cast<T*>(a.v) + elem, v);
+  if (a.k) store_values(static_cast<T*>(a.k) + elem, wk, mk);
+  if (a.v) store_values(static_cast<T*>(a.v) + elem, wv, mv);
 }
 
 template <typename Kernel>
@@ -181,7 +204,8 @@ ra_status launch_rows(Kernel kern, const Kv4RowArgs& a, cudaStream_t stream) {
   const long long groups = (long long)a.B * a.T * a.H_kv * (a.D / kKv4Group);
   const int per = kThreads / kLanes;
   const long long blocks = (groups + per - 1) / per;
-  kern<<<(unsigned)blocks, kThreads, 0, stream>>>(a, (uint32_t)groups);
+  const Divisors by = {Divisor((uint32_t)a.H_kv), Divisor((uint32_t)a.T)};
+  kern<<<(unsigned)blocks, kThreads, 0, stream>>>(a, by, (uint32_t)groups);
   return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_LAUNCH;
 }
 
