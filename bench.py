@@ -51,17 +51,15 @@ MERGE_METRIC = "LSE merge GB/s (algorithmic bytes)"
 # workload; an entry holds only while the kernel's sources have the digest
 # stored with it (see _kernel_digest). window_iter.cuh, which attn_tc.cu
 # includes too, is not among them: only the windowed instantiations use it.
-# The forward's bytes were captured at digest c97b3fa27a2b7d1b; the sources
-# have since changed in the windowed kernels' parts only.
 TRAFFIC = {
     "attn_tc": {"sha256_16": "96a8ea810a5fcb91", "bytes_per_launch": {
-        "bf16_s32k_causal_zigzag": 844294912 + 255832320,
-        "bf16_s16k_d64": 402742784 + 119375616,
-        "bf16_s128k_gqa_causal": 2729346048 + 1058723840,
-        "bf16_s4k_causal": 106966528 + 10845696,
-        "bf16_s32760_uneven_causal_zigzag": 845326592 + 255782912,
-        "bf16_varlen_32k_causal_zigzag": 828246272 + 255547392,
-        "bf16_ulysses_s16k_b2_causal": 805489408 + 252949248,
+        "bf16_s32k_causal_zigzag": 847123712 + 255776000,
+        "bf16_s16k_d64": 402886656 + 119552256,
+        "bf16_s128k_gqa_causal": 2722734080 + 1058463232,
+        "bf16_s4k_causal": 107345152 + 10795776,
+        "bf16_s32760_uneven_causal_zigzag": 844716800 + 255662592,
+        "bf16_varlen_32k_causal_zigzag": 828257280 + 255702272,
+        "bf16_ulysses_s16k_b2_causal": 805459968 + 253208064,
     }},
     # the merge was captured on S = 8192 (1.15 GiB on the device) and scaled by
     # 65536 / 8192 = 8: a streaming kernel whose bytes grow with the rows

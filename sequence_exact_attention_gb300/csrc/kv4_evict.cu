@@ -24,8 +24,10 @@
 // us of 130 at 8 x 8 heads of 32K slots). Up to kAloneSlots slots one CTA does
 // it, without the cluster's barriers. One launch either way.
 //
-// What bounds it: at large sizes the bytes copied (read and written once) and
-// the scores; at small ones the passes' barriers.
+// What bounds it: the passes' barriers and round trips first, then the bytes
+// copied (read and written once). Measured, 8 sequences of 8K to 32K slots x 8
+// heads, D = 128, 4096 kept: 35 us; of the longest's time 2 us load its scores, 15
+// are the four passes, 6 the lists and 9 the copy (92 MB).
 #include <cooperative_groups.h>
 
 #include <cstdint>
