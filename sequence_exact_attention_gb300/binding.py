@@ -12,6 +12,7 @@ missing library raises at the first call.
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -582,7 +583,7 @@ def ring_attn_fwd_window(q, k, v, P, window, n_sink=0, scale=None, order="contig
                 (dev_status, "dev_status")))
     with _on_stream(stream):
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if lse is None and want_lse:
             lse = torch.empty(B, H_q, S, device=q.device, dtype=torch.float32)
     sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
@@ -610,7 +611,7 @@ def ring_attn_fwd_window_varlen(q, k, v, cu_seqlens, max_seqlen, P, window, n_si
                 (lse, "lse"), (dev_status, "dev_status")))
     with _on_stream(stream):
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if lse is None:
             lse = torch.empty(H_q, total, device=q.device, dtype=torch.float32)
     sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
@@ -886,6 +887,8 @@ def kv4_read(cache, start, T, dtype=None, k=None, v=None, dev_status=None, strea
     return k, v
 
 
+# (a function of the sizes alone; asking the library costs as much as a launch)
+@functools.lru_cache(maxsize=256)
 def kv4_attn_workspace_bytes(B, S_q, H_q, H_kv, D, C, max_len=None, window=0, n_sink=0,
                              with_score=False):
     """Bytes of device workspace ``kv4_attn`` needs for these sizes."""
