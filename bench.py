@@ -52,7 +52,7 @@ MERGE_METRIC = "LSE merge GB/s (algorithmic bytes)"
 # stored with it (see _kernel_digest). window_iter.cuh, which attn_tc.cu
 # includes too, is not among them: only the windowed instantiations use it.
 TRAFFIC = {
-    "attn_tc": {"sha256_16": "96a8ea810a5fcb91", "bytes_per_launch": {
+    "attn_tc": {"sha256_16": "9844234043e39819", "bytes_per_launch": {
         "bf16_s32k_causal_zigzag": 847123712 + 255776000,
         "bf16_s16k_d64": 402886656 + 119552256,
         "bf16_s128k_gqa_causal": 2722734080 + 1058463232,

@@ -361,11 +361,13 @@ ra_status ring_attn_bwd_ulysses(const void* q, const void* k, const void* v,
                                 int* dev_status, void* stream);
 
 /*
- * ring_attn_fwd_window - ring attention with a sliding window and a few first
- * tokens that stay visible. The pages have no counterpart; definition, ring
- * and layouts are those of ring_attn_fwd_ex (causal, all steps), with the
- * allowed keys
+ * ring_attn_fwd_window - attention with a sliding window and a few first
+ * tokens that stay visible. The pages have no counterpart; definition and
+ * layouts are those of ring_attn_fwd_ex (causal, all steps), with the allowed
+ * keys
  *     A(i) = { j <= i : j > i - window  or  j < n_sink }
+ * P and order are checked as there and change nothing, not a bit of the result:
+ * a window meets the blocks before its own, wherever the ring keeps them.
  * window >= 1 (1: only the query's own token, and the first ones), n_sink >=
  * 0, else RA_ERR_RANGE; values of S and more mean all tokens. A query tile
  * meets only the key tiles that some row of it sees, so the work grows with

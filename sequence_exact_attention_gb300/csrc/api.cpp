@@ -16,11 +16,14 @@ bool aligned(const void* p, uintptr_t a) {
 
 constexpr long long kMaxElems = 0x7fffffffLL;   // 32-bit element indexing
 
-// Geometry of a windowed call over sequences of at most S tokens.
+// Geometry of a windowed call over sequences of at most S tokens. P and order
+// are checked, and walked as one rank: a window meets few of the ring's blocks.
 ra_status make_window_geometry(int B, int H_q, int H_kv, int S, int D, int P, int window,
                                int n_sink, float scale, int order, int tile, WinGeometry* g) {
   *g = WinGeometry();
-  const ra_status st = make_geometry(B, H_q, H_kv, S, D, P, 1, scale, order, -1, tile, g);
+  ra_status st = make_geometry(B, H_q, H_kv, S, D, P, 1, scale, order, -1, tile, g);
+  if (st != RA_OK) return st;
+  st = make_geometry(B, H_q, H_kv, S, D, 1, 1, scale, RA_ORDER_CONTIGUOUS, -1, tile, g);
   if (st != RA_OK) return st;
   if (window <= 0 || n_sink < 0) return RA_ERR_RANGE;
   g->window = window < S ? window : S;

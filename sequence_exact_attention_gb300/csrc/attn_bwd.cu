@@ -1275,18 +1275,8 @@ long long plan_window_bwd(WinGeometry* g) {
   constexpr int kMinVisits = 16;
   const int grp = g->H_q / g->H_kv;
   const long long n_kt = (long long)g->n_seg * g->nt;
-  // sequences of a packed batch cut their tiles by their own segment length:
-  // at most one ragged tile a segment more than whole tiles
-  const long long most = (g->n_sink + kT - 1) / kT + g->n_seg + 1;
-  long long tiles = g->n_sink == 0 ? 0 : (n_kt < most ? n_kt : most);
-  if (!g->cu_seqlens) {
-    tiles = 0;
-    for (int seg = 0; seg < g->n_seg; ++seg)
-      for (int ti = 0; ti < g->nt; ++ti) {
-        if ((long long)seg * g->seg_len + (long long)ti * kT >= g->n_sink) break;
-        ++tiles;
-      }
-  }
+  long long tiles = ((long long)g->n_sink + kT - 1) / kT;
+  if (tiles > n_kt) tiles = n_kt;
   g->sink_tiles = (int)tiles;
   g->sink_splits = 1;
   g->sink_span = g->S;

@@ -4,7 +4,7 @@
 // accurate exp2f, for a tolerance of 1e-4.
 //
 // A block owns 32 query rows of one (batch, head) and walks the key tiles of
-// 64 that some row sees, in ring order (window_iter.cuh), folding each into
+// 64 that some row sees, in position order (window_iter.cuh), folding each into
 // the rows' running maximum, sum and unnormalised output. Windows make short
 // walks, so rows a block are few (more blocks) and the next tile's keys and
 // values are copied (cp.async, two buffers) while this one is worked on.

@@ -315,8 +315,8 @@ __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint6
 
 // G = WinGeometry: attention with a sliding window and a few first tokens that
 // stay visible. The walk then covers only the key tiles that some row of the
-// block sees, and a score is also masked where its key lies between the first
-// tokens and the row's window.
+// block sees, in position order (window_iter.cuh), and a score is also masked
+// where its key lies between the first tokens and the row's window.
 // Measured (D = 128): S = 32768, 32 heads on 8, window 4096, halves of 8 ranks
 // 1.62 ms, 1270 TFLOP/s of the pairs that see each other; S = 16384, window 2048
 // 474 us, 1090; two sequences of 4096, 16 heads, window 1024 81 us, 745. What the
@@ -555,8 +555,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
       const uint32_t tO0 = tmem + kOCol, tO1 = tmem + kOCol + D;
       // the walk's length, counted while Q lands
       int n;
-      if constexpr (kWin) n = win_walk_length(g, r, q_lo, q_valid);
-      else n = kv_walk_length(g, r, q_lo, q_valid);
+      if constexpr (kWin) {
+        Iter it;
+        it.init(g, r, q_lo, q_valid);
+        n = it.length();
+      } else {
+        n = kv_walk_length(g, r, q_lo, q_valid);
+      }
       bool ok = mbar_wait_warp(bar(C::bQFull), 0, abort_flag, kTimeoutNs) &&
                 (!two || mbar_wait_warp(bar(C::bQFull + 1), 0, abort_flag, kTimeoutNs));
       if (ok && n > 0) {

@@ -45,7 +45,8 @@ struct Geometry {
 };
 
 // Geometry of attention with a sliding window: query i sees key j <= i when
-// j > i - window or j < n_sink (causal is set, 1 <= window <= S, n_sink <= S).
+// j > i - window or j < n_sink (causal is set, 1 <= window <= S, n_sink <= S;
+// always one rank and one segment).
 // In the dK/dV kernel the key tiles that hold a first token are seen from the
 // whole sequence: their work is cut into `sink_splits` shares of `sink_span`
 // query positions (tiles counted by their first position), joined through

@@ -162,18 +162,20 @@ def test_packed_matches_oracle(case, dtype):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_a_window_over_everything_is_the_causal_call(D, dtype):
     q, k, v, do = (t.to(DEV) for t in draw((1, 700), 4, 2, D, dtype, 31))
-    a, la = binding.ring_attn_fwd(q, k, v, 2, True, order="zigzag")
-    b, lb = binding.ring_attn_fwd_window(q, k, v, 2, 700, 0, order="zigzag")
-    if dtype == torch.float32:
-        # two kernels that sum in different orders, each within 1e-4 of the
-        # definition and far nearer here
-        assert_close(b, a.cpu().numpy(), "f32", "out")
-        assert_close(lb, la.cpu().numpy(), "f32", "lse")
-    else:
-        assert torch.equal(a, b) and torch.equal(la, lb)
-        for x, y in zip(binding.ring_attn_bwd(q, k, v, a, la, do, 2, True, order="zigzag"),
-                        binding.ring_attn_bwd_window(q, k, v, b, lb, do, 2, 700, 0, order="zigzag")):
-            assert torch.equal(x, y)
+    a, la = binding.ring_attn_fwd(q, k, v, 1, True)
+    for P, order in ((1, "contiguous"), (2, "zigzag"), (8, "contiguous")):
+        b, lb = binding.ring_attn_fwd_window(q, k, v, P, 700, 0, order=order)
+        if dtype == torch.float32:
+            # two kernels that sum in different orders, each within 1e-4 of the
+            # definition and far nearer here
+            assert_close(b, a.cpu().numpy(), "f32", "out")
+            assert_close(lb, la.cpu().numpy(), "f32", "lse")
+        else:
+            # the same sums in the same order, whatever the ranks
+            assert torch.equal(a, b) and torch.equal(la, lb)
+            for x, y in zip(binding.ring_attn_bwd(q, k, v, a, la, do, 1, True),
+                            binding.ring_attn_bwd_window(q, k, v, b, lb, do, P, 700, 0, order=order)):
+                assert torch.equal(x, y)
 
 
 @pytest.mark.parametrize("D", [64, 128])
