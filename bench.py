@@ -52,19 +52,19 @@ MERGE_METRIC = "LSE merge GB/s (algorithmic bytes)"
 # stored with it (see _kernel_digest). window_iter.cuh, which attn_tc.cu
 # includes too, is not among them: only the windowed instantiations use it.
 TRAFFIC = {
-    "attn_tc": {"sha256_16": "9844234043e39819", "bytes_per_launch": {
-        "bf16_s32k_causal_zigzag": 847123712 + 255776000,
-        "bf16_s16k_d64": 402886656 + 119552256,
-        "bf16_s128k_gqa_causal": 2722734080 + 1058463232,
-        "bf16_s4k_causal": 107345152 + 10795776,
-        "bf16_s32760_uneven_causal_zigzag": 844716800 + 255662592,
-        "bf16_varlen_32k_causal_zigzag": 828257280 + 255702272,
-        "bf16_ulysses_s16k_b2_causal": 805459968 + 253208064,
+    "attn_tc": {"sha256_16": "4538146edcdab8e1", "bytes_per_launch": {
+        "bf16_s32k_causal_zigzag": 846726912 + 255683328,
+        "bf16_s16k_d64": 402788352 + 119632384,
+        "bf16_s128k_gqa_causal": 2718674944 + 1058094080,
+        "bf16_s4k_causal": 105614080 + 10554880,
+        "bf16_s32760_uneven_causal_zigzag": 847103232 + 255800320,
+        "bf16_varlen_32k_causal_zigzag": 828689920 + 255648000,
+        "bf16_ulysses_s16k_b2_causal": 805524224 + 253269248,
     }},
     # the merge was captured on S = 8192 (1.15 GiB on the device) and scaled by
     # 65536 / 8192 = 8: a streaming kernel whose bytes grow with the rows
     # (ra_internal.h has since changed in other kernels' declarations alone)
-    "merge": {"sha256_16": "a38b296695778538", "bytes_per_launch": {
+    "merge": {"sha256_16": "e0abdc4ed4d330ba", "bytes_per_launch": {
         "merge_p8_s64k": 8 * (1082154240 + 112507904),
     }},
 }

@@ -28,7 +28,7 @@ ra_status make_window_geometry(int B, int H_q, int H_kv, int S, int D, int P, in
   if (window <= 0 || n_sink < 0) return RA_ERR_RANGE;
   g->window = window < S ? window : S;
   g->n_sink = n_sink < S ? n_sink : S;
-  g->sink_splits = 1;
+  g->sink_splits = g->head_splits = 1;
   return RA_OK;
 }
 

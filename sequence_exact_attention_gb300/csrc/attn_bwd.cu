@@ -29,7 +29,10 @@
 // The key tiles that hold a first token are seen from the whole sequence:
 // their walks would outlast all others, so each is cut into shares of the
 // query positions, one CTA each, whose float32 dV and dK meet in
-// bwd_sink_join_kernel (in a fixed order: no atomics here either).
+// bwd_share_join_kernel (in a fixed order: no atomics here either). With few
+// key/value heads and short sequences the other key tiles leave most of the card
+// idle while each walks all heads of its group; then the heads are shared out the
+// same way.
 // The two gradient kernels do not depend on each other: the windowed dQ grid
 // is launched as a programmatic dependent of the dK/dV grid and fills its last
 // wave's idle multiprocessors. (Windows make both grids many equal, short
@@ -368,6 +371,19 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (
 // Warp w covers key rows 32 (w mod 4) .. +31 and query columns 64 (w / 4)
 // .. +63; its bf16 P^T and dS^T go into the first 32 columns of its own
 // S^T and dP^T column ranges, so no warp writes columns another one reads.
+// Places of the shares of a windowed call's key tiles in its parts: of tile
+// `ordinal` with first tokens, of tile kt, and how many there are.
+__device__ __forceinline__ long long sink_shares(const WinGeometry& g, int bhk, int ordinal) {
+  return ((long long)bhk * g.sink_tiles + ordinal) * g.sink_splits;
+}
+__device__ __forceinline__ long long head_shares(const WinGeometry& g, int bhk, int kt) {
+  return (g.sink_splits > 1 ? sink_shares(g, g.B * g.H_kv, 0) : 0) +
+         ((long long)bhk * g.nt + kt) * g.head_splits;
+}
+__device__ __forceinline__ long long all_shares(const WinGeometry& g) {
+  return head_shares(g, g.head_splits > 1 ? g.B * g.H_kv : 0, 0);
+}
+
 template <int D, bool kVarlen, class G = Geometry>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -398,7 +414,7 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
   int kt = (int)(blockIdx.x % n_kt);
   int bhk = (int)(blockIdx.x / n_kt);
   // the shares of the key tiles with first tokens come first: the longest walks
-  int share = -1, ordinal = 0;
+  int share = -1, ordinal = 0, head_share = 0;
   if constexpr (kWin) {
     const int n_share = gp.B * gp.H_kv * gp.sink_tiles * gp.sink_splits;
     int block = (int)blockIdx.x;
@@ -408,8 +424,10 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
       ordinal = block % gp.sink_tiles;
       bhk = block / gp.sink_tiles;
     } else {
-      kt = (block - n_share) % n_kt;
-      bhk = (block - n_share) / n_kt;
+      block -= n_share;
+      head_share = block % gp.head_splits;
+      kt = block / gp.head_splits % n_kt;
+      bhk = block / gp.head_splits / n_kt;
     }
   }
   const int b = bhk / gp.H_kv, hk = bhk % gp.H_kv;
@@ -437,10 +455,12 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
   if (kv_valid <= 0) return;     // no key, no gradient row: the CTA leaves at once
   if constexpr (kWin) let_dependents_start();
   auto start = [&](Walk& it) {
-    if constexpr (kWin)
-      it.init(g, src, kv_lo, kv_valid, h0, h0 + grp, share > 0 ? share * gp.sink_span : 0,
+    if constexpr (kWin) {
+      const int n = share >= 0 ? 1 : gp.head_splits;
+      it.init(g, src, kv_lo, kv_valid, h0 + grp * head_share / n,
+              h0 + grp * (head_share + 1) / n, share > 0 ? share * gp.sink_span : 0,
               share >= 0 && share + 1 < gp.sink_splits ? (share + 1) * gp.sink_span : g.S);
-    else
+    } else
       it.init(g, src, kv_lo, kv_valid, h0, h0 + grp);
   };
 
@@ -729,14 +749,13 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
             for (int i = 0; i < 32; ++i) u[i] = 0u;
           }
           if constexpr (kWin) {
-            if (share >= 0 && gp.sink_splits > 1) {
-              // a share's float32 part: [bhk][ordinal][share][dV, dK][row][D]
-              const long long part =
-                  ((((long long)bhk * gp.sink_tiles + ordinal) * gp.sink_splits + share) * 2 +
-                   which) * kT + row;
-              if (in_range(part, 1, (long long)gp.B * gp.H_kv * gp.sink_tiles * gp.sink_splits *
-                                        2 * kT, status)) {
-                float4* dst4 = reinterpret_cast<float4*>(gp.sink_part + part * D + col);
+            if ((share >= 0 ? gp.sink_splits : gp.head_splits) > 1) {
+              const long long block =
+                  share >= 0 ? sink_shares(gp, bhk, ordinal) + share
+                             : head_shares(gp, bhk, kt) + head_share;
+              const long long part = (block * 2 + which) * kT + row;
+              if (in_range(part, 1, all_shares(gp) * 2 * kT, status)) {
+                float4* dst4 = reinterpret_cast<float4*>(gp.part + part * D + col);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                   dst4[i] = make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
@@ -760,34 +779,41 @@ bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
     atomicExch(status, (int)RA_ERR_TIMEOUT);
 }
 
-// Joins the shares of the key tiles with first tokens: one block a (batch, kv
-// head, tile, 16 rows); shares are added in order.
+// Joins the shares of key tiles: one block a (batch, kv head, tile, 16 rows);
+// shares are added in order. Items are the tiles with first tokens, then all
+// tiles, of which those with first tokens drop out.
 constexpr int kJoinRows = 16;
+__host__ __device__ __forceinline__ int join_items(const WinGeometry& g) {
+  return (g.sink_splits > 1 ? g.sink_tiles : 0) + (g.head_splits > 1 ? g.nt : 0);
+}
 template <int D, bool kVarlen>
 __global__ void __launch_bounds__(256)
-bwd_sink_join_kernel(const WinGeometry gp, __nv_bfloat16* __restrict__ dk,
-                     __nv_bfloat16* __restrict__ dv, int* __restrict__ status) {
+bwd_share_join_kernel(const WinGeometry gp, __nv_bfloat16* __restrict__ dk,
+                      __nv_bfloat16* __restrict__ dv, int* __restrict__ status) {
   int block = (int)blockIdx.x;
   const int r0 = block % (kT / kJoinRows) * kJoinRows;
   block /= kT / kJoinRows;
-  const int ordinal = block % gp.sink_tiles;
-  const int bhk = block / gp.sink_tiles, b = bhk / gp.H_kv, hk = bhk % gp.H_kv;
+  const int items = join_items(gp), n_sink_items = gp.sink_splits > 1 ? gp.sink_tiles : 0;
+  const int item = block % items, bhk = block / items, b = bhk / gp.H_kv, hk = bhk % gp.H_kv;
   WinGeometry gv;
   int row0 = 0;
   if constexpr (kVarlen) varlen_window_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
   const WinGeometry& g = kVarlen ? gv : gp;
-  int seg, ti;
-  if (!sink_tile(g, ordinal, seg, ti)) return;
-  const int valid = tile_tokens(g, seg, ti);
-  const size_t grow = seg_rows(gp, b, seg, row0, kVarlen).grow + (size_t)seg * g.seg_len + ti * kT;
-  const float4* part = reinterpret_cast<const float4*>(gp.sink_part) +
-                       ((long long)bhk * gp.sink_tiles + ordinal) * gp.sink_splits * 2 * kT * (D / 4);
+  const bool first = item < n_sink_items;
+  const int ti = first ? item : item - n_sink_items;
+  if ((ti * kT < g.n_sink) != first) return;         // not shared, or by the other rule
+  const int valid = tile_tokens(g, 0, ti);
+  if (valid <= 0) return;
+  const size_t grow = seg_rows(gp, b, 0, row0, kVarlen).grow + (size_t)ti * kT;
+  const int splits = first ? gp.sink_splits : gp.head_splits;
+  const float4* part = reinterpret_cast<const float4*>(gp.part) +
+                       (first ? sink_shares(gp, bhk, ti) : head_shares(gp, bhk, ti)) * 2 * kT * (D / 4);
   for (int i = threadIdx.x; i < 2 * kJoinRows * (D / 4); i += 256) {
     const int which = i / (kJoinRows * (D / 4));
     const int row = r0 + i / (D / 4) % kJoinRows, c = i % (D / 4);
     if (row >= valid) continue;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < gp.sink_splits; ++s) {
+    for (int s = 0; s < splits; ++s) {
       const float4 x = part[((long long)(s * 2 + which) * kT + row) * (D / 4) + c];
       y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
     }
@@ -1180,7 +1206,8 @@ ra_status launch_d(const G& g, const CUtensorMap& mq, const CUtensorMap& mk,
   const long long n_tiles = (long long)g.n_seg * g.nt;
   constexpr bool kWin = std::is_same<G, WinGeometry>::value;
   long long grid_kv = n_tiles * g.B * g.H_kv;
-  if constexpr (kWin) grid_kv += (long long)g.B * g.H_kv * g.sink_tiles * g.sink_splits;
+  if constexpr (kWin)
+    grid_kv = grid_kv * g.head_splits + (long long)g.B * g.H_kv * g.sink_tiles * g.sink_splits;
   const long long grid_q = n_tiles * g.B * g.H_q;
   if (prep_blocks > 0x7fffffffLL || grid_q > 0x7fffffffLL || grid_kv > 0x7fffffffLL)
     return RA_ERR_RANGE;
@@ -1216,10 +1243,10 @@ ra_status launch_d(const G& g, const CUtensorMap& mq, const CUtensorMap& mk,
       if (!launch_early(bwd_dq_kernel<D, kVarlen, G>, grid_q, kThreads, CQ::kSmemBytes, stream, mq,
                         mk, mv, mdo, g, lse2, delta, static_cast<__nv_bfloat16*>(dq), status))
         return RA_ERR_LAUNCH;
-      if (g.sink_tiles > 0 && g.sink_splits > 1) {
-        const long long blocks = (long long)g.B * g.H_kv * g.sink_tiles * (kT / kJoinRows);
+      if (join_items(g) > 0) {
+        const long long blocks = (long long)g.B * g.H_kv * join_items(g) * (kT / kJoinRows);
         if (blocks > 0x7fffffffLL) return RA_ERR_RANGE;
-        bwd_sink_join_kernel<D, kVarlen><<<(unsigned)blocks, 256, 0, stream>>>(
+        bwd_share_join_kernel<D, kVarlen><<<(unsigned)blocks, 256, 0, stream>>>(
             g, static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), status);
       }
     } else {
@@ -1266,36 +1293,64 @@ ra_status launch_attn_bwd(const Geometry& g, const void* q, const void* k, const
                               phases, dev_status, stream);
 }
 
-// The tiles with first tokens, and how many shares each is cut into: a share
-// spans as many query positions as an ordinary key tile is seen from, and at
-// least kMinVisits tiles of queries; no more shares than keep the
-// multiprocessors busy four times over (a share costs 2 * 128 * D floats).
+// How the work on key tiles is shared out.
+//
+// Heads: with a visit of the dK/dV kernel as the unit, a CTA costs its visits and
+// some 5 of set-up and end, a part and its join some 4, and a dQ CTA 0.7 a visit
+// and 4. The two grids run side by side, so the call takes the longer of its
+// longest CTA and of all work spread over the card; the shares that make that
+// least. (8 heads on 1, D = 128, 3115 tokens, window 433, forward and backward: 120
+// us without, 81 with.)
+//
+// Tiles with first tokens: a share spans as many query positions as make it as
+// long as the other CTAs, and at least 16 visits, or 8 where the others leave
+// multiprocessors idle (8 heads on 1, 477 tokens, window 4: 58 us with 16, 44 with
+// 8; 32 heads on 8, 3720 tokens, 200 first tokens: 202 and 216); no more shares
+// than keep the multiprocessors busy four times over (a share costs 2 * 128 * D
+// floats).
 long long plan_window_bwd(WinGeometry* g) {
-  constexpr long long kMaxCtas = 4 * 152;
-  constexpr int kMinVisits = 16;
+  constexpr long long kSms = 152, kMaxCtas = 4 * kSms, kMaxParts = 8 * kSms;
   const int grp = g->H_q / g->H_kv;
-  const long long n_kt = (long long)g->n_seg * g->nt;
+  const long long n_kt = g->nt, ctas = g->B * (long long)g->H_kv * n_kt;
+  // query tiles of one head that see a key tile
+  const long long seen = ((long long)g->window + kT - 1 + kT - 1) / kT;
+  const long long v = seen < n_kt ? seen : n_kt;
+  long long best = 0;
+  g->head_splits = 1;
+  for (int n = 1; n <= grp && (n == 1 || ctas * n <= kMaxParts); ++n) {
+    const long long chain = (grp + n - 1) / n * v + 5 + (n > 1 ? 4 : 0);
+    const long long all = (ctas * (grp * v + 5 * n) + ctas * grp * (v * 7 / 10 + 4)) / kSms;
+    const long long cost = chain > all ? chain : all;
+    if (n == 1 || cost < best) {
+      best = cost;
+      g->head_splits = n;
+    }
+  }
+  long long parts = g->head_splits > 1 ? ctas * g->head_splits : 0;
   long long tiles = ((long long)g->n_sink + kT - 1) / kT;
   if (tiles > n_kt) tiles = n_kt;
   g->sink_tiles = (int)tiles;
   g->sink_splits = 1;
   g->sink_span = g->S;
-  g->sink_part = nullptr;
-  if (tiles == 0) return 0;
-  long long span = ((long long)g->window + kT - 1 + kT - 1) / kT * kT;
-  const long long least = (long long)((kMinVisits + grp - 1) / grp) * kT;
-  if (span < least) span = least;
-  long long splits = (g->S + span - 1) / span;
-  const long long one = tiles * g->B * g->H_kv;
-  const long long cap = (kMaxCtas + one - 1) / one;
-  if (splits > cap) {
-    splits = cap;
-    span = ((g->S + splits - 1) / splits + kT - 1) / kT * kT;
-    splits = (g->S + span - 1) / span;
+  g->part = nullptr;
+  if (tiles > 0) {
+    long long visits = (grp + g->head_splits - 1) / g->head_splits * seen;
+    const long long least = ctas * g->head_splits < kSms ? 8 : 16;
+    if (visits < least) visits = least;
+    long long span = (visits + grp - 1) / grp * kT;
+    long long splits = (g->S + span - 1) / span;
+    const long long one = tiles * g->B * g->H_kv;
+    const long long cap = (kMaxCtas + one - 1) / one;
+    if (splits > cap) {
+      splits = cap;
+      span = ((g->S + splits - 1) / splits + kT - 1) / kT * kT;
+      splits = (g->S + span - 1) / span;
+    }
+    g->sink_splits = (int)splits;
+    g->sink_span = (int)span;
+    if (splits > 1) parts += one * splits;
   }
-  g->sink_splits = (int)splits;
-  g->sink_span = (int)span;
-  return splits > 1 ? one * splits * 2 * kT * g->D : 0;
+  return parts * 2 * kT * g->D;
 }
 
 ra_status launch_attn_bwd_window(const WinGeometry& g, const void* q, const void* k,
@@ -1311,7 +1366,7 @@ ra_status launch_attn_bwd_window(const WinGeometry& g, const void* q, const void
       !make_bshd_map(&mdo, dout, mb, ms, g.H_q, g.D, kT))
     return RA_ERR_LAUNCH;
   WinGeometry gl = g;
-  gl.sink_part = workspace + bwd_workspace_floats(g);
+  gl.part = workspace + bwd_workspace_floats(g);
   gl.q = static_cast<const __nv_bfloat16*>(q);
   gl.k = static_cast<const __nv_bfloat16*>(k);
   gl.v = static_cast<const __nv_bfloat16*>(v);

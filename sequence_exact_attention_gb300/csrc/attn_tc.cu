@@ -558,7 +558,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
       if constexpr (kWin) {
         Iter it;
         it.init(g, r, q_lo, q_valid);
-        n = it.length();
+        n = it.length(g);
       } else {
         n = kv_walk_length(g, r, q_lo, q_valid);
       }

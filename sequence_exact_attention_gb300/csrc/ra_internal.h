@@ -49,14 +49,18 @@ struct Geometry {
 // always one rank and one segment).
 // In the dK/dV kernel the key tiles that hold a first token are seen from the
 // whole sequence: their work is cut into `sink_splits` shares of `sink_span`
-// query positions (tiles counted by their first position), joined through
-// `sink_part` when there are more than one.
+// query positions (tiles counted by their first position). When the other tiles
+// are too few to fill the card, a group's query heads are cut into `head_splits`
+// shares. Shares join through `part` where there are more than one.
 struct WinGeometry : Geometry {
   int window, n_sink;
   int sink_tiles;      // at most so many key tiles of a sequence hold one
   int sink_splits;
   int sink_span;
-  float* sink_part;    // [B * H_kv][sink_tiles][sink_splits][dV, dK][tile][D]
+  int head_splits;
+  // [B * H_kv][sink_tiles][sink_splits], then [B * H_kv][nt][head_splits], each (if
+  // more than one share) [dV, dK][tile][D]
+  float* part;
   const __nv_bfloat16 *q, *k, *v;    // the backward's, for narrow windows
 };
 
@@ -118,8 +122,8 @@ ra_status launch_attn_bwd(const Geometry& g, const void* q, const void* k, const
                           void* dk, void* dv, float* workspace, int phases,
                           int* dev_status, cudaStream_t stream);
 
-// The windowed backward: plan_window_bwd fills the sink fields of g (but for
-// sink_part) and returns the floats of partial sums the launch wants after
+// The windowed backward: plan_window_bwd fills the share fields of g (but for
+// part) and returns the floats of partial sums the launch wants after
 // bwd_workspace_floats(g).
 long long plan_window_bwd(WinGeometry* g);
 ra_status launch_attn_bwd_window(const WinGeometry& g, const void* q, const void* k,

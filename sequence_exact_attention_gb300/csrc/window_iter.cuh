@@ -19,68 +19,73 @@
 namespace ra {
 
 struct WinKvIter {
-  int ti, end;      // next tile, past the last
-  int n_first, w0;  // tiles of first tokens that the windows left behind; the windows' first
-  int q_lo, q_hi;
+  int lo, end;               // first position of the next tile; past the last tile
+  int first_end, w0;         // tiles of first tokens that the windows left behind end
+                             // here; the windows' first tile
+  int full_to, window_from, sink_to;   // tiles that need no mask start here
 
-  __device__ __forceinline__ void init(const WinGeometry& g, int, int q_first, int q_valid) {
-    q_lo = q_first;
-    q_hi = q_first + q_valid - 1;
-    end = q_valid > 0 ? q_hi / g.tile + 1 : 0;
-    w0 = min(max(q_lo - g.window + 1, 0) / g.tile, end);
-    n_first = min((g.n_sink + g.tile - 1) / g.tile, w0);
-    ti = n_first > 0 ? 0 : w0;
+  __device__ __forceinline__ void init(const WinGeometry& g, int, int q_lo, int q_valid) {
+    const int q_hi = q_lo + q_valid - 1;
+    end = q_valid > 0 ? (q_hi / g.tile + 1) * g.tile : 0;
+    w0 = min(max(q_lo - g.window + 1, 0) / g.tile * g.tile, end);
+    first_end = min((g.n_sink + g.tile - 1) / g.tile * g.tile, w0);
+    lo = first_end > 0 ? 0 : w0;
+    // all keys are at or before the first query (a ragged tile never is), and in
+    // the last query's window or first tokens
+    full_to = q_lo - g.tile + 1;
+    window_from = q_hi - g.window + 1;
+    sink_to = g.n_sink - g.tile;
   }
   // Key tiles in all.
-  __device__ __forceinline__ int length() const { return n_first + end - w0; }
+  __device__ __forceinline__ int length(const WinGeometry& g) const {
+    return (first_end + end - w0) / g.tile;
+  }
 
   __device__ __forceinline__ bool next(const WinGeometry& g, KvTile& kv) {
-    if (ti >= end) return false;
-    kv.step = kv.src = kv.seg = 0;
-    kv.id = ti;
-    kv.lo = ti * g.tile;
-    kv.valid = min(g.tile, g.S - kv.lo);
-    const int hi = kv.lo + kv.valid;
-    const bool all_allowed = hi - 1 <= q_lo && (kv.lo > q_hi - g.window || hi <= g.n_sink);
-    kv.work = (all_allowed && kv.valid == g.tile) ? kNoMask : kMask;
-    if (++ti == n_first) ti = w0;
+    if (lo >= end) return false;
+    kv.step = kv.src = kv.seg = kv.id = 0;
+    kv.lo = lo;
+    kv.valid = min(g.tile, g.S - lo);
+    kv.work = lo <= full_to && (lo >= window_from || lo <= sink_to) ? kNoMask : kMask;
+    lo += g.tile;
+    if (lo == first_end) lo = w0;
     return true;
   }
 };
 
 template <int kT>
 struct WinQIterT {
-  int h, h_end;           // query heads of the group
-  int ti, first, end;     // next tile of head h; its first and past its last
-  int kv_lo, kv_hi;
+  int h, h_end;              // query heads of the group
+  int lo, first, end;        // next tile's first position; of a head's first tile, past its last
+  int masked_to, masked_from;    // tiles that start before, or whose last query is from here on
 
   // The tiles whose first position is in [share_lo, share_hi).
-  __device__ __forceinline__ void init(const WinGeometry& g, int, int kv_lo_, int kv_valid,
+  __device__ __forceinline__ void init(const WinGeometry& g, int, int kv_lo, int kv_valid,
                                        int h_begin, int h_end_, int share_lo, int share_hi) {
-    h = h_begin;
-    h_end = kv_valid > 0 ? h_end_ : h_begin;
-    kv_lo = kv_lo_;
-    kv_hi = kv_lo_ + kv_valid - 1;
+    const int kv_hi = kv_lo + kv_valid - 1;
     // the last query position that sees a key of the tile
     const int p_max = kv_lo < g.n_sink ? g.S - 1 : min(kv_hi + g.window - 1, g.S - 1);
-    first = max(kv_lo / kT, (share_lo + kT - 1) / kT);
-    end = min(p_max / kT + 1, (share_hi + kT - 1) / kT);
-    ti = first;
+    first = max(kv_lo, share_lo + kT - 1) / kT * kT;
+    end = min(p_max + 1, share_hi);
+    lo = first;
+    h = h_begin;
+    h_end = kv_valid > 0 && first < end ? h_end_ : h_begin;
+    masked_to = kv_hi;
+    masked_from = kv_hi >= g.n_sink ? kv_lo + g.window : 0x7fffffff;
   }
   __device__ __forceinline__ bool next(const WinGeometry& g, QTile& o) {
-    if (ti >= end) {
-      ti = first;
-      ++h;
-    }
-    if (h >= h_end || first >= end) return false;
+    if (h >= h_end) return false;
     o.h = h;
     o.seg = 0;
-    o.ti = ti;
-    o.lo = ti * kT;
-    o.valid = min(kT, g.S - o.lo);
-    o.mask = kv_hi > o.lo ||
-             (o.lo + o.valid - 1 >= kv_lo + g.window && kv_hi >= g.n_sink);
-    ++ti;
+    o.ti = lo / kT;
+    o.lo = lo;
+    o.valid = min(kT, g.S - lo);
+    o.mask = lo < masked_to || lo + o.valid - 1 >= masked_from;
+    lo += kT;
+    if (lo >= end) {
+      lo = first;
+      ++h;
+    }
     return true;
   }
 };

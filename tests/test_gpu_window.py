@@ -56,6 +56,8 @@ CASES = [
     ("s1300_w130_sink160", 1, 2, 2, 1300, 64, 1, "contiguous", 130, 160),
     ("s1301_w256_sink161_p2", 1, 2, 2, 1301, 128, 2, "contiguous", 256, 161),
     ("s1300_w600_sink20_p5", 1, 2, 2, 1300, 128, 5, "zigzag", 600, 20),
+    ("s1500_mqa7_heads_shared", 1, 7, 1, 1500, 128, 1, "contiguous", 300, 0),
+    ("s700_gqa6_heads_and_positions_shared", 2, 12, 2, 700, 64, 1, "contiguous", 90, 140),
     ("window_past_the_end", 1, 2, 2, 300, 128, 1, "contiguous", 1 << 30, 1 << 30),
 ]
 
@@ -121,6 +123,7 @@ PACKED = [
     ("mixed", [300, 0, 1, 777, 128, 1000], 4, 2, 128, 1, "contiguous", 100, 4),
     ("mixed_zigzag", [300, 0, 1, 777, 128, 1000], 4, 2, 64, 4, "zigzag", 130, 150),
     ("long_and_short", [2500, 3, 40], 2, 1, 64, 1, "contiguous", 64, 16),
+    ("mqa8_heads_shared", [700, 0, 130, 5], 8, 1, 64, 1, "contiguous", 200, 9),
     ("one_token_each", [1, 1, 1], 2, 2, 128, 2, "contiguous", 1, 1),
 ]
 
@@ -161,7 +164,8 @@ def test_packed_matches_oracle(case, dtype):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_a_window_over_everything_is_the_causal_call(D, dtype):
-    q, k, v, do = (t.to(DEV) for t in draw((1, 700), 4, 2, D, dtype, 31))
+    # a query head a key/value head: no heads are shared out, which would change the order of sums
+    q, k, v, do = (t.to(DEV) for t in draw((1, 700), 4, 4, D, dtype, 31))
     a, la = binding.ring_attn_fwd(q, k, v, 1, True)
     for P, order in ((1, "contiguous"), (2, "zigzag"), (8, "contiguous")):
         b, lb = binding.ring_attn_fwd_window(q, k, v, P, 700, 0, order=order)

@@ -72,10 +72,16 @@ def test_backward_refusals(lib):
 
 def test_workspace(lib):
     assert lib.ring_attn_bwd_window_workspace(1, 4, 2, 1000, 128, 2, 100, 4, 0, 0, None) == NULL
-    st, rows = need(lib, n_sink=0)
-    assert st == OK and rows == binding.bwd_workspace_bytes(1, 4, 1000, 128, 2)     # no parts without first tokens
+    one = dict(H_q=2, H_kv=2)                              # a query head a key/value head: no heads to share out
+    st, rows = need(lib, n_sink=0, **one)
+    assert st == OK and rows == binding.bwd_workspace_bytes(1, 2, 1000, 128, 2)     # no parts without first tokens
     # a window that sees everything needs no shares
-    assert need(lib, window=1000) == (OK, rows)
+    assert need(lib, window=1000, **one) == (OK, rows)
+    # few key tiles with eight heads each: a part for every head of the 2 x 8 tiles
+    st, n = need(lib, H_q=16, n_sink=0)
+    assert st == OK and n - binding.bwd_workspace_bytes(1, 16, 1000, 128, 2) == 16 * 8 * (2 * 128 * 128 * 4)
+    # ... but not where the key tiles fill the card
+    assert need(lib, H_q=16, B=8, S=8000, n_sink=0) == (OK, binding.bwd_workspace_bytes(8, 16, 8000, 128, 1))
     # long sequences: shares of 2 x 128 x D floats for the one tile of every key/value head
     st, n = need(lib, S=100000, P=1)
     base = binding.bwd_workspace_bytes(1, 4, 100000, 128, 1)

@@ -32,7 +32,7 @@ int ra_win_walk(int S, int tile, int window, int n_sink, int ti, int rows, int* 
   const int q_lo = ti * g.tile, q_valid = std::min(rows, S - q_lo);
   ra::WinKvIter it;
   it.init(g, 0, q_lo, q_valid);
-  const int length = it.length();
+  const int length = it.length(g);
   ra::KvTile kv;
   int n = 0;
   while (it.next(g, kv)) {
