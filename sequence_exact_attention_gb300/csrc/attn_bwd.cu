@@ -259,12 +259,98 @@ bwd_prep_kernel(const Geometry gp, const __nv_bfloat16* __restrict__ out,
   }
 }
 
-// The same for narrow windows, where a row sees at most kNarrow keys: delta_i =
-// sum_j p_ij <dO_i, v_j> from the probabilities themselves. The forward's out
-// is rounded to bf16, and a row of few keys cannot average that rounding away:
-// dq and dk came out 2.2 times the rounding of bf16 off at a window of 2 (the
-// products' own roundings leave 1.4), 1.5 times at 16. The sum costs less than
-// one tile product of the same rows. 8 threads a row, as above.
+// The same for windowed calls, but for the first kFirst rows of a sequence: their
+// delta_i = sum_j p_ij <dO_i, v_j> comes from the probabilities themselves. The
+// forward's out is rounded to bf16, and a row of few keys cannot average that
+// rounding away: dq and dk of sequences of 15 and 61 tokens came out 1.7 times the
+// rounding of bf16 off (the products' own roundings leave 1.4). 128 threads a row,
+// four a key, in blocks that come first: few loads behind one another.
+constexpr int kFirst = 32;
+constexpr int kFirstBlocks = kFirst / 2;       // of a (batch, head)
+template <int D, bool kVarlen>
+__global__ void __launch_bounds__(256, 8)
+bwd_prep_window_kernel(const WinGeometry gp, const __nv_bfloat16* __restrict__ out,
+                       const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,
+                       float* __restrict__ lse2, float* __restrict__ delta,
+                       int* __restrict__ status) {
+  constexpr int C = D / 8;               // 16-byte pieces of a row
+  const int heads = gp.B * gp.H_q, rows = gp.nt * kT;
+  const bool first = (int)blockIdx.x < heads * kFirstBlocks;
+  const int block = (int)blockIdx.x - (first ? 0 : heads * kFirstBlocks);
+  const int per = first ? kFirstBlocks : rows / 32 - 1;      // blocks of a (batch, head)
+  const int bh = block / per;
+  const int pos = first ? block % per * 2 + (threadIdx.x >> 7)
+                        : block % per * 32 + kFirst + (threadIdx.x >> 3);
+  const int b = bh / gp.H_q, h = bh % gp.H_q, hk = h / (gp.H_q / gp.H_kv);
+  WinGeometry gv;
+  int row0 = 0;
+  if constexpr (kVarlen) varlen_window_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
+  const WinGeometry& g = kVarlen ? gv : gp;
+  const size_t srow = seg_rows(gp, b, 0, row0, kVarlen).grow;
+  const size_t lrow = lse_base(gp, b, h, 0, row0, kVarlen);
+  const size_t off = ((srow + pos) * g.H_q + h) * D;
+  const bool valid = pos < g.S && in_range((long long)off, D, extent_q(gp), status) &&
+                     in_range((long long)(lrow + pos), 1, extent_lse(gp), status);
+  const float nl2 = valid ? -(lse[lrow + pos] * kLog2e) : -INFINITY;
+  auto dot = [](const uint4& x, const uint4& y, float sum) {
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      sum = fmaf(bf_lo(xw[w]), bf_lo(yw[w]), sum);
+      sum = fmaf(bf_hi(xw[w]), bf_hi(yw[w]), sum);
+    }
+    return sum;
+  };
+  const uint4* dp = reinterpret_cast<const uint4*>(dout + off);
+  float acc = 0.f;
+  if (first) {
+    __shared__ float sums[8];
+    const int j = (threadIdx.x >> 2) & 31, slice = threadIdx.x & 3;
+    const size_t koff = ((srow + j) * g.H_kv + hk) * D;
+    const bool sees = valid && j <= pos && (j > pos - g.window || j < g.n_sink) &&
+                      in_range((long long)koff, D, extent_kv(gp), status);
+    float s = 0.f, t = 0.f;
+    if (sees) {
+      const uint4* qp = reinterpret_cast<const uint4*>(gp.q + off) + slice;
+      const uint4* kp = reinterpret_cast<const uint4*>(gp.k + koff) + slice;
+      const uint4* vp = reinterpret_cast<const uint4*>(gp.v + koff) + slice;
+#pragma unroll
+      for (int c = 0; c < C; c += 4) s = dot(qp[c], kp[c], s);
+#pragma unroll
+      for (int c = 0; c < C; c += 4) t = dot(dp[slice + c], vp[c], t);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o *= 2) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    if (sees) acc = ex2_approx(fmaf(s, g.scale_log2, nl2)) * t;
+#pragma unroll
+    for (int o = 4; o < 32; o *= 2) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = acc;
+    __syncthreads();
+    const float* mine = sums + (threadIdx.x >> 7) * 4;
+    acc = (mine[0] + mine[1]) + (mine[2] + mine[3]);
+  } else if (valid) {
+    const int sub = threadIdx.x & 7;
+    const uint4* op = reinterpret_cast<const uint4*>(out + off);
+#pragma unroll
+    for (int i = 0; i < C / 8; ++i) acc = dot(op[sub * (C / 8) + i], dp[sub * (C / 8) + i], acc);
+  }
+  if (!first) {
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  }
+  if ((threadIdx.x & (first ? 127 : 7)) == 0) {
+    const long long at = (long long)bh * rows + pos;
+    lse2[at] = nl2;
+    delta[at] = valid ? -acc : 0.f;
+  }
+}
+
+// And for narrow windows, where every row sees at most kNarrow keys: delta_i so
+// too (2.2 roundings off at a window of 2, 1.5 at 16, with the output's). The sum
+// costs less than one tile product of the same rows. 8 threads a row, as above.
 constexpr int kNarrow = 16;
 template <int D, bool kVarlen>
 __global__ void __launch_bounds__(256)
@@ -1214,15 +1300,23 @@ ra_status launch_d(const G& g, const CUtensorMap& mq, const CUtensorMap& mk,
   if (phases & RA_BWD_PREP) {
     bool narrow = false;
     if constexpr (kWin) {
-      narrow = (long long)g.window + g.n_sink <= kNarrow || g.S <= kNarrow;
+      narrow = (long long)g.window + g.n_sink <= kNarrow;
       if (narrow)
         bwd_prep_narrow_kernel<D, kVarlen><<<(unsigned)prep_blocks, 256, 0, stream>>>(
             g, static_cast<const __nv_bfloat16*>(dout), lse, lse2, delta, rows, status);
     }
-    if (!narrow)
+    if constexpr (kWin) {
+      if (!narrow)
+        bwd_prep_window_kernel<D, kVarlen>
+            <<<(unsigned)(prep_blocks + (long long)g.B * g.H_q * (kFirstBlocks - 1)), 256, 0,
+               stream>>>(
+            g, static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout),
+            lse, lse2, delta, status);
+    } else {
       bwd_prep_kernel<D, kVarlen><<<(unsigned)prep_blocks, 256, 0, stream>>>(
           g, static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(dout),
           lse, lse2, delta, rows, status);
+    }
     if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
   }
   if (phases & RA_BWD_DKDV) {

@@ -101,9 +101,10 @@ def test_gradients_lose_no_more_than_two_roundings(D, window, n_sink):
         assert err <= 1.1 * np.sqrt(2) * np.linalg.norm(rounded - w), (name, err / np.linalg.norm(w))
 
 
-def test_packed_sequences_of_few_tokens():
+@pytest.mark.parametrize("lengths,D", [([5, 2, 16, 1, 9, 12] * 20, 64), ([61, 15], 128), ([16, 1, 38, 11, 58], 64),
+                                       ([33, 40, 70] * 3, 128)])
+def test_packed_sequences_of_few_tokens(lengths, D):
     """No row sees more than its short sequence: the same holds."""
-    lengths, D = [5, 2, 16, 1, 9, 12] * 20, 64
     total, longest = sum(lengths), max(lengths)
     q, k, v, do = draw((total,), 4, 2, D, torch.bfloat16, 78)
     cu = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
@@ -177,9 +178,16 @@ def test_a_window_over_everything_is_the_causal_call(D, dtype):
         else:
             # the same sums in the same order, whatever the ranks
             assert torch.equal(a, b) and torch.equal(la, lb)
-            for x, y in zip(binding.ring_attn_bwd(q, k, v, a, la, do, 1, True),
-                            binding.ring_attn_bwd_window(q, k, v, b, lb, do, P, 700, 0, order=order)):
-                assert torch.equal(x, y)
+            want = binding.ring_attn_bwd(q, k, v, a, la, do, 1, True)
+            got = binding.ring_attn_bwd_window(q, k, v, b, lb, do, P, 700, 0, order=order)
+            # but for the first 32 rows' delta, which windowed calls do not take from the rounded
+            # output: those rows of dq, and all of dk, may differ by what that rounding is worth,
+            # which is less than the half step 2^-8 that either result is rounded by
+            assert torch.equal(want[2], got[2]) and torch.equal(want[0][:, 32:], got[0][:, 32:])
+            for x, y in zip(want[:2], got[:2]):
+                assert (x.double() - y.double()).norm() <= 2.0 ** -8 * x.double().norm()
+            first = got if P == 1 else first
+            assert all(torch.equal(x, y) for x, y in zip(got, first))
 
 
 @pytest.mark.parametrize("D", [64, 128])
