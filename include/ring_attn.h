@@ -399,9 +399,9 @@ ra_status ring_attn_fwd_window_varlen(const void* q, const void* k, const void* 
  * those of the packed form. RA_BF16 only. The workspace size comes from
  * ring_attn_bwd_window_workspace with the call's sizes (packed: B = n_seq,
  * S = max_seqlen, varlen = 1); beside the row statistics it holds float32
- * parts of dK and dV of the key tiles with first tokens, which the whole
- * sequence sees and whose work is therefore shared out. Gradients repeat bit
- * for bit. Errors as ring_attn_bwd, RA_ERR_RANGE for window and n_sink.
+ * parts of dK and dV of the key tiles whose work is shared out: those with
+ * first tokens, which the whole sequence sees, and all where key/value heads
+ * and tiles are few. Gradients repeat bit for bit. Errors as ring_attn_bwd, RA_ERR_RANGE for window and n_sink.
  */
 ra_status ring_attn_bwd_window_workspace(int B, int H_q, int H_kv, int S, int D, int P,
                                          int window, int n_sink, int order, int varlen,

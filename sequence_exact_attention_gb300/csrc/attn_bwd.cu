@@ -38,10 +38,10 @@
 // wave's idle multiprocessors. (Windows make both grids many equal, short
 // CTAs, whose last waves are mostly idle.) It waits for that grid at its own
 // end only, so that what follows on the stream finds both done.
-// Measured with windows: 32 heads on 8, D = 128, S = 16384, window 2048 1.41 ms
-// (prep 45 us, dK/dV 680, dQ 650, joins 10), 915 TFLOP/s of 10 D a visible pair;
-// two sequences of 4096, 16 heads, window 1024 252 us. (dQ with the first tokens'
-// tile as 32 columns: no change.)
+// Measured with windows: 32 heads on 8, D = 128, S = 16384, window 2048 1.43 ms
+// (prep 46 us, dK/dV 685, dQ 650, joins 10), 900 TFLOP/s of 10 D a visible pair;
+// two sequences of 4096, 16 heads, window 1024 259 us. (dQ with the first tokens'
+// tile as 32 columns, dK/dV launched early after prep, the join after dQ: no change.)
 // The two gradient kernels both recompute S and dP; in exchange neither needs
 // atomics, and each gradient is accumulated on chip and written once.
 //

@@ -317,14 +317,15 @@ __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint6
 // stay visible. The walk then covers only the key tiles that some row of the
 // block sees, in position order (window_iter.cuh), and a score is also masked
 // where its key lies between the first tokens and the row's window.
-// Measured (D = 128): S = 32768, 32 heads on 8, window 4096, halves of 8 ranks
-// 1.62 ms, 1270 TFLOP/s of the pairs that see each other; S = 16384, window 2048
-// 474 us, 1090; two sequences of 4096, 16 heads, window 1024 81 us, 745. What the
-// tiles' edges and the first tokens' tile hold besides makes the work 1.09, 1.18
-// and 1.34 times those pairs. (Leaving out, for each query tile, the key tiles
-// that only the other one sees, and working on 32 columns of the first tokens'
-// tile, saves a tenth of the tiles and cost more in all others: the softmax loop
-// went from 147 to 156 registers and more, the times to 1.74 ms, 482 and 81 us.)
+// Measured (D = 128): S = 32768, 32 heads on 8, window 4096 1.47 ms, 1400 TFLOP/s
+// of the pairs that see each other; S = 16384, window 2048 455 us, 1135; two
+// sequences of 4096, 16 heads, window 1024 79 us, 765. What the tiles' edges and
+// the first tokens' tile hold besides makes the work 1.09, 1.18 and 1.34 times
+// those pairs. (Leaving out, for each query tile, the key tiles that only the
+// other one sees, and working on 32 columns of the first tokens' tile, saves a
+// tenth of the tiles and cost more in all others: the softmax loop went from 147
+// to 156 registers and more, the times, then 1.62 ms, 474 and 81 us, to 1.74 ms,
+// 482 and 81 us.)
 template <int D, bool kOutF32, bool kVarlen, bool kWithholdV0, class G = Geometry>
 __global__ void __launch_bounds__(Roles<D>::kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
