@@ -385,6 +385,48 @@ def test_calls_on_a_given_stream():
     assert torch.equal(out, want) and torch.equal(lse, want_l)
 
 
+def test_calls_side_by_side_and_from_two_graphs():
+    """Attention with scores and eviction on two streams at once, eager and then
+    as two captured graphs replayed together, equal the calls made alone."""
+    torch.cuda.synchronize()
+    work = []
+    for seed in (61, 62):
+        cache, _, _ = random_cache(2, 2, 4096, 64, seed=seed)
+        q = torch.randn(2, 1, 8, 64, device=DEV).to(torch.bfloat16)
+        lens = torch.tensor([4000, 2500 + seed], dtype=torch.int32, device=DEV)
+        ws = torch.empty(binding.kv4_attn_workspace_bytes(2, 1, 8, 2, 64, 4096, with_score=True), dtype=torch.uint8,
+                         device=DEV)
+        work.append((cache, q, lens, torch.zeros(2, 2, 4096, device=DEV), ws, torch.cuda.Stream()))
+
+    def step(cache, q, lens, score, ws, stream):
+        score.zero_()
+        out, lse = binding.kv4_attn(q, cache, lens, score=score, workspace=ws)
+        dst, ds, dl, kept = binding.kv4_evict(cache, score, lens, 512, 4, 64)
+        return (out, lse, score, ds, dl, kept, *dst)
+
+    want = []
+    for w in work:
+        want.append([t.clone() for t in step(*w)])
+        torch.cuda.synchronize()
+    got = []
+    for w in work:
+        with torch.cuda.stream(w[-1]):
+            got.append(step(*w))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+    graphs = []
+    for w in work:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=w[-1]):
+            graphs.append((g, step(*w)))
+    for _ in range(3):
+        for (g, _), w in zip(graphs, work):
+            with torch.cuda.stream(w[-1]):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for (_, x), y in zip(graphs, want) for a, b in zip(x, y))
+
+
 def test_attention_repeats_bit_for_bit_and_merges():
     """Two halves of a cache merged by attn_lse_merge give the whole."""
     B, H_q, H_kv, D, C = 1, 8, 2, 128, 2048
