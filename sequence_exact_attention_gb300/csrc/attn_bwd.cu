@@ -286,6 +286,7 @@ bwd_prep_window_kernel(const WinGeometry gp, const __nv_bfloat16* __restrict__ o
   int row0 = 0;
   if constexpr (kVarlen) varlen_window_geometry(gp, b, gv, row0, threadIdx.x == 0 ? status : nullptr);
   const WinGeometry& g = kVarlen ? gv : gp;
+  if (pos / kT * kT >= g.S) return;      // a tile without a token: nobody reads it
   const size_t srow = seg_rows(gp, b, 0, row0, kVarlen).grow;
   const size_t lrow = lse_base(gp, b, h, 0, row0, kVarlen);
   const size_t off = ((srow + pos) * g.H_q + h) * D;
