@@ -548,6 +548,9 @@ ra_status kv4_attn_workspace(int B, int S_q, int H_q, int H_kv, int D, int C,
  * window, n_sink is ignored). Slots are counted as they lie, so after an
  * eviction a window counts kept slots. Head h reads key/value head
  * h / (H_q / H_kv). A row that sees no slot gets out = 0, lse = -inf.
+ * A row's results depend on the slots that it sees alone, to the bit, whatever
+ * the others hold (a later drafted token that is not finite, say); a value that
+ * is not finite reaches its own group of 64 dimensions.
  *     q, out  [B, S_q, H_q, D] bfloat16    lse  [B, H_q, S_q] float32 or NULL
  * score: NULL, or float32 [B, H_kv, C]: every slot's attention weight, summed
  * over the queries and the heads of its group, is ADDED to it.

@@ -54,9 +54,12 @@
 // Roundings: q is scaled by a power of two a row and becomes half precision
 // (exact for bf16 values down to 2^-17 of the row's largest; queries beyond
 // 2^90 are out of range); p times the value scale becomes half precision, 11
-// bits, relative to the largest value scale met so far (a power of two, raised
-// like the running maximum), so a weight is off by at most 2^-11 of itself, or
-// 2^-25 of the largest where it is a subnormal half. Sums are float32.
+// bits, brought into its range by a power of two that each row keeps for each
+// group: the largest product of the row's own met so far becomes 1 or more. A
+// weight is off by at most 2^-11 of itself, or 2^-25 of the group's largest where
+// it is a subnormal half. Sums are float32. Nothing of this is shared between
+// rows: what a row does not see (a later drafted token's infinite value, a slot
+// that another row's window still holds) changes no bit of its results.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -78,8 +81,10 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kWarpSlots = kKv4Tile / kWarps;
 static_assert(kWarpSlots == 32, "two 16-slot products a warp and tile");
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr float kRescaleLog2 = 8.0f;      // p stays below 2^8
+constexpr int kRescaleLog2 = 4;           // p stays below 2^4
 constexpr int kFlush = 8;
+constexpr int kLiftMax = 112;             // p 2^112 is finite
+constexpr int kWeightLog2 = 15;           // weights stay below 2^15, in half's range
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float k2P24 = 16777216.f, k2Pm24 = 1.f / k2P24;
 
@@ -149,6 +154,7 @@ __device__ __forceinline__ uint32_t codes2(uint32_t x) {
 }
 
 __device__ __forceinline__ float pow2_field(int f) { return __uint_as_float((uint32_t)f << 23); }
+__device__ __forceinline__ int exponent_field(float x) { return (int)(__float_as_uint(x) >> 23); }
 
 // The stages, and what the warps leave for the join over the same memory
 // once all are done.
@@ -298,11 +304,12 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
     }
   }
 
-  // Running state of rows 2c and 2c + 1, in the logits' units before sl2: the
-  // maximum m, the bound that a score has to pass to raise it, and what the
-  // exponent subtracts.
+  // Running state of rows 2c and 2c + 1: what the exponent subtracts (the running
+  // maximum in base 2, rounded down, so that raising it scales sums by a power of
+  // two), and the bound that a score (before sl2) has to pass to raise it; -inf
+  // until the row has seen a slot.
   float o[NT][NG][4][4];
-  float m[NT][2], bound[NT][2], sub[NT][2], l[NT][2], zo[NT][NG][2];
+  float bound[NT][2], sub[NT][2], l[NT][2], zo[NT][NG][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -313,16 +320,25 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
         for (int i = 0; i < 4; ++i) o[nt][gr][e][i] = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      m[nt][i] = bound[nt][i] = -INFINITY;
+      bound[nt][i] = -INFINITY;
       sub[nt][i] = l[nt][i] = 0.f;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) zo[nt][gr][i] = 0.f;
     }
   }
-  // The largest value scale so far, as bf16 bits up to its binade's end, and
-  // 2^-(its exponent + 1).
-  uint32_t v_top = 127;
-  float v_down = pow2_field(253);
+  // The power of two that a row's products p sv of a group are multiplied by
+  // for half precision (o is in its units; 2^112 until the first), and the largest
+  // scale, as bf16 bits, that no product of this lane's rows leaves the range with.
+  float lift[NT][2][NG];
+  uint32_t sv_bound[NG];
+#pragma unroll
+  for (int gr = 0; gr < NG; ++gr) sv_bound[gr] = 0;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) lift[nt][h][gr] = pow2_field(127 + kLiftMax);
   // -8 2^-24 times the rows' weights not yet taken off o: of group 0 (rows 0-7
   // of the product) in the first two, of group 1 in the others
   float off[NT][4];
@@ -330,21 +346,31 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int x = 0; x < 4; ++x) off[nt][x] = 0.f;
+  auto flush_row = [&](int nt, int h, int gr) {
+    const float y = off[nt][2 * gr + h];
+    off[nt][2 * gr + h] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      o[nt][gr][e][h] += y;                                     // low nibbles
+      o[nt][gr][e][2 + h] = fmaf(16.f, y, o[nt][gr][e][2 + h]);  // high ones
+    }
+  };
   auto flush = [&] {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          const float y = off[nt][2 * gr + x];
-          off[nt][2 * gr + x] = 0.f;
+        for (int gr = 0; gr < NG; ++gr) flush_row(nt, h, gr);
+  };
+  // A row's sums of a group times mul; all lanes of the row together.
+  auto scale_row = [&](int nt, int h, int gr, float mul) {
+    flush_row(nt, h, gr);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[nt][gr][e][x] += y;                                     // low nibbles
-            o[nt][gr][e][2 + x] = fmaf(16.f, y, o[nt][gr][e][2 + x]);  // high ones
-          }
-        }
+    for (int e = 0; e < 4; ++e) {
+      o[nt][gr][e][h] *= mul;
+      o[nt][gr][e][2 + h] *= mul;
+    }
   };
 
   int stage = 0;
@@ -433,26 +459,22 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
     // ---- tiles that some row does not see in full
     const bool whole = j0 + kWarpSlots - 1 <= sp.pmin &&
                        (a.window <= 0 || j0 > sp.pmax - a.window || j0 + kWarpSlots <= a.n_sink);
+    uint32_t hidden = 0;                     // a bit for each score of a slot that its row does not see
     if (!whole) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bool any = false;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bool ok = sees(a, pos[nt][h], j0 + 8 * i + g);
-            any |= ok;
-            if (!ok) s[i][nt][h] = -INFINITY;
-          }
-        // a slot that none of this lane's rows sees may hold anything
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr)
-          if (!any) mv[i][gr] = 0;
-      }
+          for (int h = 0; h < 2; ++h)
+            if (!sees(a, pos[nt][h], j0 + 8 * i + g)) {
+              s[i][nt][h] = -INFINITY;
+              hidden |= 1u << ((i * NT + nt) * 2 + h);
+            }
     }
-    // ---- raise the running maxima and the value scale only when a score or a
-    // scale passes its bound (then for the whole warp): rare after the first tile
+    // ---- raise the running maxima, and lower lifts, only when a score or a scale
+    // passes its bound: rare after the first tile. Which rows are changed, and
+    // how, goes by what each of them sees.
     bool raise = false;
     float top[NT][2];
 #pragma unroll
@@ -462,22 +484,14 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
         top[nt][h] = fmaxf(fastmath::fmax3(s[0][nt][h], s[1][nt][h], s[2][nt][h]), s[3][nt][h]);
         raise |= top[nt][h] > bound[nt][h];
       }
-    uint32_t scale_top = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int gr = 0; gr < NG; ++gr) {
+      uint32_t sv_top = 0;
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) scale_top = max(scale_top, mv[i][gr] & 0x7fffu);
-    raise |= scale_top > v_top;
+      for (int i = 0; i < 4; ++i) sv_top = max(sv_top, mv[i][gr] & 0x7fffu);
+      raise |= sv_top > sv_bound[gr];
+    }
     if (__any_sync(0xffffffffu, raise)) {
-      flush();
-      float shrink = 1.f;
-      scale_top = __reduce_max_sync(0xffffffffu, scale_top);
-      if (scale_top > v_top) {
-        const float down = pow2_field(max(253 - (int)(scale_top >> 7), 1));
-        shrink = down / v_down;
-        v_down = down;
-        v_top = scale_top | 127u;
-      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -485,24 +499,60 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
           float x = top[nt][h];
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          float alpha = 1.f;
           if (x > bound[nt][h]) {
-            alpha = exp2f((m[nt][h] - x) * sl2[nt][h]);       // 0 from -inf
-            m[nt][h] = x;
-            bound[nt][h] = x + kRescaleLog2 / sl2[nt][h];
-            sub[nt][h] = x * sl2[nt][h];
-          }
-          l[nt][h] *= alpha;
+            // whole numbers: the sums so far take a power of two, exactly
+            const float to = floorf(x * sl2[nt][h]);
+            const float alpha = bound[nt][h] == -INFINITY ? 0.f : exp2f(sub[nt][h] - to);
+            sub[nt][h] = to;
+            bound[nt][h] = (to + (float)kRescaleLog2) / sl2[nt][h];
+            l[nt][h] *= alpha;
+            // the products met so far shrink by alpha, so what brings them to 1
+            // grows by 1 / alpha and o stays as it is, but at the end of the range
+            const int grow = 127 - exponent_field(alpha);
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            zo[nt][gr][h] *= alpha;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              o[nt][gr][e][h] *= alpha * shrink;
-              o[nt][gr][e][2 + h] *= alpha * shrink;
+            for (int gr = 0; gr < NG; ++gr) {
+              const int f = exponent_field(lift[nt][h][gr]), up = min(grow, 127 + kLiftMax - f);
+              const float mul = alpha * pow2_field(127 + up);
+              lift[nt][h][gr] = pow2_field(f + up);
+              if (mul != 1.f) scale_row(nt, h, gr, mul);
+              zo[nt][gr][h] *= alpha;
             }
           }
         }
+      // A scale that is not finite goes to the zero point as NaN, which reaches the
+      // rows that see the slot, in this group alone; a product would take it to the
+      // other group, as 0 times NaN in the constant operand's other rows.
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr)
+          if ((mv[i][gr] & 0x7f80u) == 0x7f80u) mv[i][gr] = 0x7fc00000u;
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        int most = 0;                        // exponent field of the lane's largest lift
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = 0.f;                   // the row's largest product, times 2^-16
+#pragma unroll
+            for (int i = 0; i < 4; ++i)      // NaN and hidden slots are passed over
+              x = fmaxf(x, fabsf(sm100::ex2_approx(fmaf(s[i][nt][h], sl2[nt][h], -sub[nt][h])) *
+                                 (__uint_as_float(mv[i][gr] << 16) * (1.f / 65536.f))));
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            // 2^(to - 127) brings it to 1 to 2
+            const int f = exponent_field(lift[nt][h][gr]), to = max(238 - exponent_field(x), 1);
+            if (to < f) {
+              lift[nt][h][gr] = pow2_field(to);
+              scale_row(nt, h, gr, lift[nt][h][gr] * pow2_field(254 - f));
+            }
+            if (bound[nt][h] > -INFINITY) most = max(most, min(to, f));
+          }
+        // scales below 2^(kWeightLog2 - kRescaleLog2) / lift
+        const int below = 127 + kWeightLog2 - kRescaleLog2 - (most - 127);
+        sv_bound[gr] = ((uint32_t)min(below, 255) << 7) - 1;
+      }
     }
     // ---- weights, and their products with the value codes
 #pragma unroll
@@ -515,8 +565,8 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
           s[i][nt][h] = p;
           l[nt][h] += p;
         }
-    // masked: a slot may be hidden from one row and seen by the other; a weight
-    // of 0 then takes nothing from it, whatever its value
+    // masked: a row takes nothing from a slot that it does not see, whatever the
+    // slot's value (0 times NaN is not 0)
     auto add_values = [&](auto masked) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -530,7 +580,7 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
           uint32_t pf[NT][2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float sv = __uint_as_float(mv[2 * t + i][gr] << 16) * v_down;
+            const float sv = __uint_as_float(mv[2 * t + i][gr] << 16);
             const float zv = __uint_as_float(mv[2 * t + i][gr] & 0xffff0000u);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -538,9 +588,9 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float p = s[2 * t + i][nt][h];
-                w[h] = p * sv;
+                w[h] = p * lift[nt][h][gr] * sv;
                 float z = fmaf(p, zv, zo[nt][gr][h]);
-                if (decltype(masked)::value && p == 0.f) {
+                if (decltype(masked)::value && (hidden >> (((2 * t + i) * NT + nt) * 2 + h) & 1u)) {
                   w[h] = 0.f;
                   z = zo[nt][gr][h];
                 }
@@ -597,7 +647,6 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
   __syncthreads();                           // every ring is read
   if (threadIdx.x == 0 && (*abort_flag || *never) && a.status)
     atomicExch(a.status, (int)RA_ERR_TIMEOUT);
-  const float v_up = pow2_field(254 - (int)(__float_as_uint(v_down) >> 23));
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -615,18 +664,20 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
       const int r = nt * 8 + 2 * c + h;
       if (g == 0) {
         // in base 2 now; -inf where the row saw nothing
-        sM[warp * RB + r] = m[nt][h] == -INFINITY ? -INFINITY : sub[nt][h];
+        sM[warp * RB + r] = bound[nt][h] == -INFINITY ? -INFINITY : sub[nt][h];
         sL[warp * RB + r] = ls;
       }
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr)
+      for (int gr = 0; gr < NG; ++gr) {
+        const float down = pow2_field(254 - exponent_field(lift[nt][h][gr]));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           // low and high nibbles
-          float2 y = make_float2(fmaf(o[nt][gr][e][h] * k2P24, v_up, z[gr]),
-                                 fmaf(o[nt][gr][e][2 + h] * (k2P24 / 16.f), v_up, z[gr]));
+          float2 y = make_float2(fmaf(o[nt][gr][e][h] * k2P24, down, z[gr]),
+                                 fmaf(o[nt][gr][e][2 + h] * (k2P24 / 16.f), down, z[gr]));
           *reinterpret_cast<float2*>(sO + (warp * RB + r) * D + gr * kKv4Group + 8 * g + 2 * e) = y;
         }
+      }
     }
   __syncthreads();
   for (int i = threadIdx.x; i < RB * (D / 4); i += kThreads) {
