@@ -375,6 +375,7 @@ ra_status ring_attn_bwd_ulysses(const void* q, const void* k, const void* v,
  * ring_attn_fwd_ex.
  * Keys and values must be finite where a query does not see them, too: a
  * hidden key has weight 0, and 0 times an infinity is not a number.
+ * A row that sees a NaN score has NaN in out and in lse.
  * ring_attn_fwd_window_varlen - the same for packed sequences (conventions of
  * ring_attn_fwd_varlen): windows and first tokens are each sequence's own. A
  * sequence's results depend on its own rows only, whatever the others hold;

@@ -235,7 +235,8 @@ attn_f32_window_kernel(const WinGeometry gp, const float* __restrict__ q,
         *reinterpret_cast<float4*>(out + off + 64 * n + 4 * kc) =
             make_float4(o[r][n][0] * inv, o[r][n][1] * inv, o[r][n][2] * inv, o[r][n][3] * inv);
     if (kc == 0 && lse && in_range((long long)(lrow + pos), 1, extent_lse(gp), status))
-      lse[lrow + pos] = l[r] > 0.f ? (m[r] + log2f(l[r])) * 0.69314718055994531f : -INFINITY;
+      // 0 only where every score is -inf; the NaN of a row that sees one stays
+      lse[lrow + pos] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * 0.69314718055994531f;
   }
 }
 

@@ -313,6 +313,13 @@ __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint6
             v_desc + (uint64_t)((kk * 2048) >> 4), idesc, (accumulate || kk > 0) ? 1u : 0u);
 }
 
+// Whether a row's sum l makes an lse (else -inf: the row saw no key). In a
+// windowed call every row sees itself, and the NaN of a row that sees one stays.
+template <bool kWin>
+__device__ __forceinline__ bool row_has_lse(float l) {
+  return kWin ? l != 0.f : l > 0.f;
+}
+
 // G = WinGeometry: attention with a sliding window and a few first tokens that
 // stay visible. The walk then covers only the key tiles that some row of the
 // block sees, in position order (window_iter.cuh), and a score is also masked
@@ -803,7 +810,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
           if (row_valid && lse && part == 0 &&
               in_range((long long)(lrow + q_pos), 1, extent_lse(gp), status))
             lse[lrow + q_pos] =
-                l_tot > 0.f ? (m_run + log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
+                row_has_lse<kWin>(l_tot) ? (m_run + log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
         }
       } else if (vlog && warp == R::kTileWarps && lane == 0 && tile1_exists &&
                  in_range(log_off(1), 1, log_len, status)) {
@@ -988,7 +995,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
         if (row_valid && lse && part == 0 &&
             in_range((long long)(lrow + q_pos), 1, extent_lse(gp), status))
           lse[lrow + q_pos] =
-              l_tot > 0.f ? (m_run[qi] + log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
+              row_has_lse<kWin>(l_tot) ? (m_run[qi] + log2f(l_tot)) * 0.69314718055994531f
+                                       : -INFINITY;
       }
     }
   }
