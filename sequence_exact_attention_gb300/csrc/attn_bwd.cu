@@ -1356,7 +1356,9 @@ ra_status launch_d(const G& g, const CUtensorMap& mq, const CUtensorMap& mk,
 }  // namespace
 
 long long bwd_workspace_floats(const Geometry& g) {
-  return 2 * ws_tile(g, g.B * g.H_q, 0, 0);
+  const long long heads = (long long)g.B * g.H_q, per = (long long)g.n_seg * g.nt * kT;
+  constexpr long long kHuge = 1LL << 60;             // more than any call may have
+  return heads > kHuge / per ? 2 * kHuge : 2 * heads * per;
 }
 
 ra_status launch_attn_bwd(const Geometry& g, const void* q, const void* k, const void* v,

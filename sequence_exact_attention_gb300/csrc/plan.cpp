@@ -24,8 +24,13 @@ ra_status make_geometry(int B, int H_q, int H_kv, int S, int D, int P,
   if (B <= 0 || H_q <= 0 || H_kv <= 0 || S <= 0 || P <= 0) return RA_ERR_SHAPE;
   if (H_q % H_kv != 0) return RA_ERR_SHAPE;
   if (order != RA_ORDER_CONTIGUOUS && order != RA_ORDER_ZIGZAG) return RA_ERR_DTYPE;
-  const int parts = order == RA_ORDER_ZIGZAG ? 2 * P : P;
+  constexpr long long kMax = 0x7fffffffLL;
+  const long long all_parts = order == RA_ORDER_ZIGZAG ? 2LL * P : P;
   if (step < -1 || step >= P) return RA_ERR_RANGE;
+  // padded lengths, to a multiple of `parts` and of the tile, are ints too
+  if (S + all_parts - 1 > kMax || (S + all_parts - 1) / all_parts + tile - 1 > kMax)
+    return RA_ERR_RANGE;
+  const int parts = (int)all_parts;
   g->B = B; g->H_q = H_q; g->H_kv = H_kv; g->S = S; g->D = D; g->P = P;
   g->causal = causal ? 1 : 0;
   g->order = order;
