@@ -52,14 +52,14 @@ MERGE_METRIC = "LSE merge GB/s (algorithmic bytes)"
 # stored with it (see _kernel_digest). window_iter.cuh, which attn_tc.cu
 # includes too, is not among them: only the windowed instantiations use it.
 TRAFFIC = {
-    "attn_tc": {"sha256_16": "4538146edcdab8e1", "bytes_per_launch": {
-        "bf16_s32k_causal_zigzag": 846726912 + 255683328,
-        "bf16_s16k_d64": 402788352 + 119632384,
-        "bf16_s128k_gqa_causal": 2718674944 + 1058094080,
-        "bf16_s4k_causal": 105614080 + 10554880,
-        "bf16_s32760_uneven_causal_zigzag": 847103232 + 255800320,
-        "bf16_varlen_32k_causal_zigzag": 828689920 + 255648000,
-        "bf16_ulysses_s16k_b2_causal": 805524224 + 253269248,
+    "attn_tc": {"sha256_16": "d5b0d24472603a27", "bytes_per_launch": {
+        "bf16_s32k_causal_zigzag": 844381696 + 255606272,
+        "bf16_s16k_d64": 403381248 + 119772160,
+        "bf16_s128k_gqa_causal": 2729674752 + 1058758656,
+        "bf16_s4k_causal": 107127552 + 10650112,
+        "bf16_s32760_uneven_causal_zigzag": 844837120 + 255731712,
+        "bf16_varlen_32k_causal_zigzag": 828497152 + 255643136,
+        "bf16_ulysses_s16k_b2_causal": 805508608 + 253231104,
     }},
     # the merge was captured on S = 8192 (1.15 GiB on the device) and scaled by
     # 65536 / 8192 = 8: a streaming kernel whose bytes grow with the rows
