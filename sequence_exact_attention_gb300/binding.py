@@ -240,6 +240,12 @@ def _int_buffer(t, name, n):
         raise ValueError(f"{name} must be int32 with at least {n} elements")
 
 
+def _int32(n):
+    """n as a C int that means the same: ctypes drops the bits past 32, and what
+    is out of range stays so at its ends (all tokens, too large, negative)."""
+    return max(-1, min(int(n), 0x7fffffff))
+
+
 def _on_device(named):
     """Every tensor on one CUDA device, contiguous, and that device current
     (the library launches on the current device)."""
@@ -378,6 +384,7 @@ def ring_attn_bwd(q, k, v, out, lse, dout, P, causal, scale=None, order="contigu
 
 
 BWD_NOALLOC_MAX_BYTES = 8 << 20
+RA_ERR_RANGE = 10
 RA_ERR_SCRATCH = 11
 
 
@@ -430,7 +437,7 @@ def _varlen_args(q, k, v, cu_seqlens, max_seqlen):
     H_kv = k.shape[1]
     _like(k, "k", (total, H_kv, D), q.dtype)
     _like(v, "v", (total, H_kv, D), q.dtype)
-    return total, H_q, H_kv, D, cu_seqlens.numel() - 1, int(max_seqlen)
+    return total, H_q, H_kv, D, cu_seqlens.numel() - 1, _int32(max_seqlen)
 
 
 def ring_attn_fwd_varlen(q, k, v, cu_seqlens, max_seqlen, P, causal, scale=None,
@@ -588,8 +595,8 @@ def ring_attn_fwd_window(q, k, v, P, window, n_sink=0, scale=None, order="contig
             lse = torch.empty(B, H_q, S, device=q.device, dtype=torch.float32)
     sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
     st = lib.ring_attn_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H_q, H_kv, S,
-                                  D, P, int(window), int(n_sink), sc, code, ORDERS[order],
-                                  _ptr(dev_status), _stream(stream))
+                                  D, _int32(P), _int32(window), _int32(n_sink), sc, code,
+                                  ORDERS[order], _ptr(dev_status), _stream(stream))
     _check(st, "ring_attn_fwd_window")
     return out, lse
 
@@ -616,8 +623,8 @@ def ring_attn_fwd_window_varlen(q, k, v, cu_seqlens, max_seqlen, P, window, n_si
             lse = torch.empty(H_q, total, device=q.device, dtype=torch.float32)
     sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
     st = lib.ring_attn_fwd_window_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                                         _ptr(cu_seqlens), n, total, mx, H_q, H_kv, D, P,
-                                         int(window), int(n_sink), sc, code, ORDERS[order],
+                                         _ptr(cu_seqlens), n, total, mx, H_q, H_kv, D, _int32(P),
+                                         _int32(window), _int32(n_sink), sc, code, ORDERS[order],
                                          _ptr(dev_status), _stream(stream))
     _check(st, "ring_attn_fwd_window_varlen")
     return out, lse
@@ -629,8 +636,9 @@ def bwd_window_workspace_bytes(B, H_q, H_kv, S, D, P, window, n_sink=0, order="c
     sequences of at most S tokens, ``varlen``)."""
     lib = load()
     n = ctypes.c_size_t()
-    _check(lib.ring_attn_bwd_window_workspace(B, H_q, H_kv, S, D, P, int(window), int(n_sink),
-                                              ORDERS[order], int(bool(varlen)), ctypes.byref(n)),
+    sizes = map(_int32, (B, H_q, H_kv, S, D, P, window, n_sink))
+    _check(lib.ring_attn_bwd_window_workspace(*sizes, ORDERS[order], int(bool(varlen)),
+                                              ctypes.byref(n)),
            "ring_attn_bwd_window_workspace")
     return n.value
 
@@ -666,8 +674,8 @@ def ring_attn_bwd_window(q, k, v, out, lse, dout, P, window, n_sink=0, scale=Non
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
     st = lib.ring_attn_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
-                                  _ptr(dq), _ptr(dk), _ptr(dv), B, H_q, H_kv, S, D, P,
-                                  int(window), int(n_sink), sc, code, ORDERS[order],
+                                  _ptr(dq), _ptr(dk), _ptr(dv), B, H_q, H_kv, S, D, _int32(P),
+                                  _int32(window), _int32(n_sink), sc, code, ORDERS[order],
                                   _ptr(workspace), workspace.numel(), _ptr(dev_status),
                                   _stream(stream))
     _check(st, "ring_attn_bwd_window")
@@ -704,8 +712,8 @@ def ring_attn_bwd_window_varlen(q, k, v, out, lse, dout, cu_seqlens, max_seqlen,
     sc = float(scale) if scale is not None else 1.0 / math.sqrt(D)
     st = lib.ring_attn_bwd_window_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
                                          _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
-                                         _ptr(cu_seqlens), n, total, mx, H_q, H_kv, D, P,
-                                         int(window), int(n_sink), sc, code, ORDERS[order],
+                                         _ptr(cu_seqlens), n, total, mx, H_q, H_kv, D, _int32(P),
+                                         _int32(window), _int32(n_sink), sc, code, ORDERS[order],
                                          _ptr(workspace), workspace.numel(), _ptr(dev_status),
                                          _stream(stream))
     _check(st, "ring_attn_bwd_window_varlen")
@@ -893,8 +901,8 @@ def kv4_attn_workspace_bytes(B, S_q, H_q, H_kv, D, C, max_len=None, window=0, n_
                              with_score=False):
     """Bytes of device workspace ``kv4_attn`` needs for these sizes."""
     n = ctypes.c_size_t()
-    _check(load().kv4_attn_workspace(B, S_q, H_q, H_kv, D, C, C if max_len is None else max_len,
-                                     window, n_sink, 1 if with_score else 0, ctypes.byref(n)),
+    sizes = map(_int32, (B, S_q, H_q, H_kv, D, C, C if max_len is None else max_len, window, n_sink))
+    _check(load().kv4_attn_workspace(*sizes, 1 if with_score else 0, ctypes.byref(n)),
            "kv4_attn_workspace")
     return n.value
 
@@ -918,8 +926,8 @@ def kv4_attn(q, cache, lens, max_len=None, window=0, n_sink=0, scale=None, out=N
     if len(shape) != 4 or shape[0] != B or shape[3] != D:
         raise ValueError("q must be [B, S_q, H_q, D] matching the cache")
     _, S_q, H_q, _ = shape
-    max_len = C if max_len is None else int(max_len)
-    window, n_sink = int(window), int(n_sink)
+    max_len = C if max_len is None else _int32(max_len)
+    window, n_sink = _int32(window), _int32(n_sink)
     _like(out, "out", shape, q.dtype)
     _like(lse, "lse", (B, H_q, S_q), torch.float32)
     _like(score, "score", (B, H_kv, C), torch.float32)
@@ -964,7 +972,7 @@ def kv4_evict(cache, score, lens, budget, n_sink=0, n_recent=0, dst=None, dst_sc
     torch = _T or _import_torch()
     lib = load()
     B, H_kv, C, D = cache.dims
-    budget, n_sink, n_recent = int(budget), int(n_sink), int(n_recent)
+    budget, n_sink, n_recent = int(budget), _int32(n_sink), _int32(n_recent)
     if budget <= 0:
         raise ValueError("budget must be positive")
     C_dst = -(-budget // 16) * 16
@@ -972,6 +980,8 @@ def kv4_evict(cache, score, lens, budget, n_sink=0, n_recent=0, dst=None, dst_sc
         dB, dH, C_dst, dD = dst.dims
         if (dB, dH, dD) != (B, H_kv, D):
             raise ValueError("dst must have the cache's B, H_kv and D")
+    if budget > min(C_dst, 0x7fffffff):
+        _check(RA_ERR_RANGE, "kv4_evict")
     _like(score, "score", (B, H_kv, C), torch.float32)
     _like(dst_score, "dst_score", (B, H_kv, C_dst), torch.float32)
     _like(kept, "kept", (B, H_kv, budget), torch.int32)
