@@ -867,13 +867,14 @@ def kv4_append(cache, k, v, start, n_new=None, dev_status=None, stream=None):
 
 def kv4_read(cache, start, T, dtype=None, k=None, v=None, dev_status=None, stream=None):
     """The values (k, v) [B, T, H_kv, D] of slots start[b] ... start[b] + T - 1
-    (start None: from slot 0), bf16 unless ``dtype`` or given tensors say
+    (start None: from slot 0), bf16 unless ``dtype`` or a given k or v says
     float32."""
     torch = _T or _import_torch()
     lib = load()
     B, H_kv, C, D = cache.dims
     if dtype is None:
-        dtype = torch.bfloat16 if k is None else k.dtype
+        given = k if k is not None else v
+        dtype = torch.bfloat16 if given is None else given.dtype
     code = _dtype_code(dtype)
     T = int(T)
     if T <= 0:
