@@ -57,7 +57,11 @@
 // bits, brought into its range by a power of two that each row keeps for each
 // group: the largest product of the row's own met so far becomes 1 or more. A
 // weight is off by at most 2^-11 of itself, or 2^-25 of the group's largest where
-// it is a subnormal half. Sums are float32. Nothing of this is shared between
+// it is a subnormal half. Sums are float32, but for one cut: the matrix unit lines
+// products up by their operands' exponents, a subnormal's being its type's least,
+// so what lies below 2^-16 (high nibbles 2^-20) of the largest weight of 16 slots
+// falls off a product with a code (measured on two slots, one of them with the
+// code 8 and so without a product of its own). Nothing of this is shared between
 // rows: what a row does not see (a later drafted token's infinite value, a slot
 // that another row's window still holds) changes no bit of its results.
 #include <cuda_bf16.h>
@@ -84,7 +88,8 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kRescaleLog2 = 4;           // p stays below 2^4
 constexpr int kFlush = 8;
 constexpr int kLiftMax = 112;             // p 2^112 is finite
-constexpr int kWeightLog2 = 15;           // weights stay below 2^15, in half's range
+constexpr int kWeightLog2 = 13;           // weights stay below 2^13; half ends at 2^16, but
+                                          // bounds on logits past 2^24 are rounded
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float k2P24 = 16777216.f, k2Pm24 = 1.f / k2P24;
 
