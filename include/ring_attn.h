@@ -374,7 +374,8 @@ ra_status ring_attn_bwd_ulysses(const void* q, const void* k, const void* v,
  * S * window. dtype RA_BF16 or RA_F32; no visit log. Errors as
  * ring_attn_fwd_ex.
  * Keys and values must be finite where a query does not see them, too: a
- * hidden key has weight 0, and 0 times an infinity is not a number.
+ * hidden key has weight 0, and 0 times an infinity is not a number (in the
+ * backward so must queries, out and dout).
  * A row that sees a NaN score has NaN in out and in lse.
  * ring_attn_fwd_window_varlen - the same for packed sequences (conventions of
  * ring_attn_fwd_varlen): windows and first tokens are each sequence's own. A
@@ -555,9 +556,11 @@ ra_status kv4_attn_workspace(int B, int S_q, int H_q, int H_kv, int D, int C,
  *     q, out  [B, S_q, H_q, D] bfloat16    lse  [B, H_q, S_q] float32 or NULL
  * score: NULL, or float32 [B, H_kv, C]: every slot's attention weight, summed
  * over the queries and the heads of its group, is ADDED to it.
- * dtype RA_BF16. scale <= 0 means 1 / sqrt(D). The workspace is the caller's,
- * 16-byte aligned; its contents do not matter. Calls that may overlap on the
- * GPU need workspaces of their own. Results repeat bit for bit.
+ * dtype RA_BF16; queries of up to 2^90 in magnitude and logits of up to 2^28
+ * (beyond them results may not be finite). scale <= 0 means 1 / sqrt(D). The
+ * workspace is the caller's, 16-byte aligned; its contents do not matter. Calls
+ * that may overlap on the GPU need workspaces of their own. Results repeat bit
+ * for bit.
  * Errors: RA_ERR_NULL, RA_ERR_SHAPE, RA_ERR_HEADDIM, RA_ERR_ALIGN,
  * RA_ERR_DTYPE, RA_ERR_RANGE (max_len, window, n_sink, sizes), RA_ERR_BUFFER,
  * RA_ERR_DEVICE, RA_ERR_LAUNCH.

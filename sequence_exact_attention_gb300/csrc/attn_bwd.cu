@@ -38,8 +38,9 @@
 // wave's idle multiprocessors. (Windows make both grids many equal, short
 // CTAs, whose last waves are mostly idle.) It waits for that grid at its own
 // end only, so that what follows on the stream finds both done.
-// Measured with windows: 32 heads on 8, D = 128, S = 16384, window 2048 1.43 ms
-// (prep 46 us, dK/dV 685, dQ 650, joins 10), 900 TFLOP/s of 10 D a visible pair;
+// Measured with windows, replayed from a graph: 32 heads on 8, D = 128, S = 16384,
+// window 2048 1.44 ms (one by one under ncu: prep 47 us, dK/dV 698, dQ 676, joins
+// 9), 900 TFLOP/s of 10 D a visible pair;
 // two sequences of 4096, 16 heads, window 1024 259 us. (dQ with the first tokens'
 // tile as 32 columns, dK/dV launched early after prep, the join after dQ: no change.)
 // The two gradient kernels both recompute S and dP; in exchange neither needs
@@ -452,12 +453,6 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (
 }
 
 // ------------------------------------------------------------------ dK, dV
-// Per visit the tensor cores run S^T, dP^T, dV, dK in that order and the
-// compute warps run two passes: P^T (from S^T) while dP^T is computed, then
-// dS^T (from dP^T and the P^T kept in registers) while dV is accumulated.
-// Warp w covers key rows 32 (w mod 4) .. +31 and query columns 64 (w / 4)
-// .. +63; its bf16 P^T and dS^T go into the first 32 columns of its own
-// S^T and dP^T column ranges, so no warp writes columns another one reads.
 // Places of the shares of a windowed call's key tiles in its parts: of tile
 // `ordinal` with first tokens, of tile kt, and how many there are.
 __device__ __forceinline__ long long sink_shares(const WinGeometry& g, int bhk, int ordinal) {
@@ -471,6 +466,12 @@ __device__ __forceinline__ long long all_shares(const WinGeometry& g) {
   return head_shares(g, g.head_splits > 1 ? g.B * g.H_kv : 0, 0);
 }
 
+// Per visit the tensor cores run S^T, dP^T, dV, dK in that order and the
+// compute warps run two passes: P^T (from S^T) while dP^T is computed, then
+// dS^T (from dP^T and the P^T kept in registers) while dV is accumulated.
+// Warp w covers key rows 32 (w mod 4) .. +31 and query columns 64 (w / 4)
+// .. +63; its bf16 P^T and dS^T go into the first 32 columns of its own
+// S^T and dP^T column ranges, so no warp writes columns another one reads.
 template <int D, bool kVarlen, class G = Geometry>
 __global__ void __launch_bounds__(kThreads, 1)
 bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -1406,6 +1407,8 @@ ra_status launch_attn_bwd(const Geometry& g, const void* q, const void* k, const
 // than keep the multiprocessors busy four times over (a share costs 2 * 128 * D
 // floats).
 long long plan_window_bwd(WinGeometry* g) {
+  // a GB300's multiprocessors: a constant, as the workspace's size has to be the
+  // same where there is no device to ask
   constexpr long long kSms = 152, kMaxCtas = 4 * kSms, kMaxParts = 8 * kSms;
   const int grp = g->H_q / g->H_kv;
   const long long n_kt = g->nt, ctas = g->B * (long long)g->H_kv * n_kt;

@@ -92,8 +92,8 @@ attn_f32_window_kernel(const WinGeometry gp, const float* __restrict__ q,
       x = *reinterpret_cast<const float4*>(q + off);
     *reinterpret_cast<float4*>(Qs + r * S::kStride + 4 * c) = x;
   }
-  // rows of the tile past its keys are left as they are: masked scores, and
-  // weights of 0 that meet values of 0 (below)
+  // rows of the tile past its keys are zeroed: their scores are masked, and their
+  // weights of 0 would meet what the buffer held before, where NaN survives them
   auto fetch = [&](const KvTile& t, int buf) {
     float* Ks = smem + S::kBuf + buf * S::kBufFloats;
     float* Vs = Ks + kK * S::kStride;

@@ -324,8 +324,9 @@ __device__ __forceinline__ bool row_has_lse(float l) {
 // stay visible. The walk then covers only the key tiles that some row of the
 // block sees, in position order (window_iter.cuh), and a score is also masked
 // where its key lies between the first tokens and the row's window.
-// Measured (D = 128): S = 32768, 32 heads on 8, window 4096 1.47 ms, 1400 TFLOP/s
-// of the pairs that see each other; S = 16384, window 2048 455 us, 1135; two
+// Measured, replayed from a graph (of the first, a call among others takes 1.57
+// ms; D = 128): S = 32768, 32 heads on 8, window 4096 1.48 ms, 1400 TFLOP/s of the
+// pairs that see each other; S = 16384, window 2048 459 us, 1125; two
 // sequences of 4096, 16 heads, window 1024 79 us, 765. What the tiles' edges and
 // the first tokens' tile hold besides makes the work 1.09, 1.18 and 1.34 times
 // those pairs. (Leaving out, for each query tile, the key tiles that only the

@@ -23,7 +23,7 @@
 // at 131072 slots), and of the unrounded weights with their roundings times 8
 // (1.4e-3). (Making c - 8 from each pair of codes took two operations more a
 // pair: 340 instead of 285 instructions on 16 slots; a product with the
-// constant for every 16 dimensions 231 instead of 227 us at the size below.)
+// constant for every 16 dimensions took 4 us more at the size below.)
 //
 // What bounds it: the cache's bytes, 144 a slot and head at D = 128, read
 // once. A row has 2 * 2 * D flops a slot, some 4 to 16 rows share a slot, far
@@ -45,11 +45,13 @@
 // repeat bit for bit.
 //
 // Measured, 8 sequences x 8 key/value heads x 131072 slots, D = 128, 32 query
-// heads: 227 us, 5.3 TB/s of the 6.8 of a copy (loads alone 173 us, arithmetic
-// alone 199 us; 59 % of the issue slots, 55 % of the integer pipe). 16 ragged
-// sequences of up to 8192 slots, with scores: 44 us, the chunks, then the join,
-// then the scores. (One wave of CTAs, each an equal run of tiles across the
-// sequences' borders, measured 236 instead of 227 and 43.5 instead of 46 us.)
+// heads, replayed from a graph: 231 us, 5.2 TB/s of the 6.8 of a copy (59 % of the
+// issue slots, 55 % of the integer pipe). With one power of two a warp in place of
+// each row's own (Roundings, below) it was 227: loads alone 173 us, arithmetic
+// alone 199 us. 16 ragged sequences of up to 8192 slots, with scores: 45 us, the
+// chunks, then the join, then the scores. (One wave of CTAs, each an equal run of
+// tiles across the sequences' borders, measured 236 instead of 227 and 43.5
+// instead of 46 us then.)
 //
 // Roundings: q is scaled by a power of two a row and becomes half precision
 // (exact for bf16 values down to 2^-17 of the row's largest; queries beyond
@@ -63,7 +65,9 @@
 // falls off a product with a code (measured on two slots, one of them with the
 // code 8 and so without a product of its own). Nothing of this is shared between
 // rows: what a row does not see (a later drafted token's infinite value, a slot
-// that another row's window still holds) changes no bit of its results.
+// that another row's window still holds) changes no bit of its results. (Asking
+// of the products themselves whether one leaves the range, by a second vote a
+// tile, instead of the scales' bound: 251 instead of 243 us a call.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -891,7 +895,9 @@ ra_status kv4_attn_plan(Kv4AttnArgs* a, bool score, size_t* bytes) {
                            ((long long)a->window + a->S_q - 1 + kKv4Tile - 1) / kKv4Tile + 1;
     if (seen < tiles) tiles = seen;
   }
-  const long long wave = 152 * (a->rows == 8 ? 4 : 2);       // CTAs resident at a time
+  // CTAs resident at a time on a GB300: a constant, as the workspace's size has to
+  // be the same where there is no device to ask
+  const long long wave = 152 * (a->rows == 8 ? 4 : 2);
   long long best = 1, best_full = 0;                        // chunks, and what they fill of their waves
   for (int w = 2; w >= 1; --w) {
     const long long n = wave * w / blocks;
