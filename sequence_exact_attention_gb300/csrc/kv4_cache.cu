@@ -11,8 +11,10 @@
 // holds the range of any input. A group that holds an infinity or a NaN reads
 // back as NaN.
 //
-// Both kernels are bound by the bytes they move, once the instructions a value
-// are few (below). Eight lanes share a group, eight values each: the float side
+// Reading is bound by the bytes moved, once the instructions a value are few
+// (below); appending by its instructions, an IEEE division a value among them: a
+// prompt of 8 x 8192 tokens of 8 heads, D = 128, 152 us from bfloat16 (2.3 TB/s) and
+// 150 us from float32 (4.1 TB/s). Eight lanes share a group, eight values each: the float side
 // moves in 16-byte vectors, a group's codes are one 32-byte sector. Measured,
 // reading 4096 slots of 64 heads, D = 128, as bfloat16: 31 us, 5.6 TB/s (with two
 // divisions a thread and float32 arithmetic 33 us, 76 % of the issue slots).
