@@ -78,8 +78,8 @@ typedef enum {
   RA_ERR_DEVICE = 6,   /* current device is not compute capability 10.3            */
   RA_ERR_LAUNCH = 7,   /* CUDA runtime error while preparing or launching          */
   RA_ERR_TIMEOUT = 8,  /* a device-side bounded wait expired (dev_status only)     */
-  RA_ERR_BUFFER = 9,   /* a caller buffer is too small; 4-bit cache: one that a
-                          call writes overlaps another of its buffers            */
+  RA_ERR_BUFFER = 9,   /* a caller buffer is too small; caches: one that a call
+                          writes overlaps another of its buffers                 */
   RA_ERR_RANGE = 10,   /* a size overflows 32-bit indexing, or step out of range;
                           in dev_status (checked build only): a device index out
                           of its tensor's range                                   */
@@ -87,7 +87,8 @@ typedef enum {
                           built-in array holds (ring_attn_bwd_noalloc)           */
 } ra_status;
 
-typedef enum { RA_BF16 = 0, RA_F32 = 1 } ra_dtype;
+/* RA_E4M3 (8 bits) is a type of pages only. */
+typedef enum { RA_BF16 = 0, RA_F32 = 1, RA_E4M3 = 2 } ra_dtype;
 typedef enum { RA_ORDER_CONTIGUOUS = 0, RA_ORDER_ZIGZAG = 1 } ra_order;
 
 /* Classes of a (query set, key set) pair under the causal rule j <= i. */
@@ -593,12 +594,119 @@ ra_status kv4_evict(const void* k_codes, const void* k_meta, const void* v_codes
                     int B, int H_kv, int D, int C, int C_dst, int budget,
                     int n_sink, int n_recent, int* dev_status, void* stream);
 
+/*
+ * The paged key/value cache: what served sequences have attended to so far, in
+ * pages that the caller hands out from one pool, in bfloat16 or 8 bits. The pages
+ * have no counterpart in the sources; it continues the forward above (the same
+ * attention, the same lse, so that its results merge with attn_lse_merge).
+ *
+ * A page holds `page` slots (16, 32, 64 or 128) of every key/value head; a slot is
+ * one token's key row and value row of D values (64 or 128):
+ *     k, v               [n_pages, H_kv, page, D]   bfloat16 (RA_BF16), or e4m3
+ *                        codes (RA_E4M3)
+ *     k_scale, v_scale   [n_pages, H_kv, page]      RA_E4M3 only (else NULL): a
+ *                        byte b in 1..254 a row; a code c stands for c 2^(b - 127)
+ * all 16-byte aligned. Which page holds which slots is the caller's table, device
+ * int32 [B, width]: slot j of sequence b is row j % page of page
+ * table[b][j / page]. An entry outside [0, n_pages) is a page that is not there;
+ * only entries of slots that a call touches are read. Sequences may share pages
+ * that no call writes. Nothing here reads tables, lengths or offsets on the host,
+ * so a step can be captured into a graph and replayed while they change. A tensor
+ * that a call writes (its workspace too) may not overlap any other of the call's
+ * (RA_ERR_BUFFER).
+ */
+typedef struct {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  int n_pages, H_kv, page, D;
+  int dtype;                 /* RA_BF16 or RA_E4M3 */
+} ra_pages;
+
+/*
+ * paged_append - writes T tokens a sequence, k and v [B, T, H_kv, D] of `dtype`
+ * (RA_BF16 or RA_F32), to slots start[b], start[b] + 1, ... (start: device int32
+ * [B]). n_new: NULL, or device int32 [B]: only the first n_new[b] tokens of
+ * sequence b count. bfloat16 pages: each value rounded once. 8 bits: a row's
+ * scale is 2^e, e the least from -117 on with max |x| / 2^e <= 448 over its finite
+ * values, its codes e4m3(x / 2^e), half to even; an infinity or a NaN reads back
+ * as NaN, it alone. (What rounds to 2^128, from 1.9375 2^127 on, reads back as an
+ * infinity.) A slot without a page is not written and sets RA_ERR_RANGE in
+ * `dev_status` (device int, may be NULL). The slots that a call writes have to be
+ * different ones.
+ * paged_append_varlen - the same of packed tokens: k, v [total, H_kv, D], sequence
+ * b's in rows [cu_seqlens[b], cu_seqlens[b + 1]) (device int32 [n_seq + 1], not
+ * decreasing); rows that no sequence has are passed over.
+ * Errors: RA_ERR_NULL, RA_ERR_SHAPE, RA_ERR_HEADDIM, RA_ERR_ALIGN, RA_ERR_DTYPE,
+ * RA_ERR_RANGE (sizes), RA_ERR_BUFFER, RA_ERR_DEVICE, RA_ERR_LAUNCH.
+ */
+ra_status paged_append(const ra_pages* pages, const int* table, int width, const void* k,
+                       const void* v, const int* start, const int* n_new, int B, int T,
+                       int dtype, int* dev_status, void* stream);
+ra_status paged_append_varlen(const ra_pages* pages, const int* table, int width,
+                              const void* k, const void* v, const int* start,
+                              const int* cu_seqlens, int n_seq, int total, int dtype,
+                              int* dev_status, void* stream);
+
+/*
+ * paged_read - the values of slots start[b] ... start[b] + T - 1 (start NULL: from
+ * slot 0), as k and v [B, T, H_kv, D] of `dtype` (either may be NULL). What 8 bits
+ * hold is a bfloat16 number. A slot without a page gives zeros and sets
+ * RA_ERR_RANGE in `dev_status`.
+ */
+ra_status paged_read(const ra_pages* pages, const int* table, int width, const int* start,
+                     void* k, void* v, int B, int T, int dtype, int* dev_status,
+                     void* stream);
+
+/* Bytes of workspace that paged_attn needs for these sizes, and (varlen = 1, B =
+ * n_seq, S_q = max_seqlen) paged_attn_varlen of `total` rows; host only. Of the
+ * pages their sizes and type count. */
+ra_status paged_attn_workspace(const ra_pages* pages, int B, int S_q, int total, int H_q,
+                               int max_len, int window, int n_sink, int varlen,
+                               size_t* bytes);
+
+/*
+ * paged_attn - attention of S_q new tokens a sequence (one in plain decoding) over
+ * its slots, which already hold them (append first).
+ * lens: device int32 [B], slots in use, the new ones included (clamped to
+ * [0, max_len]); max_len in [1, width * page] bounds them and sizes the launch.
+ * Query t of sequence b is at slot p = lens[b] - S_q + t and sees the slots j <= p;
+ * with window > 0 only those with j > p - window or j < n_sink (window 0: no
+ * window, n_sink is ignored). Head h reads key/value head h / (H_q / H_kv); H_q /
+ * H_kv is 128 at most. A row that sees no slot gets out = 0, lse = -inf.
+ *     q, out  [B, S_q, H_q, D] bfloat16    lse  [B, H_q, S_q] float32 or NULL
+ * paged_attn_varlen - the same of packed tokens, a prompt's pieces of different
+ * lengths and single tokens side by side: sequence b's are rows [cu_seqlens[b],
+ * cu_seqlens[b + 1]) of q, out [total, H_q, D], lse [H_q, total]; max_seqlen bounds
+ * their numbers. Malformed offsets are brought into range; rows that no sequence
+ * has are left as they were.
+ * Slots past lens[b] and those that no row of the call sees may hold anything,
+ * NaN included. A slot whose page is not there is not seen, and sets RA_ERR_RANGE
+ * in `dev_status` where a row would have seen it.
+ * dtype RA_BF16. scale <= 0 means 1 / sqrt(D). The workspace is the caller's,
+ * 16-byte aligned; its contents do not matter. Calls that may overlap on the GPU
+ * need workspaces of their own. Results repeat bit for bit.
+ * Errors: as paged_append, RA_ERR_RANGE for max_len, window, n_sink, too.
+ */
+ra_status paged_attn(const void* q, const ra_pages* pages, const int* table, int width,
+                     const int* lens, void* out, float* lse, int B, int S_q, int H_q,
+                     int max_len, int window, int n_sink, float scale, int dtype,
+                     void* workspace, size_t workspace_bytes, int* dev_status,
+                     void* stream);
+ra_status paged_attn_varlen(const void* q, const ra_pages* pages, const int* table,
+                            int width, const int* lens, const int* cu_seqlens, void* out,
+                            float* lse, int n_seq, int total, int max_seqlen, int H_q,
+                            int max_len, int window, int n_sink, float scale, int dtype,
+                            void* workspace, size_t workspace_bytes, int* dev_status,
+                            void* stream);
+
 /* Human-readable text of a status; never NULL. */
 const char* ring_attn_strerror(int status);
 
 /* Library ABI version (major * 100 + minor); 103 adds the backward, the
  * packed variable-length and the Ulysses-layout entry points, 104 the 4-bit
- * key/value cache and the windowed entry points. */
+ * key/value cache and the windowed entry points, 105 the paged cache. */
 int ring_attn_version(void);
 
 #ifdef __cplusplus

@@ -30,6 +30,8 @@ Everything here is float64 NumPy, written to be read against the pages:
   a sliding window and first tokens that stay visible, and its gradients.
 * ``kv4``               - the 4-bit key/value cache: quantising, what codes
   stand for, attention of a few tokens over a cache, eviction.
+* ``paged``             - the paged key/value cache: slots and pages, 8-bit
+  rows, attention of packed tokens over their slots.
 * ``tile_visits``       - expands the chunk-level schedule into the sequence of
   fixed-size key tiles a tiled kernel must visit, classifying every tile by
   brute force over its (query, key) pairs.
@@ -50,6 +52,7 @@ from .ring import ring_attention
 from .backward import attention_backward, ring_attention_backward, backward_rows
 from .varlen import attention_varlen, attention_backward_varlen
 from . import kv4
+from . import paged
 from .window import (window_attention, window_attention_varlen, window_backward,
                      window_backward_varlen)
 from .ulysses import (ulysses_attention, to_sequence_shards, from_sequence_shards,
@@ -60,7 +63,7 @@ __all__ = [
     "lse_merge", "lse_merge_n",
     "SKIP", "FULL", "PARTIAL", "ORDER_CONTIGUOUS", "ORDER_ZIGZAG",
     "rank_segments", "ring_schedule", "schedule_table", "tile_visits",
-    "ring_attention", "kv4",
+    "ring_attention", "kv4", "paged",
     "window_attention", "window_attention_varlen", "window_backward", "window_backward_varlen",
     "attention_backward", "ring_attention_backward", "backward_rows",
     "attention_varlen", "attention_backward_varlen",

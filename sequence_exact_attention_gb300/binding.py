@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libringattn.so")
 LIBRARIES = {"release": LIB_PATH,
              "debug": os.path.join(_HERE, "_lib", "libringattn_debug.so")}
 
-RA_BF16, RA_F32 = 0, 1
+RA_BF16, RA_F32, RA_E4M3 = 0, 1, 2
 ORDERS = {"contiguous": 0, "zigzag": 1}
 PLAN_COLS = 9
 MERGE_MAX_N = 16
@@ -39,6 +39,8 @@ EXPORTS = ("ring_attn_fwd", "ring_attn_fwd_ex", "ring_attn_visit_log_len",
            "ring_attn_bwd_window_varlen",
            "attn_lse_merge", "attn_lse_merge_n",
            "kv4_append", "kv4_read", "kv4_attn_workspace", "kv4_attn", "kv4_evict",
+           "paged_append", "paged_append_varlen", "paged_read", "paged_attn_workspace",
+           "paged_attn", "paged_attn_varlen",
            "ring_attn_plan",
            "ring_attn_expiry_test", "ring_attn_strerror", "ring_attn_version")
 
@@ -142,6 +144,20 @@ def load():
     lib.kv4_attn.argtypes = [vp] * 9 + [c_int] * 9 + [c_float, c_int, vp, ctypes.c_size_t, vp, vp]
     lib.kv4_evict.restype = c_int
     lib.kv4_evict.argtypes = [vp] * 13 + [c_int] * 8 + [vp, vp]
+    lib.paged_append.restype = c_int
+    lib.paged_append.argtypes = [vp, vp, c_int] + [vp] * 4 + [c_int] * 3 + [vp, vp]
+    lib.paged_append_varlen.restype = c_int
+    lib.paged_append_varlen.argtypes = [vp, vp, c_int] + [vp] * 4 + [c_int] * 3 + [vp, vp]
+    lib.paged_read.restype = c_int
+    lib.paged_read.argtypes = [vp, vp, c_int] + [vp] * 3 + [c_int] * 3 + [vp, vp]
+    lib.paged_attn_workspace.restype = c_int
+    lib.paged_attn_workspace.argtypes = [vp] + [c_int] * 8 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.paged_attn.restype = c_int
+    lib.paged_attn.argtypes = ([vp, vp, vp, c_int] + [vp] * 3 + [c_int] * 6 +
+                               [c_float, c_int, vp, ctypes.c_size_t, vp, vp])
+    lib.paged_attn_varlen.restype = c_int
+    lib.paged_attn_varlen.argtypes = ([vp, vp, vp, c_int] + [vp] * 4 + [c_int] * 7 +
+                                      [c_float, c_int, vp, ctypes.c_size_t, vp, vp])
     lib.ring_attn_plan.restype = c_int
     lib.ring_attn_plan.argtypes = [c_int, c_int, c_int, c_int, ip, ctypes.c_size_t]
     lib.ring_attn_expiry_test.restype = c_int
@@ -1008,6 +1024,266 @@ def kv4_evict(cache, score, lens, budget, n_sink=0, n_recent=0, dst=None, dst_sc
                        n_sink, n_recent, _ptr(dev_status), _stream(stream))
     _check(st, "kv4_evict")
     return dst, dst_score, dst_lens, kept
+
+
+# ------------------------------------------------------------------ paged key/value cache
+
+class _Pages(ctypes.Structure):
+    """ra_pages of ``include/ring_attn.h``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("H_kv", ctypes.c_int),
+                ("page", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class PagedCache(tuple):
+    """A pool of pages of keys and values (format: ``include/ring_attn.h``):
+    k and v [n_pages, H_kv, page, D], bfloat16 or float8_e4m3fn, the latter with
+    k_scale and v_scale uint8 [n_pages, H_kv, page].
+
+    A tuple of its tensors, whose shapes, dtypes and layout are checked here,
+    once, and not again by the calls that take the cache.
+    """
+
+    def __new__(cls, k, v, k_scale=None, v_scale=None):
+        torch = _T or _import_torch()
+        quant = k.dtype == torch.float8_e4m3fn
+        if not quant and k.dtype != torch.bfloat16:
+            raise ValueError(f"pages must be bfloat16 or float8_e4m3fn, got {k.dtype}")
+        if k.dim() != 4:
+            raise ValueError("k must be [n_pages, H_kv, page, D]")
+        if quant != (k_scale is not None) or quant != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to pages of 8 bits")
+        shape = tuple(k.shape)
+        _like(v, "v", shape, k.dtype)
+        _like(k_scale, "k_scale", shape[:3], torch.uint8)
+        _like(v_scale, "v_scale", shape[:3], torch.uint8)
+        parts = (k, v, k_scale, v_scale) if quant else (k, v)
+        self = super().__new__(cls, parts)
+        self.dims = shape
+        self.dtype = k.dtype
+        self.device = dev = k.get_device()
+        for t, n in zip(parts, ("k", "v", "k_scale", "v_scale")):
+            if not t.is_contiguous():
+                raise ValueError(f"{n} must be contiguous")
+            if t.get_device() != dev:
+                raise ValueError("the cache's tensors are on several devices")
+        if max(shape[:3]) > 0x7fffffff:
+            _check(RA_ERR_RANGE, "PagedCache")
+        self._c = _Pages(*map(_ptr, (k, v, k_scale, v_scale)), *shape, RA_E4M3 if quant else RA_BF16)
+        self._ref = ctypes.addressof(self._c)
+        return self
+
+    k = property(lambda self: self[0])
+    v = property(lambda self: self[1])
+    k_scale = property(lambda self: self[2] if len(self) > 2 else None)
+    v_scale = property(lambda self: self[3] if len(self) > 2 else None)
+
+
+def paged_cache(n_pages, H_kv, page, D, dtype=None, device="cuda"):
+    """A zeroed pool of ``n_pages`` pages of ``page`` slots (16, 32, 64 or 128),
+    in bfloat16 or, with ``dtype=torch.float8_e4m3fn``, 8 bits."""
+    torch = _T or _import_torch()
+    if D not in (64, 128) or page not in (16, 32, 64, 128) or n_pages <= 0 or H_kv <= 0:
+        raise ValueError("D must be 64 or 128, page 16, 32, 64 or 128, n_pages and H_kv positive")
+    dtype = torch.bfloat16 if dtype is None else dtype
+    shape = (n_pages, H_kv, page, D)
+    parts = [torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)]
+    if dtype == torch.float8_e4m3fn:
+        parts += [torch.full(shape[:3], 127, dtype=torch.uint8, device=device) for _ in range(2)]
+    return PagedCache(*parts)
+
+
+def _table(table, B):
+    """The width of a table int32 [B, width]."""
+    if table.dim() != 2:
+        raise ValueError("table must be int32 [B, width]")
+    _like(table, "table", (B, table.shape[1]), (_T or _import_torch()).int32)
+    return table.shape[1]
+
+
+def paged_append(cache, table, k, v, start, n_new=None, dev_status=None, stream=None):
+    """Writes k, v [B, T, H_kv, D] (bf16 or float32) to slots start[b],
+    start[b] + 1, ... of the sequences whose pages ``table`` int32 [B, width]
+    names; with ``n_new`` int32 [B] only the first n_new[b] tokens of a padded
+    batch. start: int32 [B]. All CUDA tensors."""
+    lib = load()
+    _, H_kv, _, D = cache.dims
+    if k.dim() != 4:
+        raise ValueError("k must be [B, T, H_kv, D]")
+    B, T = k.shape[:2]
+    _like(k, "k", (B, T, H_kv, D), k.dtype)
+    _like(v, "v", (B, T, H_kv, D), k.dtype)
+    width = _table(table, B)
+    _ints(start, "start", B)
+    _ints(n_new, "n_new", B)
+    _int_buffer(dev_status, "dev_status", 1)
+    code = _dtype_code(k.dtype)
+    _with_cache(cache, (table, k, v, start, n_new, dev_status),
+                ("table", "k", "v", "start", "n_new", "dev_status"))
+    st = lib.paged_append(cache._ref, table.data_ptr(), width, k.data_ptr(), v.data_ptr(),
+                          start.data_ptr(), _ptr(n_new), B, T, code, _ptr(dev_status),
+                          _stream(stream))
+    _check(st, "paged_append")
+
+
+def paged_append_varlen(cache, table, k, v, cu_seqlens, start, dev_status=None, stream=None):
+    """``paged_append`` of packed tokens k, v [total, H_kv, D]: sequence b's are
+    rows [cu_seqlens[b], cu_seqlens[b + 1]) (int32 [B + 1], CUDA)."""
+    torch = _T or _import_torch()
+    lib = load()
+    _, H_kv, _, D = cache.dims
+    if k.dim() != 3:
+        raise ValueError("k must be [total, H_kv, D]")
+    total = k.shape[0]
+    _like(k, "k", (total, H_kv, D), k.dtype)
+    _like(v, "v", (total, H_kv, D), k.dtype)
+    if cu_seqlens.dim() != 1 or cu_seqlens.dtype != torch.int32:
+        raise ValueError("cu_seqlens must be a 1-D int32 CUDA tensor")
+    B = cu_seqlens.numel() - 1
+    width = _table(table, B)
+    _ints(start, "start", B)
+    _int_buffer(dev_status, "dev_status", 1)
+    code = _dtype_code(k.dtype)
+    _with_cache(cache, (table, k, v, cu_seqlens, start, dev_status),
+                ("table", "k", "v", "cu_seqlens", "start", "dev_status"))
+    st = lib.paged_append_varlen(cache._ref, table.data_ptr(), width, k.data_ptr(), v.data_ptr(),
+                                 start.data_ptr(), cu_seqlens.data_ptr(), B, total, code,
+                                 _ptr(dev_status), _stream(stream))
+    _check(st, "paged_append_varlen")
+
+
+def paged_read(cache, table, start, T, dtype=None, k=None, v=None, dev_status=None, stream=None):
+    """The values (k, v) [B, T, H_kv, D] of slots start[b] ... start[b] + T - 1
+    (start None: from slot 0), bf16 unless ``dtype`` or a given k or v says
+    float32; zeros where ``table`` int32 [B, width] names no page."""
+    torch = _T or _import_torch()
+    lib = load()
+    _, H_kv, _, D = cache.dims
+    if dtype is None:
+        given = k if k is not None else v
+        dtype = torch.bfloat16 if given is None else given.dtype
+    code = _dtype_code(dtype)
+    T = int(T)
+    if T <= 0:
+        raise ValueError("T must be positive")
+    B = table.shape[0]
+    width = _table(table, B)
+    shape = (B, T, H_kv, D)
+    _like(k, "k", shape, dtype)
+    _like(v, "v", shape, dtype)
+    _ints(start, "start", B)
+    _int_buffer(dev_status, "dev_status", 1)
+    _with_cache(cache, (table, k, v, start, dev_status), ("table", "k", "v", "start", "dev_status"))
+    T = _int32(T)
+    with _on_stream(stream):
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=table.device)
+        if v is None:
+            v = torch.empty(shape, dtype=dtype, device=table.device)
+    st = lib.paged_read(cache._ref, table.data_ptr(), width, _ptr(start), k.data_ptr(),
+                        v.data_ptr(), B, T, code, _ptr(dev_status), _stream(stream))
+    _check(st, "paged_read")
+    return k, v
+
+
+# (a function of the sizes alone; asking the library costs as much as a launch)
+@functools.lru_cache(maxsize=256)
+def _paged_workspace(dims, quant, B, S_q, total, H_q, max_len, window, n_sink, varlen):
+    n = ctypes.c_size_t()
+    pages = _Pages(None, None, None, None, *dims, RA_E4M3 if quant else RA_BF16)
+    _check(load().paged_attn_workspace(ctypes.addressof(pages), B, S_q, total, H_q, max_len, window,
+                                       n_sink, varlen, ctypes.byref(n)), "paged_attn_workspace")
+    return n.value
+
+
+def paged_attn_workspace_bytes(cache, B, S_q, H_q, max_len, window=0, n_sink=0, total=None):
+    """Bytes of device workspace that ``paged_attn`` needs for these sizes; with
+    ``total``, ``paged_attn_varlen`` of B sequences of at most S_q new tokens in
+    ``total`` rows."""
+    torch = _T or _import_torch()
+    sizes = map(_int32, (B, S_q, 0 if total is None else total, H_q, max_len, window, n_sink))
+    return _paged_workspace(cache.dims, cache.dtype == torch.float8_e4m3fn, *sizes,
+                            int(total is not None))
+
+
+def _paged_attn(q, cache, table, lens, cu_seqlens, B, S_q, total, max_len, window, n_sink, scale,
+                out, lse, workspace, dev_status, stream):
+    """Both forms of the attention; ``cu_seqlens`` None: [B, S_q, H_q, D]."""
+    torch = _T or _import_torch()
+    lib = load()
+    D = cache.dims[3]
+    H_q = q.shape[-2]
+    width = _table(table, B)
+    max_len = width * cache.dims[2] if max_len is None else max_len
+    S_q, max_len, window, n_sink = _int32(S_q), _int32(max_len), _int32(window), _int32(n_sink)
+    lse_shape = (B, H_q, S_q) if cu_seqlens is None else (H_q, total)
+    _like(out, "out", q.shape, q.dtype)
+    _like(lse, "lse", lse_shape, torch.float32)
+    _ints(lens, "lens", B)
+    _int_buffer(dev_status, "dev_status", 1)
+    if workspace is not None and workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a uint8 tensor")
+    code = _dtype_code(q.dtype)
+    _with_cache(cache, (q, table, lens, cu_seqlens, out, lse, workspace, dev_status),
+                ("q", "table", "lens", "cu_seqlens", "out", "lse", "workspace", "dev_status"))
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            need = _paged_workspace(cache.dims, len(cache) > 2, B, S_q, total, H_q, max_len, window,
+                                    n_sink, int(cu_seqlens is not None))
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    sizes = (H_q, max_len, window, n_sink, 0.0 if scale is None else float(scale), code,
+             _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(dev_status),
+             _stream(stream))
+    if cu_seqlens is None:
+        st = lib.paged_attn(q.data_ptr(), cache._ref, table.data_ptr(), width, lens.data_ptr(),
+                            out.data_ptr(), lse.data_ptr(), B, S_q, *sizes)
+    else:
+        st = lib.paged_attn_varlen(q.data_ptr(), cache._ref, table.data_ptr(), width,
+                                   lens.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(),
+                                   lse.data_ptr(), B, total, S_q, *sizes)
+    _check(st, "paged_attn" if cu_seqlens is None else "paged_attn_varlen")
+    return out, lse
+
+
+def paged_attn(q, cache, table, lens, max_len=None, window=0, n_sink=0, scale=None, out=None,
+               lse=None, workspace=None, dev_status=None, stream=None):
+    """Attention of new tokens q [B, S_q, H_q, D] (bf16) over the slots that
+    ``table`` int32 [B, width] finds in the pages.
+
+    ``lens`` int32 [B] (CUDA) counts the slots in use, the S_q new tokens'
+    included; ``max_len`` (default: all that the table is wide) bounds it and
+    sizes the launch. ``window`` > 0 limits every query to its last ``window``
+    slots and the first ``n_sink``. Returns (out [B, S_q, H_q, D], lse
+    [B, H_q, S_q]). A ``workspace`` (uint8, ``paged_attn_workspace_bytes``) is
+    allocated here when not given; calls that may overlap need their own.
+    """
+    if q.dim() != 4 or q.shape[3] != cache.dims[3]:
+        raise ValueError("q must be [B, S_q, H_q, D] matching the cache")
+    B, S_q = q.shape[:2]
+    return _paged_attn(q, cache, table, lens, None, B, S_q, B * S_q, max_len, window, n_sink, scale,
+                       out, lse, workspace, dev_status, stream)
+
+
+def paged_attn_varlen(q, cache, table, lens, cu_seqlens, max_seqlen, max_len=None, window=0,
+                      n_sink=0, scale=None, out=None, lse=None, workspace=None, dev_status=None,
+                      stream=None):
+    """``paged_attn`` of packed tokens q [total, H_q, D]: sequence b's new ones,
+    at most ``max_seqlen``, are rows [cu_seqlens[b], cu_seqlens[b + 1]) (int32
+    [B + 1], CUDA): pieces of prompts behind what is cached, and single tokens.
+    Returns (out [total, H_q, D], lse [H_q, total])."""
+    torch = _T or _import_torch()
+    if q.dim() != 3 or q.shape[2] != cache.dims[3]:
+        raise ValueError("q must be [total, H_q, D] matching the cache")
+    if cu_seqlens.dim() != 1 or cu_seqlens.dtype != torch.int32:
+        raise ValueError("cu_seqlens must be a 1-D int32 CUDA tensor")
+    return _paged_attn(q, cache, table, lens, cu_seqlens, cu_seqlens.numel() - 1, max_seqlen,
+                       q.shape[0], max_len, window, n_sink, scale, out, lse, workspace, dev_status,
+                       stream)
 
 
 def expiry_test(q, k, v, out, lse, dev_status, stream=None):

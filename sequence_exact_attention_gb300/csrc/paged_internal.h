@@ -1,0 +1,78 @@
+// Internal declarations of the paged key/value cache: its format, the
+// arguments of its kernels and their launchers.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "ring_attn.h"
+
+namespace ra {
+
+// A pool of pages: rows of D values (one slot of one key/value head),
+// [n_pages, H_kv, page, D] bfloat16, or e4m3 codes with one power of two a row,
+// its biased exponent in ks, vs [n_pages, H_kv, page]: a code c stands for
+// c 2^(byte - 127). Slot j of sequence b is row j % page of page
+// table[b * width + j / page].
+struct PagePool {
+  uint8_t *k, *v, *ks, *vs;
+  int n_pages, H_kv, page, D;
+  int quant;               // 1: e4m3 codes
+};
+constexpr int kPageMin = 16, kPageMax = 128;
+
+// append and read.
+struct PagedRowArgs {
+  PagePool p;
+  const int* table;
+  int width;
+  void* k;                 // [B, T, H_kv, D] or, with cu, [rows, H_kv, D]
+  void* v;
+  const int* start;        // [B], or null for 0
+  const int* n_new;        // [B] tokens that count, or null for T (append)
+  const int* cu;           // [B + 1] packed rows' offsets, or null (append)
+  int B, T;
+  long long rows;          // B * T, or the packed rows
+  int* status;
+};
+ra_status launch_paged_append(const PagedRowArgs& a, int dtype, cudaStream_t stream);
+ra_status launch_paged_read(const PagedRowArgs& a, int dtype, cudaStream_t stream);
+
+// Attention of each sequence's new tokens over its slots.
+struct PagedAttnArgs {
+  const void* q;           // [rows, H_q, D] bf16
+  PagePool p;
+  const int* table;
+  int width;
+  const int* lens;         // [B] slots in use, the new tokens' included
+  const int* cu;           // [B + 1] offsets of packed rows, or null: T rows a sequence
+  void* out;               // [rows, H_q, D] bf16
+  float* lse;              // [B, H_q, T] or, packed, [H_q, rows]; may be null
+  int B, T, rows, H_q;     // T: new tokens a sequence; packed: at most so many
+  int max_len;             // bound on lens
+  int window, n_sink;      // window 0: every slot up to the query's own
+  float scale_log2;        // softmax scale * log2(e)
+  // plan (paged_attn_plan): a sequence's new tokens give T * H_q / H_kv query
+  // rows a key/value head, cut into n_rb blocks; the visible tiles of each are
+  // cut into n_split chunks of `chunk` tiles.
+  int block_rows, n_rb, n_split, chunk;
+  float* workspace;
+  float* part_o;           // [n_split][rows * H_q][D]
+  float* part_ml;          // [n_split][rows * H_q][2]: maximum (base 2), sum
+  int* status;
+};
+
+// Fills the plan fields for the sizes in `a`; bytes: the workspace needed (the
+// same for packed rows and others).
+ra_status paged_attn_plan(PagedAttnArgs* a, size_t* bytes);
+ra_status launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
+
+// TMA map of a pool's keys or values as [n_pages * H_kv, page, D]: a box is
+// `box_rows` rows of one page by 64 values (bfloat16) or D (codes), swizzled
+// over the bytes of its rows (128, or 64 where D is 64 and codes are held).
+bool make_page_map(CUtensorMap* m, const PagePool& p, const void* ptr, int box_rows);
+
+}  // namespace ra

@@ -1,0 +1,100 @@
+// Device code that the paged cache's kernels share: number formats, boxes of
+// pages, a sequence's rows and the tiles of slots that a block of them sees.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "paged_internal.h"
+
+namespace ra {
+
+// Two e4m3 codes (lo in the low byte), to nearest, half to even.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two codes, in the low 16 bits, as two halves (exact).
+__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
+  return r;
+}
+__device__ __forceinline__ float2 half2_values(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// 2^(byte - 127).
+__device__ __forceinline__ float pow2_byte(int byte) { return __uint_as_float((uint32_t)byte << 23); }
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int c0,
+                                            int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// A sequence's new tokens: their first row in q and out, how many they are, and
+// the slots in use with them. Offsets are brought into the tensors' range.
+struct PagedSeq {
+  int row0, n, len;
+};
+__device__ __forceinline__ PagedSeq paged_seq(const PagedAttnArgs& a, int b) {
+  PagedSeq s;
+  if (a.cu) {
+    s.row0 = min(max(__ldg(a.cu + b), 0), a.rows);
+    s.n = min(min(max(__ldg(a.cu + b + 1) - s.row0, 0), a.T), a.rows - s.row0);
+  } else {
+    s.row0 = b * a.T;
+    s.n = a.T;
+  }
+  s.len = min(max(__ldg(a.lens + b), 0), a.max_len);
+  return s;
+}
+
+// Whether the row at position p sees slot j.
+__device__ __forceinline__ bool paged_sees(const PagedAttnArgs& a, int p, int j) {
+  return j <= p && (a.window <= 0 || j > p - a.window || j < a.n_sink);
+}
+
+// The tiles of kTile slots that rows at positions pmin to pmax see: those of the
+// first slots that the windows have left behind, then the windows' own.
+template <int kTile>
+struct PagedSpan {
+  int hi;              // slots from here on are invisible to every row
+  int pmin, pmax;
+  int n_sink_tiles, w0;
+  int n;               // tiles in all
+  __device__ __forceinline__ void init(const PagedAttnArgs& a, int p0, int p1) {
+    pmin = p0;
+    pmax = p1;
+    hi = max(p1 + 1, 0);
+    const int lo = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
+    w0 = lo / kTile;
+    n_sink_tiles = min((min(a.n_sink, hi) + kTile - 1) / kTile, w0);
+    n = n_sink_tiles + max((hi + kTile - 1) / kTile - w0, 0);
+  }
+  __device__ __forceinline__ int tile(int v) const {
+    return v < n_sink_tiles ? v : v - n_sink_tiles + w0;
+  }
+  // Whether some row sees one of the n slots from j0 on, a run that starts below hi.
+  __device__ __forceinline__ bool meets(const PagedAttnArgs& a, int j0, int n_slots) const {
+    return a.window <= 0 || j0 + n_slots > pmin - a.window + 1 || j0 < a.n_sink;
+  }
+  // Whether every row sees all of the n slots from j0 on.
+  __device__ __forceinline__ bool whole(const PagedAttnArgs& a, int j0, int n_slots) const {
+    return j0 + n_slots - 1 <= pmin &&
+           (a.window <= 0 || j0 > pmax - a.window || j0 + n_slots <= a.n_sink);
+  }
+};
+
+// The place of a row's log-sum.
+__device__ __forceinline__ long long paged_lse_at(const PagedAttnArgs& a, int b, int row, int t,
+                                                  int h) {
+  return a.cu ? (long long)h * a.rows + row : ((long long)b * a.H_q + h) * a.T + t;
+}
+
+}  // namespace ra

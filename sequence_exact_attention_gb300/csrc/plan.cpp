@@ -185,7 +185,7 @@ const char* ring_attn_strerror(int status) {
     case RA_ERR_LAUNCH: return "CUDA error while preparing or launching a kernel";
     case RA_ERR_TIMEOUT: return "a device-side bounded wait expired";
     case RA_ERR_BUFFER: return "caller buffer too small, or it overlaps another of the call's";
-    case RA_ERR_RANGE: return "size or index out of range (32-bit indexing; ring step outside [-1, P); window; cache slots)";
+    case RA_ERR_RANGE: return "size or index out of range (32-bit indexing; ring step outside [-1, P); window; cache slots; pages)";
     case RA_ERR_SCRATCH:
       return "problem too large for the library's built-in backward scratch "
              "(8 MiB: at most 2^20 tile-padded query rows; use ring_attn_bwd with a workspace)";
@@ -193,6 +193,6 @@ const char* ring_attn_strerror(int status) {
   }
 }
 
-int ring_attn_version(void) { return 104; }   // 1.04: 4-bit key/value cache, windows
+int ring_attn_version(void) { return 105; }   // 1.05: paged key/value cache
 
 }  // extern "C"
