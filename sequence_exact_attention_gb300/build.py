@@ -29,8 +29,8 @@ VARIANTS = {"release": (LIB, OUT, []),
 
 SOURCES = ["plan.cpp", "api.cpp", "tensor_map.cpp", "merge.cu", "attn_simt.cu", "attn_tc.cu",
            "attn_f32_window.cu", "attn_bwd.cu", "bwd_noalloc.cu", "kv4_api.cpp", "kv4_cache.cu",
-           "kv4_attn.cu", "kv4_evict.cu", "paged_api.cpp", "paged_map.cpp", "paged_cache.cu",
-           "paged_attn.cu"]
+           "kv4_attn.cu", "kv4_evict.cu", "paged_api.cpp", "paged_plan.cpp", "paged_map.cpp",
+           "paged_cache.cu", "paged_attn.cu", "paged_tiles.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC",

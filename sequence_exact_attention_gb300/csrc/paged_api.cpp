@@ -152,9 +152,11 @@ ra_status attn(const void* q, const ra_pages* pages, const int* table, int width
   a.out = out;
   a.lse = lse;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / __builtin_sqrtf((float)pages->D)) * 1.4426950408889634f;
-  a.workspace = static_cast<float*>(workspace);
   a.status = status;
-  return launch_paged_attn(a, reinterpret_cast<cudaStream_t>(stream));
+  paged_attn_place(&a, workspace);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = a.block_rows <= 16 ? launch_paged_rows(a, s) : launch_paged_tiles(a, s);
+  return st != RA_OK || a.n_split == 1 ? st : launch_paged_join(a, s);
 }
 
 }  // namespace

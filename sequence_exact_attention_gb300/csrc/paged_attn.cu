@@ -17,8 +17,9 @@
 // Roundings: weights to half (2^-12) or, in bf16 pages, to bf16 (2^-9); sums and
 // statistics are float32.
 //
-// A CTA takes one chunk of the slots of one (sequence, key/value head, block of 8
-// or 16 query rows). A producer warp looks the pages up, a lane for each, and asks
+// For up to 16 query rows a sequence and key/value head (new tokens times the heads
+// that share it; more: paged_tiles.cu). A CTA takes one chunk of the slots of one
+// sequence and key/value head. A producer warp looks the pages up, a lane for each, and asks
 // for their boxes (TMA, swizzled, so that ldmatrix meets no bank conflict); four
 // warps share a tile's slots and keep running maxima, sums and outputs of their own,
 // joined in shared memory at the end. Chunks of a long axis are joined by a second
@@ -129,7 +130,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   constexpr int kTile = S::kTile;
   constexpr int WS = kTile / kWarps;        // slots a warp
   constexpr int MB = WS / 16;
-  constexpr int RB = 8 * NT;                // query rows of the block
+  constexpr int RB = 8 * NT;                // query rows, at most
   constexpr int KS = D / 16;                // steps of 16 dimensions
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = sm100::smem_u32(smem_raw);
@@ -146,11 +147,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int H_kv = a.p.H_kv, grp = a.H_q / H_kv;
-  int blk = blockIdx.x;
-  const int split = blk % a.n_split;
-  blk /= a.n_split;
-  const int rb = blk % a.n_rb;
-  const int bh = blk / a.n_rb;
+  const int split = blockIdx.x % a.n_split;
+  const int bh = blockIdx.x / a.n_split;
   const int hk = bh % H_kv, b = bh / H_kv;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
@@ -162,11 +160,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
   const PagedSeq sq = paged_seq(a, b);
   const int R = sq.n * grp;                 // query rows of this head
-  const int r0 = rb * RB;
-  if (r0 >= R) return;                      // a shorter sequence of the batch
+  if (R == 0) return;                       // a sequence without new tokens
   const int first = sq.len - sq.n;          // position of the first new token
   PagedSpan<kTile> sp;
-  sp.init(a, first + r0 / grp, first + (min(r0 + RB, R) - 1) / grp);
+  sp.init(a, first, first + sq.n - 1);
   const int v_begin = split * a.chunk;
   const int n_tiles = max(min(sp.n, v_begin + a.chunk) - v_begin, 0);
   let_dependents_start();
@@ -236,14 +233,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     __syncthreads();                         // every warp has read the ring
   } else {
     // ======================= the warps that compute =======================
-    // the block's query rows as B operands: lane (g, c) holds row g's dimensions
+    // the query rows as B operands: lane (g, c) holds row g's dimensions
     // 16 k + 2 c, + 1, + 8, + 9 of step k; codes come four to a lane, 16 k + 4 c on
     uint32_t qf[NT][KS][2];
     float sl2[NT][2];                        // of rows 2c and 2c + 1
     int pos[NT][2];                          // their positions; below 0: sees nothing
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + nt * 8 + g;
+      const int r = nt * 8 + g;
       const bool row_ok = r < R;
       const long long off =
           row_ok ? ((long long)(sq.row0 + r / grp) * a.H_q + hk * grp + r % grp) * D : 0;
@@ -286,7 +283,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int rr = r0 + nt * 8 + 2 * c + h;
+        const int rr = nt * 8 + 2 * c + h;
         pos[nt][h] = rr < R ? first + rr / grp : -1;
       }
     }
@@ -573,7 +570,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     atomicExch(a.status, (int)RA_ERR_TIMEOUT);
   for (int i = threadIdx.x; i < RB * (D / 4); i += kThreads) {
     const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-    if (r0 + r >= R) continue;
+    if (r >= R) continue;
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sM[w * RB + r]);
@@ -591,7 +588,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       y.w = fmaf(f, x.w, y.w);
       ls = fmaf(f, lw, ls);
     }
-    const int t = (r0 + r) / grp, h = hk * grp + (r0 + r) % grp;
+    const int t = r / grp, h = hk * grp + r % grp;
     const long long row = (long long)(sq.row0 + t) * a.H_q + h;
     if (a.n_split > 1) {
       const long long part = (long long)split * a.rows * a.H_q + row;
@@ -695,7 +692,7 @@ ra_status launch_rows(const PagedAttnArgs& a, cudaStream_t stream) {
   const int box_rows = a.p.page < S::kTile ? a.p.page : S::kTile;
   if (!make_page_map(&mk, a.p, a.p.k, box_rows) || !make_page_map(&mv, a.p, a.p.v, box_rows))
     return RA_ERR_LAUNCH;
-  const long long grid = (long long)a.B * a.p.H_kv * a.n_rb * a.n_split;
+  const long long grid = (long long)a.B * a.p.H_kv * a.n_split;
   if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
   auto kern = paged_attn_kernel<D, NT, kQuant>;
   static std::atomic<uint64_t> allowed;
@@ -704,66 +701,21 @@ ra_status launch_rows(const PagedAttnArgs& a, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_LAUNCH;
 }
 
-template <int D>
-ra_status launch_d(const PagedAttnArgs& a, cudaStream_t stream) {
-  ra_status st;
-  if (a.block_rows == 8)
-    st = a.p.quant ? launch_rows<D, 1, true>(a, stream) : launch_rows<D, 1, false>(a, stream);
-  else
-    st = a.p.quant ? launch_rows<D, 2, true>(a, stream) : launch_rows<D, 2, false>(a, stream);
-  if (st != RA_OK || a.n_split == 1) return st;
-  return launch_early(paged_join_kernel<D>, (long long)a.rows * a.H_q, 32 * kJoinWarps, 0, stream, a)
-             ? RA_OK : RA_ERR_LAUNCH;
-}
-
 }  // namespace
 
-// Chunks: as many as fill whole waves of resident CTAs best, two waves by
-// preference (sequences of different lengths then even out), but none under
-// kMinChunk tiles, where joining would cost more than it spreads.
-ra_status paged_attn_plan(PagedAttnArgs* a, size_t* bytes) {
-  constexpr int kMinChunk = 2;
-  const int tile = !a->p.quant && a->p.D == 128 ? 64 : 128;
-  const long long R = (long long)a->T * (a->H_q / a->p.H_kv);
-  a->block_rows = R <= 8 ? 8 : 16;
-  const long long n_rb = (R + a->block_rows - 1) / a->block_rows;
-  const long long blocks = (long long)a->B * a->p.H_kv * n_rb;
-  long long tiles = ((long long)a->max_len + tile - 1) / tile;
-  if (a->window > 0) {
-    const long long seen = ((long long)a->n_sink + tile - 1) / tile +
-                           ((long long)a->window + a->T - 1 + tile - 1) / tile + 1;
-    if (seen < tiles) tiles = seen;
-  }
-  // CTAs resident at a time on a GB300: a constant, as the workspace's size has to
-  // be the same where there is no device to ask
-  const long long wave = 152 * 2;
-  long long best = 1, best_full = 0;                        // chunks, and what they fill of their waves
-  for (int w = 2; w >= 1; --w) {
-    const long long n = wave * w / blocks;
-    const long long full = n * blocks * 1000 / (wave * w);
-    if (full > best_full + 20) {
-      best = n;
-      best_full = full;
-    }
-  }
-  long long chunk = (tiles + best - 1) / best;
-  if (chunk < kMinChunk) chunk = kMinChunk;
-  const long long n_split = tiles > chunk ? (tiles + chunk - 1) / chunk : 1;
-  if (blocks * n_split > 0x7fffffffLL) return RA_ERR_RANGE;
-  a->n_rb = (int)n_rb;
-  a->chunk = (int)chunk;
-  a->n_split = (int)n_split;
-  const size_t parts = n_split > 1 ? (size_t)n_split * a->rows * a->H_q : 0;
-  *bytes = parts * (a->p.D + 2) * sizeof(float);
-  return RA_OK;
+ra_status launch_paged_rows(const PagedAttnArgs& a, cudaStream_t stream) {
+  auto launch = [&](auto few, auto more) { return a.block_rows == 8 ? few(a, stream) : more(a, stream); };
+  if (a.p.D == 64)
+    return a.p.quant ? launch(launch_rows<64, 1, true>, launch_rows<64, 2, true>)
+                     : launch(launch_rows<64, 1, false>, launch_rows<64, 2, false>);
+  return a.p.quant ? launch(launch_rows<128, 1, true>, launch_rows<128, 2, true>)
+                   : launch(launch_rows<128, 1, false>, launch_rows<128, 2, false>);
 }
 
-ra_status launch_paged_attn(const PagedAttnArgs& args, cudaStream_t stream) {
-  PagedAttnArgs a = args;
-  // partial outputs, then their (maximum, sum)
-  a.part_o = a.workspace;
-  a.part_ml = a.workspace + (a.n_split > 1 ? (size_t)a.n_split * a.rows * a.H_q * a.p.D : 0);
-  return a.p.D == 64 ? launch_d<64>(a, stream) : launch_d<128>(a, stream);
+ra_status launch_paged_join(const PagedAttnArgs& a, cudaStream_t stream) {
+  auto kern = a.p.D == 64 ? paged_join_kernel<64> : paged_join_kernel<128>;
+  return launch_early(kern, (long long)a.rows * a.H_q, 32 * kJoinWarps, 0, stream, a) ? RA_OK
+                                                                                      : RA_ERR_LAUNCH;
 }
 
 }  // namespace ra

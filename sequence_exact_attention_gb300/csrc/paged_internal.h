@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "ring_attn.h"
@@ -58,21 +59,32 @@ struct PagedAttnArgs {
   // plan (paged_attn_plan): a sequence's new tokens give T * H_q / H_kv query
   // rows a key/value head, cut into n_rb blocks; the visible tiles of each are
   // cut into n_split chunks of `chunk` tiles.
-  int block_rows, n_rb, n_split, chunk;
-  float* workspace;
+  int block_rows;          // 8 or 16: few rows (paged_attn.cu); 256: many (paged_tiles.cu)
+  int n_rb, n_split, chunk;
+  int rb_major;            // many rows: the blocks' order, see there
+  int n_expanded;          // many rows over 8-bit pages: tiles a sequence's rows see at most
   float* part_o;           // [n_split][rows * H_q][D]
   float* part_ml;          // [n_split][rows * H_q][2]: maximum (base 2), sum
+  __nv_bfloat16* expanded_k;     // [B][n_expanded][H_kv][128][D]
+  __nv_bfloat16* expanded_v;
   int* status;
 };
 
 // Fills the plan fields for the sizes in `a`; bytes: the workspace needed (the
-// same for packed rows and others).
+// same for packed rows and others). paged_attn_place puts its parts there.
 ra_status paged_attn_plan(PagedAttnArgs* a, size_t* bytes);
-ra_status launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
+void paged_attn_place(PagedAttnArgs* a, void* workspace);
+// The launchers of the two kernels and of the join of their chunks.
+ra_status launch_paged_rows(const PagedAttnArgs& a, cudaStream_t stream);
+ra_status launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t stream);
+ra_status launch_paged_join(const PagedAttnArgs& a, cudaStream_t stream);
 
 // TMA map of a pool's keys or values as [n_pages * H_kv, page, D]: a box is
 // `box_rows` rows of one page by 64 values (bfloat16) or D (codes), swizzled
 // over the bytes of its rows (128, or 64 where D is 64 and codes are held).
 bool make_page_map(CUtensorMap* m, const PagePool& p, const void* ptr, int box_rows);
+// TMA map of bf16 queries [rows, H_q, D]: a box is 64 columns of `heads` heads of
+// `tokens` rows, a row of the box after the other, 128-byte swizzle.
+bool make_query_map(CUtensorMap* m, const void* q, int rows, int H_q, int D, int heads, int tokens);
 
 }  // namespace ra

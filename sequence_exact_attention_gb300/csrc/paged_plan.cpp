@@ -1,0 +1,84 @@
+// How an attention call over pages is cut up: which kernel, its blocks of query rows
+// and its chunks of slots. Host only, and the same where there is no device to ask,
+// as the workspace's size follows from it: the card's numbers are a GB300's.
+#include "paged_internal.h"
+
+namespace ra {
+namespace {
+
+constexpr long long kSms = 152;
+
+// Tiles of `tile` slots that a run of T new tokens sees at most.
+long long tiles_seen(const PagedAttnArgs& a, int tile, long long T) {
+  const long long all = ((long long)a.max_len + tile - 1) / tile;
+  if (a.window <= 0) return all;
+  const long long seen = ((long long)a.n_sink + tile - 1) / tile +
+                         ((long long)a.window + T - 1 + tile - 1) / tile + 1;
+  return seen < all ? seen : all;
+}
+
+}  // namespace
+
+ra_status paged_attn_plan(PagedAttnArgs* a, size_t* bytes) {
+  const int grp = a->H_q / a->p.H_kv;
+  const long long R = (long long)a->T * grp;
+  long long n_rb, tiles, best = 1, least;
+  // Few rows: chunks that fill whole waves of resident CTAs best, two waves by
+  // preference (sequences of different lengths then even out), but none under two
+  // tiles, where joining would cost more than it spreads.
+  if (R <= 16) {
+    a->block_rows = R <= 8 ? 8 : 16;
+    n_rb = 1;
+    const int tile = !a->p.quant && a->p.D == 128 ? 64 : 128;
+    tiles = tiles_seen(*a, tile, a->T);
+    least = 2;
+    const long long blocks = (long long)a->B * a->p.H_kv, wave = 2 * kSms;
+    long long best_full = 0;
+    for (int w = 2; w >= 1; --w) {
+      const long long n = wave * w / blocks;
+      const long long full = n * blocks * 1000 / (wave * w);
+      if (full > best_full + 20) {
+        best = n;
+        best_full = full;
+      }
+    }
+  } else {
+    // Many rows: a CTA a multiprocessor; chunks only where blocks are fewer.
+    a->block_rows = 256;
+    const int block_tokens = 2 * (128 / grp);
+    n_rb = ((long long)a->T + block_tokens - 1) / block_tokens;
+    tiles = tiles_seen(*a, 128, block_tokens < a->T ? block_tokens : a->T);
+    least = 4;
+    const long long blocks = (long long)a->B * a->p.H_kv * n_rb;
+    if (blocks < kSms) best = kSms / blocks;
+    // keys and values within half of the 126 MB L2
+    a->rb_major = (long long)a->B * a->max_len * a->p.H_kv * a->p.D * 4 <= (64ll << 20);
+  }
+  long long chunk = (tiles + best - 1) / best;
+  if (chunk < least) chunk = least;
+  const long long n_split = tiles > chunk ? (tiles + chunk - 1) / chunk : 1;
+  if ((long long)a->B * a->p.H_kv * n_rb * n_split > 0x7fffffffLL) return RA_ERR_RANGE;
+  a->n_rb = (int)n_rb;
+  a->chunk = (int)chunk;
+  a->n_split = (int)n_split;
+  size_t n = n_split > 1 ? (size_t)n_split * a->rows * a->H_q * (a->p.D + 2) * sizeof(float) : 0;
+  if (a->block_rows == 256 && a->p.quant) {
+    const long long e = tiles_seen(*a, 128, a->T);
+    if ((long long)a->B * e * a->p.H_kv > 0x7fffffffLL) return RA_ERR_RANGE;
+    a->n_expanded = (int)e;
+    n += (size_t)a->B * e * a->p.H_kv * 128 * a->p.D * 2 * 2;
+  }
+  *bytes = n;
+  return RA_OK;
+}
+
+void paged_attn_place(PagedAttnArgs* a, void* workspace) {
+  __nv_bfloat16* e = static_cast<__nv_bfloat16*>(workspace);
+  const size_t tensor = (size_t)a->B * a->n_expanded * a->p.H_kv * 128 * a->p.D;
+  a->expanded_k = e;
+  a->expanded_v = e + tensor;
+  a->part_o = reinterpret_cast<float*>(e + 2 * tensor);
+  a->part_ml = a->part_o + (a->n_split > 1 ? (size_t)a->n_split * a->rows * a->H_q * a->p.D : 0);
+}
+
+}  // namespace ra

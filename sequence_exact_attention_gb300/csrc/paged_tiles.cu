@@ -1,0 +1,637 @@
+// Attention of many query rows a sequence (pieces of prompts) over its pages, on
+// the tcgen05 tensor cores; definitions as in paged_attn.cu.
+//
+// A query tile is 128 rows of one key/value head: the rows of a group's heads
+// side by side, 128 / group tokens of them, so that a key/value tile is loaded once
+// for the whole group and a short piece still fills a tile. (A group that does not
+// divide 128 leaves the last rows unused.) One CTA owns two query tiles and walks
+// the tiles of 128 slots that some row of them sees; each tile of keys and values
+// serves both. Where query blocks are too few to fill the card the walk is cut into
+// chunks, joined by paged_join_kernel.
+//
+// bf16 pages are read where they lie: the producer warp looks a tile's pages up, a
+// lane for each, and asks for their boxes; a page that is not there, or that holds
+// nothing that the block sees, comes as zeros (a coordinate past the tensor). 8-bit
+// pages are expanded first, by a kernel of their own, to bf16 tiles in the
+// workspace: exact, as a code times its row's power of two is a bf16 number. It
+// moves 5 bytes a value where the products take 4 D flops a row and value pair.
+//
+// Roles (320 threads): warps 0-7 softmax, two threads a query row, 64 columns each,
+// for Q0 and then Q1 at every tile; a producer warp; an issuer warp whose elected
+// lane issues every MMA. Tensor memory: S_i (128 f32 columns) at 128 i, over whose
+// first 64 the weights are written as bf16; O_i (D columns) at 256 + D i. Per tile
+// j the tensor core runs PV0(j) S0(j+1) PV1(j) S1(j+1), one tile's products under
+// the other's softmax. Barriers:
+//   qfull[i]         Q_i landed
+//   kfull/vfull[s]   keys / values of a tile landed in slot s
+//   done[j mod kKBuf] every MMA up to S1(j) is done: K_j's and V_{j-1}'s slots are free
+//   sfull[i]         S_i(j) done; it covers PV_i(j-1)
+//   pfull[i]         P_i(j) written, O_i rescaled (256 arrivals)
+//   odone[i]         the last PV_i done
+// Every wait is bounded: after kTimeoutNs a thread raises the CTA's abort flag, all
+// roles fall through to the teardown, which waits (bounded) for copies and MMAs in
+// flight and frees the tensor memory, and the status word says RA_ERR_TIMEOUT.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "checks.cuh"
+#include "early_launch.cuh"
+#include "fastmath.cuh"
+#include "kv4_internal.h"
+#include "paged_internal.h"
+#include "paged_ops.cuh"
+#include "sm100.cuh"
+#include "tc_tiles.cuh"
+
+namespace ra {
+namespace {
+
+using namespace sm100;
+using namespace fastmath;
+using tc::kBoxBytes;
+using tc::kTile;
+
+constexpr int kSoftmaxWarps = 8;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 32 * 10;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 256;
+constexpr float kRescaleLog2 = 8.0f;       // O is rescaled when the maximum grows by more
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kKBuf = D == 128 ? 2 : 3;
+  static constexpr int kVBuf = kKBuf;
+  static constexpr int kQOff = 0;
+  static constexpr int kKOff = 2 * kTileBytes;
+  static constexpr int kVOff = kKOff + kKBuf * kTileBytes;
+  static constexpr int kBarOff = kVOff + kVBuf * kTileBytes;
+  static constexpr int kBarBytes = 256;
+  // maxima [2 parities][2 parts][128 rows], sums [2 tiles][2 parts][128 rows]
+  static constexpr int kRedOff = kBarOff + kBarBytes;
+  static constexpr int kRedBytes = (512 + 512) * 4;
+  static constexpr int kUsed = kRedOff + kRedBytes + 1024;   // + alignment slack
+  // more than half an SM's shared memory: one CTA an SM, so the allocation of all
+  // tensor memory never waits for another CTA
+  static constexpr int kSmemBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+  static constexpr int bQFull = 0;                  // [2]
+  static constexpr int bKFull = 2;                  // [kKBuf]
+  static constexpr int bVFull = bKFull + kKBuf;     // [kVBuf]
+  static constexpr int bDone = bVFull + kVBuf;      // [kKBuf]
+  static constexpr int bSFull = bDone + kKBuf;      // [2]
+  static constexpr int bPFull = bSFull + 2;         // [2]
+  static constexpr int bODone = bPFull + 2;         // [2]
+  static constexpr int bFinal = bODone + 2;
+  static constexpr int kNumBars = bFinal + 1;
+  static constexpr int kGoneOff = kBarBytes - 48;     // [8] pages not there, of tile j at j mod 8
+  static constexpr int kHolderOff = kBarBytes - 16;   // tensor memory's address
+  static constexpr int kNeverOff = kBarBytes - 12;    // stays 0: waits that ignore aborts
+  static constexpr int kAbortOff = kBarBytes - 8;     // abort flag
+  static_assert(kNumBars * 8 <= kGoneOff, "barrier area overflow");
+  static_assert(kSmemBytes > 116 * 1024, "must not fit two CTAs per SM");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+  static_assert(kOCol + 2 * D <= kTmemCols, "tensor memory budget");
+};
+
+// Rows [from, to) of a tile of 64-column boxes, as 0, by the 256 softmax threads.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int from, int to, int thread) {
+  for (int bx = 0; bx < boxes; ++bx)
+    for (int i = thread; i < (to - from) * 8; i += 32 * kSoftmaxWarps)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                       tile + (uint32_t)(bx * kBoxBytes + from * 128 + i * 16)),
+                   "r"(0)
+                   : "memory");
+}
+
+// The tiles of 128 slots that a sequence's new tokens see, all of them: their
+// places among the expanded ones.
+__device__ __forceinline__ PagedSpan<kTile> sequence_span(const PagedAttnArgs& a,
+                                                          const PagedSeq& sq) {
+  PagedSpan<kTile> s;
+  s.init(a, sq.len - sq.n, sq.len - 1);
+  return s;
+}
+
+template <int D, bool kExpanded>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const PagedAttnArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw);
+  auto bar = [&](int i) -> uint32_t { return base + C::kBarOff + 8u * (uint32_t)i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + C::kBarOff + C::kAbortOff);
+  volatile int* never = reinterpret_cast<volatile int*>(base_ptr + C::kBarOff + C::kNeverOff);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + C::kBarOff + C::kHolderOff);
+  volatile uint32_t* gone = reinterpret_cast<volatile uint32_t*>(base_ptr + C::kBarOff + C::kGoneOff);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- work item: two query tiles of one key/value head, one chunk of their walk.
+  // Blocks of late tokens (the longest walks) come first: across all heads and
+  // sequences when the keys and values fit in L2 anyway, else within each head.
+  const int H_kv = a.p.H_kv, grp = a.H_q / H_kv;
+  const int tt = kTile / grp;                     // tokens a query tile
+  int item = blockIdx.x;
+  const int split = item % a.n_split;
+  item /= a.n_split;
+  const int n_bh = a.B * H_kv;
+  const int rb = a.n_rb - 1 - (a.rb_major ? item / n_bh : item % a.n_rb);
+  const int bh = a.rb_major ? item % n_bh : item / a.n_rb;
+  const int b = bh / H_kv, hk = bh % H_kv;
+  const PagedSeq sq = paged_seq(a, b);
+  const int t0 = rb * 2 * tt;                     // the block's first new token
+  if (t0 >= sq.n) return;                         // a shorter sequence of the batch
+  const int n_tok = min(2 * tt, sq.n - t0);
+  const bool two = n_tok > tt;
+  const int first = sq.len - sq.n + t0;           // its position
+  PagedSpan<kTile> sp;
+  sp.init(a, first, first + n_tok - 1);
+  const int v_begin = split * a.chunk;
+  const int n = max(min(sp.n, v_begin + a.chunk) - v_begin, 0);   // tiles to walk
+  auto tile_lo = [&](int j) -> int { return sp.tile(v_begin + j) * kTile; };
+
+  // ---- set-up: barriers, abort flag, TMEM
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::bQFull + i), 1);
+      mbar_init(bar(C::bSFull + i), 1);
+      mbar_init(bar(C::bPFull + i), 32 * kSoftmaxWarps);
+      mbar_init(bar(C::bODone + i), 1);
+    }
+    for (int i = 0; i < C::kKBuf; ++i) {
+      mbar_init(bar(C::bKFull + i), 1);
+      mbar_init(bar(C::bVFull + i), 1);
+      mbar_init(bar(C::bDone + i), 1);
+    }
+    mbar_init(bar(C::bFinal), 1);
+    *abort_flag = 0;
+    *never = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+    tmem_relinquish();
+  }
+  let_dependents_start();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == kProducerWarp) {
+    // ======================= TMA producer =======================
+    if (lane == 0) {
+      for (int i = 0; i < (two ? 2 : 1); ++i) {
+        mbar_arrive_expect_tx(bar(C::bQFull + i), (uint32_t)(C::kBoxes * tt * grp * 128));
+        for (int bx = 0; bx < C::kBoxes; ++bx)
+          tma_load_3d(base + C::kQOff + i * C::kTileBytes + bx * kBoxBytes, &tm_q,
+                      bar(C::bQFull + i), bx * 64, hk * grp, sq.row0 + t0 + i * tt);
+      }
+    }
+    __syncwarp();
+    // done(x) is phase x / kKBuf of ring barrier x mod kKBuf. It is waited for only
+    // while K_{x + kKBuf}, which done(x + kKBuf) needs, is not loaded, so the barrier
+    // is never two phases ahead.
+    auto wait_done = [&](int x) -> bool {
+      return mbar_wait_warp(bar(C::bDone + x % C::kKBuf), (uint32_t)(x / C::kKBuf) & 1, abort_flag,
+                            kTimeoutNs);
+    };
+    const int shift = 31 - __clz(a.p.page);
+    const int n_box = kTile >> shift;             // pages a tile
+    const int at = lane << shift;                 // this lane's page's first slot in the tile
+    const PagedSpan<kTile> whole = sequence_span(a, sq);
+    const int past = kExpanded ? 0 : a.p.n_pages * H_kv;      // past the tensor: zeros
+    auto look_up = [&](int j) -> int {            // -1: nothing to load; -2: no such page
+      if (j >= n || lane >= n_box) return -1;
+      const int slot = tile_lo(j) + at;
+      if (slot >= sp.hi || !sp.meets(a, slot, a.p.page)) return -1;
+      const int p = slot >> shift;
+      if (p >= a.width) return -2;
+      const int id = __ldg(a.table + (size_t)b * a.width + p);
+      return id >= 0 && id < a.p.n_pages ? id : -2;
+    };
+    auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t full, int id, int j) {
+      if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
+      __syncwarp();
+      if constexpr (kExpanded) {
+        const int t = sp.tile(v_begin + j);
+        const int v = t < whole.n_sink_tiles ? t : t - whole.w0 + whole.n_sink_tiles;
+        if (lane < C::kBoxes)
+          tma_load_3d(dst + lane * kBoxBytes, m, full, lane * 64, 0,
+                      (b * a.n_expanded + v) * H_kv + hk);
+      } else if (lane < n_box) {
+        const int z = id >= 0 ? id * H_kv + hk : past;
+#pragma unroll
+        for (int bx = 0; bx < C::kBoxes; ++bx)
+          tma_load_3d(dst + bx * kBoxBytes + at * 128, m, full, bx * 64, 0, z);
+      }
+    };
+    int id = look_up(0);
+    int nk = 0, nv = 0, s = 0;                    // tiles of keys, of values asked for; slot
+    bool bad = false;
+    for (int j = 0; j < n; ++j) {
+      const int next = look_up(j + 1);
+      const uint32_t missing = __ballot_sync(0xffffffffu, id == -2);
+      bad |= missing != 0;
+      // K_j reuses the slot of K_{j-kKBuf}: free at done(j - kKBuf)
+      if (j >= C::kKBuf && !wait_done(j - C::kKBuf)) break;
+      if (lane == 0) gone[j & 7] = missing;       // tile j - 8's has been read long since
+      load(base + C::kKOff + s * C::kTileBytes, &tm_k, bar(C::bKFull + s), id, j);
+      ++nk;
+      // V_j reuses the slot of V_{j-kVBuf}: free at done(j - kVBuf + 1)
+      if (j >= C::kVBuf && !wait_done(j - C::kVBuf + 1)) break;
+      load(base + C::kVOff + s * C::kTileBytes, &tm_v, bar(C::bVFull + s), id, j);
+      ++nv;
+      id = next;
+      if (++s == C::kKBuf) s = 0;
+    }
+    // what was asked for lands before the CTA leaves (it has, unless it aborted)
+    for (int x = max(nk - C::kKBuf, 0); x < nk; ++x)
+      mbar_wait(bar(C::bKFull + x % C::kKBuf), (uint32_t)(x / C::kKBuf) & 1, never, kTimeoutNs);
+    for (int x = max(nv - C::kVBuf, 0); x < nv; ++x)
+      mbar_wait(bar(C::bVFull + x % C::kVBuf), (uint32_t)(x / C::kVBuf) & 1, never, kTimeoutNs);
+    for (int i = 0; i < (two ? 2 : 1); ++i) mbar_wait(bar(C::bQFull + i), 0, never, kTimeoutNs);
+    if (bad && lane == 0 && a.status) atomicExch(a.status, (int)RA_ERR_RANGE);
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ======================= MMA issuer =======================
+    // The whole warp runs the loop, so its descriptor arithmetic is warp-uniform;
+    // one elected lane issues the MMAs and commits.
+    const bool leader = elect_one_sync();
+    const uint64_t q_desc = sw128_desc(base + C::kQOff, 16, 1024);
+    const uint64_t k_desc = sw128_desc(base + C::kKOff, 16, 1024);
+    const uint64_t v_desc = sw128_desc(base + C::kVOff, kBoxBytes, 1024);
+    const uint64_t q1_off = (uint64_t)(C::kTileBytes >> 4);
+    const uint32_t tS0 = tmem, tS1 = tmem + kTile;
+    const uint32_t tO0 = tmem + kOCol, tO1 = tmem + kOCol + D;
+    bool ok = mbar_wait_warp(bar(C::bQFull), 0, abort_flag, kTimeoutNs) &&
+              (!two || mbar_wait_warp(bar(C::bQFull + 1), 0, abort_flag, kTimeoutNs));
+    if (ok && n > 0) {
+      ok = mbar_wait_warp(bar(C::bKFull), 0, abort_flag, kTimeoutNs);
+      if (ok) {
+        tc_fence_after();
+        if (leader) {
+          tc::issue_s<D>(tS0, q_desc, k_desc);
+          umma_commit(bar(C::bSFull));
+          if (two) {
+            tc::issue_s<D>(tS1, q_desc + q1_off, k_desc);
+            umma_commit(bar(C::bSFull + 1));
+          }
+        }
+        __syncwarp();
+      }
+    }
+    int ks = 0, kn = 0;                           // slot and use of tile j
+    for (int j = 0; ok && j < n; ++j) {
+      const bool last = j + 1 == n;
+      int nks = ks + 1, nkn = kn;
+      if (nks == C::kKBuf) { nks = 0; ++nkn; }
+      const uint64_t vd = v_desc + (uint64_t)((ks * C::kTileBytes) >> 4);
+      const uint64_t kd = k_desc + (uint64_t)((nks * C::kTileBytes) >> 4);
+      // V_j and K_{j+1} have almost always landed long before P0(j): test all three
+      // at once and wait one by one only when one is missing
+      const uint32_t kb = bar(C::bKFull + (last ? ks : nks));
+      const uint32_t kp = (uint32_t)(last ? kn : nkn) & 1;
+      if (!__all_sync(0xffffffffu,
+                      tc::mbar_test3(bar(C::bVFull + ks), (uint32_t)kn & 1, kb, kp,
+                                     bar(C::bPFull), (uint32_t)j & 1)))
+        ok = mbar_wait_warp(bar(C::bVFull + ks), (uint32_t)kn & 1, abort_flag, kTimeoutNs) &&
+             mbar_wait_warp(kb, kp, abort_flag, kTimeoutNs) &&
+             mbar_wait_warp(bar(C::bPFull), (uint32_t)j & 1, abort_flag, kTimeoutNs);
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
+        tc::issue_pv<D>(tO0, tS0, vd, j > 0);
+        if (last) {
+          umma_commit(bar(C::bODone));
+        } else {
+          tc::issue_s<D>(tS0, q_desc, kd);
+          umma_commit(bar(C::bSFull));
+        }
+      }
+      __syncwarp();
+      if (two) {
+        ok = mbar_wait_warp(bar(C::bPFull + 1), (uint32_t)j & 1, abort_flag, kTimeoutNs);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          tc::issue_pv<D>(tO1, tS1, vd, j > 0);
+          if (last) {
+            umma_commit(bar(C::bODone + 1));
+          } else {
+            tc::issue_s<D>(tS1, q_desc + q1_off, kd);
+            umma_commit(bar(C::bSFull + 1));
+          }
+        }
+        __syncwarp();
+      }
+      ks = nks;
+      kn = nkn;
+    }
+    // all tensor-core work this warp issued has completed before teardown
+    if (leader) {
+      umma_commit(bar(C::bFinal));
+      mbar_wait(bar(C::bFinal), 0, never, kTimeoutNs);
+    }
+    __syncwarp();
+  } else {
+    // ============ softmax: two threads a query row, Q0 and Q1 in turn ============
+    // Warps w and w + 4 share TMEM lane quarter w % 4 (the same 32 rows of each
+    // query tile); part p = w / 4 takes columns [64p, 64p + 64) of S_i and
+    // [pD/2, (p + 1)D/2) of O_i. A row's two partial maxima meet in shared memory at a
+    // named barrier of the pair, which also orders both parts' loads of S before
+    // either writes P over it.
+    const int wq = warp & 3, part = warp >> 2;
+    const int row = wq * 32 + lane;
+    const uint32_t t_lane = (uint32_t)(wq * 32) << 16;
+    const int ntile = two ? 2 : 1;
+    const float sl2 = a.scale_log2;
+    const uint64_t sl2x2 = pack2(sl2, sl2);
+    const uint32_t pair_bar = 1 + wq;
+    float* red = reinterpret_cast<float*>(base_ptr + C::kRedOff);
+    const int tok = row / grp;                    // the row's token in its tile
+    const int shift = 31 - __clz(a.p.page);
+    // no row of the block sees the slots from n_sink to dead_to, nor from sp.hi on
+    const int dead_to = a.window > 0 ? first - a.window + 1 : 0;
+    int ex = 0;                                   // exchanges so far (buffer parity)
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    bool ok = true;
+    const bool relay = warp == 0 && lane == 0;
+    int rd = 0;
+    for (int j = 0; j < n; ++j) {
+      const int lo = tile_lo(j);
+#pragma unroll
+      for (int qi = 0; qi < 2; ++qi) {
+        if (qi >= ntile) break;
+        const uint32_t tS = tmem + t_lane + (uint32_t)(qi * kTile);
+        const int p_first = first + qi * tt;      // the tile's first position
+        float* red_e = red + (ex & 1) * 256;
+        ++ex;
+        if (ok) ok = mbar_wait_warp(bar(C::bSFull + qi), (uint32_t)j & 1, abort_flag, kTimeoutNs);
+        if (!ok) {
+          // keep meeting the partner at every exchange so it never waits alone
+          tc::named_bar_sync(pair_bar, 64);
+          continue;
+        }
+        tc_fence_after();
+        uint32_t uu[2][32];
+        tmem_ld32(tS + part * 64, uu[0]);
+        tmem_ld32(tS + part * 64 + 32, uu[1]);
+        // (the keys have landed: the test makes the producer's note of their pages visible)
+        mbar_test_wait(bar(C::bKFull + j % C::kKBuf), (uint32_t)(j / C::kKBuf) & 1);
+        const uint32_t missing = gone[j & 7];
+        if (relay && qi == ntile - 1) {
+          mbar_arrive(bar(C::bDone + rd));
+          if (++rd == C::kKBuf) rd = 0;
+        }
+        tmem_ld_wait();
+        reg_fence(uu[0]);
+        reg_fence(uu[1]);
+        const bool all = lo + kTile - 1 <= p_first &&
+                         (a.window <= 0 || lo > p_first + tt - 1 - a.window ||
+                          lo + kTile <= a.n_sink);
+        if (!all) {
+          const int q_pos = p_first + tok;
+          const int lim = q_pos - lo + 1 - part * 64;         // columns from lim on are masked
+          if (a.window > 0) {
+            const int w_lo = q_pos - a.window + 1 - lo - part * 64;
+            const int s_hi = a.n_sink - lo - part * 64;       // and those in [s_hi, w_lo)
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c >= lim || (c >= s_hi && c < w_lo)) uu[c / 32][c % 32] = __float_as_uint(-INFINITY);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c >= lim) uu[c / 32][c % 32] = __float_as_uint(-INFINITY);
+          }
+        }
+        if (missing) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (missing >> ((part * 64 + c) >> shift) & 1u)
+              uu[c / 32][c % 32] = __float_as_uint(-INFINITY);
+        }
+        float m8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m8[i] = -INFINITY;
+        tc::max_chunk(uu[0], m8);
+        tc::max_chunk(uu[1], m8);
+        red_e[part * 128 + row] = tc::max8(m8);
+        tc_fence_before();
+        tc::named_bar_sync(pair_bar, 64);
+        tc_fence_after();
+        const float mx = fmaxf(red_e[row], red_e[128 + row]);
+        const float m_new = fmaxf(m_run[qi], mx * sl2);
+        const bool resc = m_new > m_run[qi] + kRescaleLog2;
+        float alpha = 1.f;
+        if (resc) {
+          alpha = ex2_approx(m_run[qi] - m_new);     // 0 when m_run = -inf
+          m_run[qi] = m_new;
+          l_run[qi] *= alpha;
+        }
+        const float m_use = (m_run[qi] == -INFINITY) ? 0.f : m_run[qi];
+        const uint64_t neg_m2 = pack2(-m_use, -m_use);
+        uint64_t sum2a = pack2(0.f, 0.f), sum2b = sum2a;
+        tc::exp_chunk(uu[0], sl2x2, neg_m2, sum2a, sum2b, tS + part * 32);
+        tc::exp_chunk(uu[1], sl2x2, neg_m2, sum2a, sum2b, tS + part * 32 + 16);
+        {
+          float a0, a1;
+          unpack2(fadd2(sum2a, sum2b), a0, a1);
+          l_run[qi] += a0 + a1;
+        }
+        // O_i is scaled before P_i(j) V_j is added to it; PV_i(j-1) is done. Both
+        // parts take the same decision for a row.
+        if (__any_sync(0xffffffffu, resc) && j > 0)
+          tc::scale_cols<D / 2>(tmem + t_lane + kOCol + (uint32_t)(qi * D + part * (D / 2)), alpha);
+        // values that no row of the block sees have weight 0, which NaN would survive
+        if (qi == 0) {
+          const int z0 = max(a.n_sink - lo, 0), z1 = min(dead_to - lo, kTile);
+          const int z2 = max(sp.hi - lo, 0);
+          if (z0 < z1 || z2 < kTile) {
+            const int vs = j % C::kVBuf;
+            ok = mbar_wait_warp(bar(C::bVFull + vs), (uint32_t)(j / C::kVBuf) & 1, abort_flag,
+                                kTimeoutNs);
+            const uint32_t tile = base + C::kVOff + vs * C::kTileBytes;
+            if (ok && z0 < z1) zero_rows(tile, C::kBoxes, z0, z1, threadIdx.x);
+            if (ok && z2 < kTile) zero_rows(tile, C::kBoxes, z2, kTile, threadIdx.x);
+            fence_proxy_async_smem();
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(C::bPFull + qi));
+      }
+    }
+
+    // ---- epilogue: out = O / l, lse = ln2 (m + log2 l), l = sum of both parts
+    float* red_l = red + 512;
+    for (int qi = 0; qi < ntile; ++qi) red_l[(qi * 2 + part) * 128 + row] = l_run[qi];
+    tc::named_bar_sync(pair_bar, 64);
+    for (int qi = 0; qi < ntile; ++qi) {
+      const float ls = red_l[qi * 256 + row] + red_l[qi * 256 + 128 + row];
+      const int t = t0 + qi * tt + tok;
+      const bool valid = tok < tt && t < t0 + n_tok;
+      if (ok && n > 0) {
+        ok = mbar_wait_warp(bar(C::bODone + qi), 0, abort_flag, kTimeoutNs);
+        tc_fence_after();
+      }
+      if (!ok) break;
+      const int h = hk * grp + row % grp;
+      const long long orow = (long long)(sq.row0 + t) * a.H_q + h;
+      const uint32_t tO = tmem + t_lane + kOCol + (uint32_t)(qi * D + part * (D / 2));
+      const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);   // 0: no slot; NaN stays
+      const long long prow = (long long)split * a.rows * a.H_q + orow;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t uo[32];
+        if (n > 0) {
+          tmem_ld32(tO + c * 32, uo);
+          tmem_ld_wait(uo);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) uo[i] = 0u;
+        }
+        if (!valid) continue;
+        const int col = part * (D / 2) + c * 32;
+        if (a.n_split > 1) {
+          if (n == 0) continue;
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + col);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_uint4(uo[4 * i], uo[4 * i + 1], uo[4 * i + 2], uo[4 * i + 3]);
+        } else if (in_range(orow * D + col, 32, (long long)a.rows * a.H_q * D, a.status)) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + col);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              w[x] = pack_bf16x2(__uint_as_float(uo[8 * i + 2 * x]) * inv,
+                                 __uint_as_float(uo[8 * i + 2 * x + 1]) * inv);
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (valid && part == 0) {
+        if (a.n_split > 1) {
+          a.part_ml[2 * prow] = ls == 0.f ? -INFINITY : m_run[qi];
+          a.part_ml[2 * prow + 1] = ls;
+        } else if (a.lse) {
+          const long long at = paged_lse_at(a, b, sq.row0 + t, t, h);
+          if (in_range(at, 1, (long long)a.rows * a.H_q, a.status))
+            a.lse[at] = ls == 0.f ? -INFINITY : (m_run[qi] + log2f(ls)) * kLn2;
+        }
+      }
+    }
+  }
+
+  // ---- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && (*abort_flag || *never) && a.status)
+    atomicExch(a.status, (int)RA_ERR_TIMEOUT);
+}
+
+// 8-bit pages to bf16 tiles [B][n_expanded][H_kv][128][D], keys and values: the
+// tiles that the sequences' new tokens see, in order; slots past the last and those
+// that no token sees as zeros. A CTA makes one tile of one head, 16 values a thread
+// and step. Bound by the bytes.
+constexpr int kExpandThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kExpandThreads)
+paged_expand_kernel(const PagedAttnArgs a) {
+  const int hk = blockIdx.x % a.p.H_kv;
+  const int rest = blockIdx.x / a.p.H_kv;
+  const int v = rest % a.n_expanded, b = rest / a.n_expanded;
+  const PagedSeq sq = paged_seq(a, b);
+  if (sq.n <= 0) return;
+  const PagedSpan<kTile> sp = sequence_span(a, sq);
+  if (v >= sp.n) return;
+  const int lo = sp.tile(v) * kTile;
+  const int shift = 31 - __clz(a.p.page);
+  constexpr int kLanes = D / 16;                 // threads a row
+  const size_t tile = (size_t)blockIdx.x;        // ((b, v), hk) in order
+#pragma unroll
+  for (int i = threadIdx.x; i < kTile * kLanes; i += kExpandThreads) {
+    const int r = i / kLanes, d = (i % kLanes) * 16;
+    const int slot = lo + r;
+    long long from = -1;
+    if (slot < sp.hi && sp.meets(a, slot, 1) && (slot >> shift) < a.width) {
+      const int id = __ldg(a.table + (size_t)b * a.width + (slot >> shift));
+      if (id >= 0 && id < a.p.n_pages)
+        from = (((long long)id * a.p.H_kv + hk) << shift) + (slot & (a.p.page - 1));
+    }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      uint32_t w[8] = {};
+      if (from >= 0) {
+        const uint4 c = *reinterpret_cast<const uint4*>((side ? a.p.v : a.p.k) + from * D + d);
+        const float scale = pow2_byte((side ? a.p.vs : a.p.ks)[from]);
+        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float2 f = half2_values(e4m3x2_half2(cw[x / 2] >> (16 * (x % 2))));
+          w[x] = pack_bf16x2(f.x * scale, f.y * scale);
+        }
+      }
+      uint4* dst = reinterpret_cast<uint4*>((side ? a.expanded_v : a.expanded_k) +
+                                            (tile * kTile + r) * D + d);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
+template <int D, bool kExpanded>
+ra_status launch_tiles(const PagedAttnArgs& a, cudaStream_t stream) {
+  const int grp = a.H_q / a.p.H_kv, tt = kTile / grp;
+  CUtensorMap mq, mk, mv;
+  PagePool p = a.p;
+  if (kExpanded) {
+    const long long blocks = (long long)a.B * a.n_expanded * a.p.H_kv;
+    if (blocks > 0x7fffffffLL) return RA_ERR_RANGE;
+    paged_expand_kernel<D><<<(unsigned)blocks, kExpandThreads, 0, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
+    p.k = reinterpret_cast<uint8_t*>(a.expanded_k);
+    p.v = reinterpret_cast<uint8_t*>(a.expanded_v);
+    p.n_pages = a.B * a.n_expanded;
+    p.page = kTile;
+    p.quant = 0;
+  }
+  if (!make_query_map(&mq, a.q, a.rows, a.H_q, D, grp, tt) ||
+      !make_page_map(&mk, p, p.k, p.page) || !make_page_map(&mv, p, p.v, p.page))
+    return RA_ERR_LAUNCH;
+  const long long grid = (long long)a.B * a.p.H_kv * a.n_rb * a.n_split;
+  if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
+  auto kern = paged_tiles_kernel<D, kExpanded>;
+  static std::atomic<uint64_t> allowed;
+  if (!allow_smem(kern, Cfg<D>::kSmemBytes, allowed)) return RA_ERR_LAUNCH;
+  kern<<<(unsigned)grid, kThreads, Cfg<D>::kSmemBytes, stream>>>(mq, mk, mv, a);
+  return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+ra_status launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t stream) {
+  if (a.p.D == 64)
+    return a.p.quant ? launch_tiles<64, true>(a, stream) : launch_tiles<64, false>(a, stream);
+  return a.p.quant ? launch_tiles<128, true>(a, stream) : launch_tiles<128, false>(a, stream);
+}
+
+}  // namespace ra
