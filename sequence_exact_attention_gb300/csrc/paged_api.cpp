@@ -94,8 +94,8 @@ ra_status append(const ra_pages* pages, const int* table, int width, const void*
 }
 
 // Sizes of an attention call, brought to the form the plan wants.
-ra_status attn_sizes(const ra_pages& p, int B, int T, long long rows, int H_q, int max_len,
-                     int window, int n_sink, PagedAttnArgs* a) {
+ra_status attn_sizes(const ra_pages& p, bool varlen, int B, int T, long long rows, int H_q,
+                     int max_len, int window, int n_sink, PagedAttnArgs* a) {
   if (B <= 0 || T <= 0 || rows <= 0 || H_q <= 0) return RA_ERR_SHAPE;
   if (H_q % p.H_kv != 0 || H_q / p.H_kv > 128) return RA_ERR_SHAPE;
   if (max_len <= 0 || max_len > (1 << 30) || window < 0 || n_sink < 0) return RA_ERR_RANGE;
@@ -107,6 +107,7 @@ ra_status attn_sizes(const ra_pages& p, int B, int T, long long rows, int H_q, i
   a->B = B;
   a->T = T;
   a->rows = (int)rows;
+  a->packed = varlen;
   a->H_q = H_q;
   a->max_len = max_len;
   // a window that no query leaves is none
@@ -124,7 +125,7 @@ ra_status attn(const void* q, const ra_pages* pages, const int* table, int width
   ra_status st = check_pages(pages, table, width);
   if (st != RA_OK) return st;
   PagedAttnArgs a = {};
-  st = attn_sizes(*pages, B, T, rows, H_q, max_len, window, n_sink, &a);
+  st = attn_sizes(*pages, varlen, B, T, rows, H_q, max_len, window, n_sink, &a);
   if (st != RA_OK) return st;
   if (max_len > (long long)width * pages->page) return RA_ERR_RANGE;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16)) return RA_ERR_ALIGN;
@@ -218,8 +219,8 @@ ra_status paged_attn_workspace(const ra_pages* pages, int B, int S_q, int total,
   ra_status st = check_sizes(pages);
   if (st != RA_OK) return st;
   PagedAttnArgs a = {};
-  st = attn_sizes(*pages, B, S_q, varlen ? total : (long long)B * S_q, H_q, max_len, window,
-                  n_sink, &a);
+  st = attn_sizes(*pages, varlen != 0, B, S_q, varlen ? total : (long long)B * S_q, H_q, max_len,
+                  window, n_sink, &a);
   if (st != RA_OK) return st;
   return paged_attn_plan(&a, bytes);
 }

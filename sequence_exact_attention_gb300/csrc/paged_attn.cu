@@ -14,8 +14,10 @@
 // in base 2, with a maximum m' of their own: the row's largest weight is between
 // 1 and 2^5, whatever the scales. Queries become halves times a power of two a row
 // (exact for values down to 2^-17 of the row's largest).
-// Roundings: weights to half (2^-12) or, in bf16 pages, to bf16 (2^-9); sums and
-// statistics are float32.
+// Roundings: weights to half (2^-11 of a weight at most). A bf16 page's values may
+// pass half's range, so there a weight is the sum of two bf16 numbers (2^-16) in two
+// products (one, rounded at 2^-8, made the error against 64 bits 2.3e-3 where the
+// outputs' rounding alone makes 1.7e-3). Sums and statistics are float32.
 //
 // For up to 16 query rows a sequence and key/value head (new tokens times the heads
 // that share it; more: paged_tiles.cu). A CTA takes one chunk of the slots of one
@@ -27,8 +29,9 @@
 //
 // Slots that a row does not see change no bit of its results, whatever they hold:
 // scores are replaced, and in tiles that are not whole the values' operands are
-// masked, too (0 times a NaN is not 0); where the block's tokens differ in what
-// they see, such a tile is multiplied once for each of them.
+// masked, too (0 times a NaN is not 0); where tokens differ in what they see and a
+// value is not finite, such a tile is multiplied once for each of them (always doing
+// so took 26 instead of 20 us for 4 x 4 tokens under a window of 4096).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -129,7 +132,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   using S = Smem<D, NT, kQuant>;
   constexpr int kTile = S::kTile;
   constexpr int WS = kTile / kWarps;        // slots a warp
-  constexpr int MB = WS / 16;
+  static_assert(WS % 16 == 0, "products of 16 slots");
   constexpr int RB = 8 * NT;                // query rows, at most
   constexpr int KS = D / 16;                // steps of 16 dimensions
   extern __shared__ uint8_t smem_raw[];
@@ -147,9 +150,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int H_kv = a.p.H_kv, grp = a.H_q / H_kv;
-  const int split = blockIdx.x % a.n_split;
-  const int bh = blockIdx.x / a.n_split;
-  const int hk = bh % H_kv, b = bh / H_kv;
+  const PagedWork work = paged_work(a, blockIdx.x);
+  const int b = work.item / H_kv, hk = work.item % H_kv;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       sm100::mbar_init(full + 8 * i, 1);
@@ -164,8 +166,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int first = sq.len - sq.n;          // position of the first new token
   PagedSpan<kTile> sp;
   sp.init(a, first, first + sq.n - 1);
-  const int v_begin = split * a.chunk;
-  const int n_tiles = max(min(sp.n, v_begin + a.chunk) - v_begin, 0);
+  const int v_begin = max(work.split, 0) * a.chunk;
+  const int n_tiles = max((work.split < 0 ? sp.n : min(sp.n, v_begin + a.chunk)) - v_begin, 0);
   let_dependents_start();
   __syncthreads();
 
@@ -314,6 +316,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
     };
 
+    // the largest of a row's values, which the lanes of equal c hold
+    auto row_max = [](float x) {
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+      return x;
+    };
+    constexpr int kSteps = kQuant ? KS / 2 : KS, kPer = kQuant ? 2 : 1;
+    const int box_shift = 31 - __clz(min(a.p.page, kTile));
+
     int stage = 0;
     uint32_t phase = 0;
     for (int it = 0; it < n_tiles; ++it) {
@@ -321,26 +332,28 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (!__all_sync(0xffffffffu, sm100::mbar_test_wait(full + 8 * stage, phase)) &&
           !sm100::mbar_wait_warp(full + 8 * stage, phase, abort_flag, kTimeoutNs))
         break;
-      const int w0 = WS * warp;              // the warp's first slot in the tile
-      const int j0 = sp.tile(v_begin + it) * kTile + w0;
       const uint32_t tile = ring + stage * S::kStage;
       const uint32_t missing = gone[stage];
-      // ---- scores: rows of s are slots, columns query rows
-      float s[MB][NT][4];
-      int ev[MB][2];                         // the value scales' exponents
-#pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        const int slot = w0 + 16 * m + (lane & 15);
+      // 16 slots at a time, in a loop that is not unrolled: code that a short call runs
+      // once or twice costs it more to fetch than to run (two blocks side by side took
+      // 20 instead of 17 us for 4 x 4 tokens under a window of 4096)
+#pragma unroll 1
+      for (int w0 = WS * warp; w0 < WS * (warp + 1); w0 += 16) {
+        const int j0 = sp.tile(v_begin + it) * kTile + w0;
+        // ---- scores: rows of s are slots, columns query rows
+        float s[NT][4];
+        int ev[2];                           // the value scales' exponents
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[m][nt][i] = 0.f;
+          for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+        const int slot = w0 + (lane & 15);
         if constexpr (kQuant) {
           float ks[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            ks[i] = pow2_byte(smem[stage * S::kStage + S::kKs + w0 + 16 * m + 8 * i + g]);
-            ev[m][i] = (int)smem[stage * S::kStage + S::kVs + w0 + 16 * m + 8 * i + g] - 127;
+            ks[i] = pow2_byte(smem[stage * S::kStage + S::kKs + w0 + 8 * i + g]);
+            ev[i] = (int)smem[stage * S::kStage + S::kVs + w0 + 8 * i + g] - 127;
           }
 #pragma unroll
           for (int x = 0; x < KS / 2; ++x) {   // two chunks of 16 dimensions
@@ -353,13 +366,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
                                       e4m3x2_half2(w[2 * y + 1] >> 16)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma16816<true>(s[m][nt], af, qf[nt][2 * x + y][0], qf[nt][2 * x + y][1]);
+                mma16816<true>(s[nt], af, qf[nt][2 * x + y][0], qf[nt][2 * x + y][1]);
             }
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[m][nt][i] *= ks[i >> 1] * sl2[nt][i & 1];
+            for (int i = 0; i < 4; ++i) s[nt][i] *= ks[i >> 1] * sl2[nt][i & 1];
         } else {
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
@@ -368,82 +381,70 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
                               swizzled<S::kRowBytes>(slot, 2 * (k % 4) + (lane >> 4)));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816<false>(s[m][nt], af, qf[nt][k][0], qf[nt][k][1]);
+              mma16816<false>(s[nt], af, qf[nt][k][0], qf[nt][k][1]);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[m][nt][i] *= sl2[nt][i & 1];
+            for (int i = 0; i < 4; ++i) s[nt][i] *= sl2[nt][i & 1];
         }
-      }
-      // ---- tiles that some row does not see in full
-      const int box_shift = 31 - __clz(min(a.p.page, kTile));
-      const bool whole = missing == 0 && sp.whole(a, j0, WS);
-      if (!whole) {
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
+        // ---- slots that some row does not see
+        const bool whole = missing == 0 && sp.whole(a, j0, 16);
+        if (!whole) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int x = 16 * m + 8 * i + g;
+            const int x = 8 * i + g;
             const bool lost = missing >> ((w0 + x) >> box_shift) & 1u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                if (lost || !paged_sees(a, pos[nt][h], j0 + x)) s[m][nt][2 * i + h] = -INFINITY;
+                if (lost || !paged_sees(a, pos[nt][h], j0 + x)) s[nt][2 * i + h] = -INFINITY;
           }
-      }
-      // ---- raise the maxima when a score passes its bound: rare after the first tile
-      float top[NT][2], top2[NT][2];
-      bool raise = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          top[nt][h] = top2[nt][h] = -INFINITY;
-#pragma unroll
-          for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float x = s[m][nt][2 * i + h];
-              top[nt][h] = fmaxf(top[nt][h], x);
-              if (kQuant) top2[nt][h] = fmaxf(top2[nt][h], x + (float)ev[m][i]);
-            }
-          raise |= top[nt][h] > bound[nt][h];
-          if (kQuant) raise |= top2[nt][h] > bound2[nt][h];
         }
-      if (__any_sync(0xffffffffu, raise)) {
+        // ---- raise the maxima when a score passes its bound: rare after the first tile
+        float top[NT][2], top2[NT][2];
+        bool raise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float x = top[nt][h], y = top2[nt][h];
-#pragma unroll
-            for (int d = 4; d < 32; d *= 2) {
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-              if (kQuant) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-            }
-            if (x > bound[nt][h]) {
-              const float to = floorf(x);
-              const float alpha = bound[nt][h] == -INFINITY ? 0.f : exp2f(sub[nt][h] - to);
-              sub[nt][h] = to;
-              bound[nt][h] = to + kRescaleLog2;
-              l[nt][h] *= alpha;
-              if (!kQuant) scale_row(nt, h, alpha);
-            }
-            if (kQuant && y > bound2[nt][h]) {
-              const float to = floorf(y);
-              const float alpha = bound2[nt][h] == -INFINITY ? 0.f : exp2f(sub2[nt][h] - to);
-              sub2[nt][h] = to;
-              bound2[nt][h] = to + kRescaleLog2;
-              scale_row(nt, h, alpha);
+            top[nt][h] = fmaxf(s[nt][h], s[nt][2 + h]);
+            raise |= top[nt][h] > bound[nt][h];
+            if (kQuant) {
+              top2[nt][h] = fmaxf(s[nt][h] + (float)ev[0], s[nt][2 + h] + (float)ev[1]);
+              raise |= top2[nt][h] > bound2[nt][h];
             }
           }
-      }
-      // ---- weights, as B operands
-      uint32_t pf[MB][NT][2];
+        if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float x = row_max(top[nt][h]);
+              if (x > bound[nt][h]) {
+                const float to = floorf(x);
+                const float alpha = bound[nt][h] == -INFINITY ? 0.f : exp2f(sub[nt][h] - to);
+                sub[nt][h] = to;
+                bound[nt][h] = to + kRescaleLog2;
+                l[nt][h] *= alpha;
+                if (!kQuant) scale_row(nt, h, alpha);
+              }
+              if constexpr (kQuant) {
+                const float y = row_max(top2[nt][h]);
+                if (y > bound2[nt][h]) {
+                  const float to = floorf(y);
+                  const float alpha = bound2[nt][h] == -INFINITY ? 0.f : exp2f(sub2[nt][h] - to);
+                  sub2[nt][h] = to;
+                  bound2[nt][h] = to + kRescaleLog2;
+                  scale_row(nt, h, alpha);
+                }
+              }
+            }
+        }
+        // ---- weights, as B operands: one half, or two bf16 numbers, what the first
+        // leaves being the second
+        uint32_t pf[NT][2], pl[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -451,82 +452,118 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
             float w[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float x = s[m][nt][2 * i + h];
+              const float x = s[nt][2 * i + h];
               const float p = sm100::ex2_approx(x - sub[nt][h]);
               l[nt][h] += p;
-              w[h] = kQuant ? sm100::ex2_approx(x + ((float)ev[m][i] - sub2[nt][h])) : p;
+              w[h] = kQuant ? sm100::ex2_approx(x + ((float)ev[i] - sub2[nt][h])) : p;
             }
-            pf[m][nt][i] = transpose8x8(kQuant ? pack_half2(w[0], w[1])
-                                               : sm100::pack_bf16x2(w[0], w[1]));
-          }
-      // ---- their products with the values: rows of o are dimensions. p: the
-      // position whose rows alone count, with the slots that it sees; below 0: all
-      auto add_values = [&](int p) {
-#pragma unroll
-        for (int m = 0; m < MB; ++m) {
-          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};     // slots 2c, 2c + 1, and + 8
-          // o += v w of one product, for the rows that count
-          auto add = [&](int nt, int k, const uint32_t (&af)[4]) {
-            if (p < 0) {
-              mma16816<kQuant>(o[nt][k], af, pf[m][nt][0], pf[m][nt][1]);
+            if constexpr (kQuant) {
+              pf[nt][i] = transpose8x8(pack_half2(w[0], w[1]));
             } else {
-              float y[4] = {o[nt][k][0], o[nt][k][1], o[nt][k][2], o[nt][k][3]};
-              mma16816<kQuant>(y, af, pf[m][nt][0], pf[m][nt][1]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (pos[nt][i & 1] == p) o[nt][k][i] = y[i];
-            }
-          };
-          if (p >= 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              keep[i] = 0;
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const int x = 16 * m + 8 * i + 2 * c + y;
-                if (!(missing >> ((w0 + x) >> box_shift) & 1u) && paged_sees(a, p, j0 + x))
-                  keep[i] |= 0xffffu << (16 * y);
-              }
+              const uint32_t u = sm100::pack_bf16x2(w[0], w[1]);
+              pf[nt][i] = transpose8x8(u);
+              pl[nt][i] = transpose8x8(sm100::pack_bf16x2(
+                  w[0] - __uint_as_float(u << 16), w[1] - __uint_as_float(u & 0xffff0000u)));
             }
           }
+        // ---- their products with the values: rows of o are dimensions
+        // the halves of slots 2c, 2c + 1, and + 8 to keep: those that the row at p, or
+        // (kAny) any row, sees
+        constexpr int kAny = -1;
+        auto keep_slots = [&](int p, uint32_t (&keep)[2]) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            keep[i] = 0;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int x = 8 * i + 2 * c + y;
+              const bool see = p == kAny ? j0 + x < sp.hi && sp.meets(a, j0 + x, 1)
+                                         : paged_sees(a, p, j0 + x);
+              if (!(missing >> ((w0 + x) >> box_shift) & 1u) && see) keep[i] |= 0xffffu << (16 * y);
+            }
+          }
+        };
+        // the operand of the 16 slots and of 16 dimensions (8 bits: two steps' at once)
+        auto load_values = [&](int k, const uint32_t (&keep)[2], uint32_t (&af)[kPer][4]) {
           if constexpr (kQuant) {
-            const int slot = w0 + 16 * m + (lane & 15);
+            uint32_t w[4];
+            ldmatrix4_trans(w, tile + S::kKv + swizzled<S::kRowBytes>(slot, 2 * k + (lane >> 4)));
 #pragma unroll
-            for (int x = 0; x < KS / 2; ++x) {
-              uint32_t w[4];
-              ldmatrix4_trans(w, tile + S::kKv +
-                                     swizzled<S::kRowBytes>(slot, 2 * x + (lane >> 4)));
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                // bytes: (slot 2c, dimensions 2g, 2g + 1), (slot 2c + 1, the same)
-                const uint32_t lo = __byte_perm(w[2 * y], 0, 0x3120);
-                const uint32_t hi = __byte_perm(w[2 * y + 1], 0, 0x3120);
-                const uint32_t af[4] = {e4m3x2_half2(lo) & keep[0], e4m3x2_half2(lo >> 16) & keep[0],
-                                        e4m3x2_half2(hi) & keep[1], e4m3x2_half2(hi >> 16) & keep[1]};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  add(nt, 2 * x + y, af);
-              }
+            for (int y = 0; y < 2; ++y) {
+              // bytes: (slot 2c, dimensions 2g, 2g + 1), (slot 2c + 1, the same)
+              const uint32_t lo = __byte_perm(w[2 * y], 0, 0x3120);
+              const uint32_t hi = __byte_perm(w[2 * y + 1], 0, 0x3120);
+              af[y][0] = e4m3x2_half2(lo) & keep[0];
+              af[y][1] = e4m3x2_half2(lo >> 16) & keep[0];
+              af[y][2] = e4m3x2_half2(hi) & keep[1];
+              af[y][3] = e4m3x2_half2(hi >> 16) & keep[1];
             }
           } else {
-            const int slot = w0 + 16 * m + (lane & 7) + ((lane & 16) >> 1);
+            const int row = w0 + (lane & 7) + ((lane & 16) >> 1);
+            ldmatrix4_trans(af[0], tile + S::kKv + (k / 4) * S::kPart +
+                                       swizzled<S::kRowBytes>(row, 2 * (k % 4) + ((lane >> 3) & 1)));
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              uint32_t af[4];
-              ldmatrix4_trans(af, tile + S::kKv + (k / 4) * S::kPart +
-                                      swizzled<S::kRowBytes>(slot, 2 * (k % 4) + ((lane >> 3) & 1)));
+            for (int x = 0; x < 4; ++x) af[0][x] &= keep[x >> 1];
+          }
+        };
+        auto multiply = [&](float (&acc)[4], const uint32_t (&af)[4], int nt) {
+          mma16816<kQuant>(acc, af, pf[nt][0], pf[nt][1]);
+          if (!kQuant) mma16816<kQuant>(acc, af, pl[nt][0], pl[nt][1]);
+        };
+        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+        bool apart = false;
+        if (!whole) {
+          keep_slots(kAny, keep);
+          // where tokens differ in what they see, a value that is not finite would reach
+          // the rows that do not see it
+          if (sp.pmin != sp.pmax) {
+#pragma unroll 1
+            for (int k = 0; k < kSteps; ++k) {
+              uint32_t af[kPer][4];
+              load_values(k, keep, af);
+              constexpr uint32_t ones = kQuant ? 0x7c007c00u : 0x7f807f80u;   // exponents
 #pragma unroll
-              for (int x = 0; x < 4; ++x) af[x] &= keep[x >> 1];
+              for (int x = 0; x < kPer; ++x)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) add(nt, k, af);
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t u = af[x][i] & ones;
+                  apart |= (u & 0xffffu) == (ones & 0xffffu) || (u >> 16) == (ones >> 16);
+                }
+            }
+            apart = __any_sync(0xffffffffu, apart);
+          }
+        }
+        if (!apart) {
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t af[kPer][4];
+            load_values(k, keep, af);
+#pragma unroll
+            for (int x = 0; x < kPer; ++x)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) multiply(o[nt][kPer * k + x], af[x], nt);
+          }
+        } else {
+          for (int p = max(sp.pmin, 0); p <= sp.pmax; ++p) {
+            keep_slots(p, keep);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+              uint32_t af[kPer][4];
+              load_values(k, keep, af);
+#pragma unroll
+              for (int x = 0; x < kPer; ++x)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  float(&acc)[4] = o[nt][kPer * k + x];
+                  float y[4] = {acc[0], acc[1], acc[2], acc[3]};
+                  multiply(y, af[x], nt);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    if (pos[nt][i & 1] == p) acc[i] = y[i];
+                }
             }
           }
         }
-      };
-      if (whole) {
-        add_values(-1);
-      } else {
-        for (int p = max(sp.pmin, 0); p <= sp.pmax; ++p) add_values(p);
       }
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(free_ + 8 * stage);
@@ -590,8 +627,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     const int t = r / grp, h = hk * grp + r % grp;
     const long long row = (long long)(sq.row0 + t) * a.H_q + h;
-    if (a.n_split > 1) {
-      const long long part = (long long)split * a.rows * a.H_q + row;
+    if (work.split >= 0) {
+      const long long part = paged_part(a, work.item, work.split, r);
       if (d == 0) {
         a.part_ml[2 * part] = mx;
         a.part_ml[2 * part + 1] = ls;
@@ -612,76 +649,145 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
 }
 
-// Joins the chunks of one query row: the warps share the chunks, a warp's lanes
-// the row's D values. A chunk without a visible slot has the sum 0.
-constexpr int kJoinWarps = 4;
+// ---- Joining chunks. A chunk without a visible slot has the sum 0, and outputs that
+// nobody wrote: they may be read, never used.
+
+__device__ __forceinline__ float chunk_weight(float2 ml, float m) {     // below 0: nothing there
+  if (ml.x == -INFINITY && ml.y == 0.f) return -1.f;
+  return ml.x == m ? 1.f : exp2f(ml.x - m);
+}
+
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-paged_join_kernel(const PagedAttnArgs a) {
-  constexpr int V = D / 32;                  // values a lane
-  __shared__ float sO[kJoinWarps][D], sM[kJoinWarps], sL[kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = blockIdx.x;          // (token row, head)
-  const int tok = (int)(row / a.H_q), h = (int)(row % a.H_q);
+__device__ __forceinline__ void store_row(const PagedAttnArgs& a, const PagedBlock& blk,
+                                          const PagedSeq& sq, int t, int g, int d, float4 y,
+                                          float m, float l) {
+  const int h = blk.hk * (a.H_q / a.p.H_kv) + g;
+  const long long row = (long long)(sq.row0 + t) * a.H_q + h;
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);     // 0: no slot; NaN stays
+  if (in_range(row * D + d, 4, (long long)a.rows * a.H_q * D, a.status))
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d) =
+        make_uint2(sm100::pack_bf16x2(y.x * inv, y.y * inv), sm100::pack_bf16x2(y.z * inv, y.w * inv));
+  if (d == 0 && a.lse) {
+    const long long at = paged_lse_at(a, blk.b, sq.row0 + t, t, h);
+    if (in_range(at, 1, (long long)a.rows * a.H_q, a.status))
+      a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
+// Few rows: a CTA joins one row, whose chunks may be hundreds: its parts, each D / 4
+// threads, a float4 of the output a thread, take every kParts-th chunk.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+paged_join_few_kernel(const PagedAttnArgs a, int rows) {
+  constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes;
+  __shared__ float4 sO[kParts][kLanes];
+  __shared__ float sM[kParts], sL[kParts];
   let_dependents_start();
+  const int item = (int)(blockIdx.x / (uint32_t)rows), r = (int)(blockIdx.x % (uint32_t)rows);
+  const PagedBlock blk = paged_block(a, item);
+  const int grp = a.H_q / a.p.H_kv;
+  const PagedSeq sq = paged_seq(a, blk.b);
   wait_for_prior_grid();
-  // the token's sequence; rows behind the last one stay as they are
-  int b, t;
-  if (a.cu) {
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(a.cu + mid) <= tok) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-    const PagedSeq sq = paged_seq(a, b);
-    t = tok - sq.row0;
-    if (t < 0 || t >= sq.n) return;
-  } else {
-    b = tok / a.T;
-    t = tok % a.T;
+  if (r / grp >= sq.n) return;
+  const int part = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + paged_part(a, item, 0, r);
+  const float* o = a.part_o + paged_part(a, item, 0, r) * D + d;
+  float m = -INFINITY, l = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = part; s < a.n_split; s += kParts) m = fmaxf(m, ml[s * a.block_rows].x);
+#pragma unroll 4
+  for (int s = part; s < a.n_split; s += kParts) {
+    const float2 x = ml[s * a.block_rows];
+    const float4 f = *reinterpret_cast<const float4*>(o + (size_t)s * a.block_rows * D);
+    const float w = chunk_weight(x, m);
+    if (w < 0.f) continue;
+    l = fmaf(w, x.y, l);
+    y.x = fmaf(w, f.x, y.x);
+    y.y = fmaf(w, f.y, y.y);
+    y.z = fmaf(w, f.z, y.z);
+    y.w = fmaf(w, f.w, y.w);
   }
-  const long long stride = (long long)a.rows * a.H_q;
-  float y[V], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) y[i] = 0.f;
-  for (int s = warp; s < a.n_split; s += kJoinWarps) {
-    const long long part = s * stride + row;
-    const float pm = a.part_ml[2 * part], pl = a.part_ml[2 * part + 1];
-    if (pm == -INFINITY && pl == 0.f) continue;
-    const float mn = fmaxf(m, pm);
-    const float f0 = m == -INFINITY ? 0.f : exp2f(m - mn), f1 = pm == mn ? 1.f : exp2f(pm - mn);
-    l = l * f0 + pl * f1;
-#pragma unroll
-    for (int i = 0; i < V; ++i) y[i] = y[i] * f0 + a.part_o[part * D + i * 32 + lane] * f1;
-    m = mn;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) sO[warp][i * 32 + lane] = y[i];
-  if (lane == 0) {
-    sM[warp] = m;
-    sL[warp] = l;
+  sO[part][d / 4] = y;
+  if (d == 0) {
+    sM[part] = m;
+    sL[part] = l;
   }
   __syncthreads();
-  if (threadIdx.x >= D) return;
-  float mx = -INFINITY, ls = 0.f, z = 0.f;
+  if (part > 0) return;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, sM[w]);
+  for (int w = 1; w < kParts; ++w) m = fmaxf(m, sM[w]);
+  l = 0.f;
+  y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    if (sM[w] == -INFINITY && sL[w] == 0.f) continue;
-    const float f = sM[w] == mx ? 1.f : exp2f(sM[w] - mx);
-    ls = fmaf(f, sL[w], ls);
-    z = fmaf(f, sO[w][threadIdx.x], z);
+  for (int w = 0; w < kParts; ++w) {
+    const float f = chunk_weight(make_float2(sM[w], sL[w]), m);
+    if (f < 0.f) continue;
+    const float4 x = sO[w][d / 4];
+    l = fmaf(f, sL[w], l);
+    y.x = fmaf(f, x.x, y.x);
+    y.y = fmaf(f, x.y, y.y);
+    y.z = fmaf(f, x.z, y.z);
+    y.w = fmaf(f, x.w, y.w);
   }
-  const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
-  if (in_range(row * D + threadIdx.x, 1, (long long)a.rows * a.H_q * D, a.status))
-    static_cast<__nv_bfloat16*>(a.out)[row * D + threadIdx.x] = __float2bfloat16_rn(z * inv);
-  if (threadIdx.x == 0 && a.lse) {
-    const long long at = paged_lse_at(a, b, tok, t, h);
-    if (in_range(at, 1, (long long)a.rows * a.H_q, a.status))
-      a.lse[at] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * kLn2;
+  store_row<D>(a, blk, sq, r / grp, r % grp, d, y, m, l);
+}
+
+// Many rows: a CTA joins `rows` rows of one block (a power of two), first all their
+// weights, then all their outputs, so that what it looks up and waits for comes once.
+// (A warp for every row took 25 us of 19456 rows of two chunks, a CTA 32.)
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+paged_join_many_kernel(const PagedAttnArgs a, int rows) {
+  extern __shared__ float2 sW[];             // [n_split][rows] (weight, sum), [rows] (maximum, sum)
+  let_dependents_start();
+  const int per = a.block_rows / rows;
+  const int item = a.n_whole + blockIdx.x / per, r0 = blockIdx.x % per * rows;
+  const PagedBlock blk = paged_block(a, item);
+  if (blk.b < 0) return;                     // past the last block of the batch
+  const int grp = a.H_q / a.p.H_kv, tt = 128 / grp;
+  const PagedSeq sq = paged_seq(a, blk.b);
+  wait_for_prior_grid();
+  // row r's token; below 0: it has none
+  auto token = [&](int r) -> int {
+    const int t = (2 * blk.rb + (r >> 7)) * tt + (r & 127) / grp;
+    return (r & 127) < tt * grp && t < sq.n ? t : -1;
+  };
+  for (int i = threadIdx.x; i < rows * a.n_split; i += kJoinThreads) {
+    const int s = i / rows, r = i & (rows - 1);
+    sW[i] = token(r0 + r) < 0 ? make_float2(-INFINITY, 0.f)
+                              : reinterpret_cast<const float2*>(a.part_ml)[paged_part(a, item, s, r0 + r)];
+  }
+  __syncthreads();
+  if (threadIdx.x < rows) {
+    float m = -INFINITY, l = 0.f;
+    for (int s = 0; s < a.n_split; ++s) m = fmaxf(m, sW[s * rows + threadIdx.x].x);
+    for (int s = 0; s < a.n_split; ++s) {
+      float2& x = sW[s * rows + threadIdx.x];
+      x.x = chunk_weight(x, m);
+      if (!(x.x < 0.f)) l = fmaf(x.x, x.y, l);
+    }
+    sW[a.n_split * rows + threadIdx.x] = make_float2(m, l);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * (D / 4); i += kJoinThreads) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    const int t = token(r0 + r);
+    if (t < 0) continue;
+    const float* o = a.part_o + paged_part(a, item, 0, r0 + r) * D + d;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < a.n_split; ++s) {
+      const float4 f = *reinterpret_cast<const float4*>(o + (size_t)s * a.block_rows * D);
+      const float w = sW[s * rows + r].x;
+      if (w < 0.f) continue;
+      y.x = fmaf(w, f.x, y.x);
+      y.y = fmaf(w, f.y, y.y);
+      y.z = fmaf(w, f.z, y.z);
+      y.w = fmaf(w, f.w, y.w);
+    }
+    const float2 ml = sW[a.n_split * rows + r];
+    store_row<D>(a, blk, sq, t, ((r0 + r) & 127) % grp, d, y, ml.x, ml.y);
   }
 }
 
@@ -692,7 +798,7 @@ ra_status launch_rows(const PagedAttnArgs& a, cudaStream_t stream) {
   const int box_rows = a.p.page < S::kTile ? a.p.page : S::kTile;
   if (!make_page_map(&mk, a.p, a.p.k, box_rows) || !make_page_map(&mv, a.p, a.p.v, box_rows))
     return RA_ERR_LAUNCH;
-  const long long grid = (long long)a.B * a.p.H_kv * a.n_split;
+  const long long grid = (long long)a.n_items * a.n_split;
   if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
   auto kern = paged_attn_kernel<D, NT, kQuant>;
   static std::atomic<uint64_t> allowed;
@@ -713,9 +819,22 @@ ra_status launch_paged_rows(const PagedAttnArgs& a, cudaStream_t stream) {
 }
 
 ra_status launch_paged_join(const PagedAttnArgs& a, cudaStream_t stream) {
-  auto kern = a.p.D == 64 ? paged_join_kernel<64> : paged_join_kernel<128>;
-  return launch_early(kern, (long long)a.rows * a.H_q, 32 * kJoinWarps, 0, stream, a) ? RA_OK
-                                                                                      : RA_ERR_LAUNCH;
+  const long long items = a.n_items - a.n_whole;
+  int rows, smem = 0;
+  long long grid;
+  auto kern = a.p.D == 64 ? paged_join_few_kernel<64> : paged_join_few_kernel<128>;
+  if (a.block_rows <= 16) {
+    rows = a.T * (a.H_q / a.p.H_kv);         // those that may hold a token
+    grid = items * rows;
+  } else {
+    kern = a.p.D == 64 ? paged_join_many_kernel<64> : paged_join_many_kernel<128>;
+    rows = 64;                               // fewer where CTAs would be, too
+    while (rows > 8 && items * (a.block_rows / rows) < 2 * 152) rows /= 2;
+    grid = items * (a.block_rows / rows);
+    smem = (a.n_split + 1) * rows * (int)sizeof(float2);
+  }
+  if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
+  return launch_early(kern, grid, kJoinThreads, smem, stream, a, rows) ? RA_OK : RA_ERR_LAUNCH;
 }
 
 }  // namespace ra

@@ -53,25 +53,28 @@ struct PagedAttnArgs {
   void* out;               // [rows, H_q, D] bf16
   float* lse;              // [B, H_q, T] or, packed, [H_q, rows]; may be null
   int B, T, rows, H_q;     // T: new tokens a sequence; packed: at most so many
+  int packed;
   int max_len;             // bound on lens
   int window, n_sink;      // window 0: every slot up to the query's own
   float scale_log2;        // softmax scale * log2(e)
-  // plan (paged_attn_plan): a sequence's new tokens give T * H_q / H_kv query
-  // rows a key/value head, cut into n_rb blocks; the visible tiles of each are
-  // cut into n_split chunks of `chunk` tiles.
-  int block_rows;          // 8 or 16: few rows (paged_attn.cu); 256: many (paged_tiles.cu)
-  int n_rb, n_split, chunk;
+  // plan (paged_attn_plan): a sequence's new tokens give n * H_q / H_kv query rows
+  // a key/value head. Few (block_rows 8 or 16: paged_attn.cu) are one block; many
+  // (256: paged_tiles.cu) are cut into blocks. Of the n_items blocks the first
+  // n_whole go to one CTA each, the visible tiles of the others are cut into n_split
+  // chunks of `chunk` tiles.
+  int block_rows, n_items, n_whole, n_split, chunk;
+  int n_rb;                // many rows: blocks of the longest sequence and head
   int rb_major;            // many rows: the blocks' order, see there
   int n_expanded;          // many rows over 8-bit pages: tiles a sequence's rows see at most
-  float* part_o;           // [n_split][rows * H_q][D]
-  float* part_ml;          // [n_split][rows * H_q][2]: maximum (base 2), sum
+  float* part_o;           // [n_items - n_whole][n_split][block_rows][D]
+  float* part_ml;          // [n_items - n_whole][n_split][block_rows][2]: maximum (base 2), sum
   __nv_bfloat16* expanded_k;     // [B][n_expanded][H_kv][128][D]
   __nv_bfloat16* expanded_v;
   int* status;
 };
 
-// Fills the plan fields for the sizes in `a`; bytes: the workspace needed (the
-// same for packed rows and others). paged_attn_place puts its parts there.
+// Fills the plan fields for the sizes in `a`; bytes: the workspace
+// needed. paged_attn_place puts its parts there.
 ra_status paged_attn_plan(PagedAttnArgs* a, size_t* bytes);
 void paged_attn_place(PagedAttnArgs* a, void* workspace);
 // The launchers of the two kernels and of the join of their chunks.

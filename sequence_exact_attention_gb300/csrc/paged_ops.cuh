@@ -91,6 +91,64 @@ struct PagedSpan {
   }
 };
 
+// The block of query rows that item `item` is; every lane of a warp calls it. Few
+// rows: a sequence and head is one block. Many: blocks of late tokens (the longest
+// walks) come first, across all heads of a sequence (and the sequences, where all
+// have T new tokens) when keys and values fit in L2 anyway, else within each head.
+// Packed sequences are looked up among their numbers of blocks: the launch knows
+// only how many there are at most (b = -1 past the last).
+struct PagedBlock {
+  int b, hk, rb;
+};
+__device__ __forceinline__ PagedBlock paged_block(const PagedAttnArgs& a, int item) {
+  const int H_kv = a.p.H_kv;
+  if (a.block_rows <= 16) return {item / H_kv, item % H_kv, 0};
+  if (!a.cu) {
+    if (a.rb_major) {
+      const int bh = item % (a.B * H_kv);
+      return {bh / H_kv, bh % H_kv, a.n_rb - 1 - item / (a.B * H_kv)};
+    }
+    const int bh = item / a.n_rb;
+    return {bh / H_kv, bh % H_kv, a.n_rb - 1 - item % a.n_rb};
+  }
+  const int lane = threadIdx.x & 31, tokens = 2 * (128 / (a.H_q / H_kv));
+  int before = 0;                                  // blocks of a head before these 32 sequences
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int nb = b < a.B ? (paged_seq(a, b).n + tokens - 1) / tokens : 0;
+    int sum = nb;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, item < (long long)(before + sum) * H_kv);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      const int n = __shfl_sync(0xffffffffu, nb, src);
+      const int in = item - (before + __shfl_sync(0xffffffffu, sum, src) - n) * H_kv;
+      if (a.rb_major) return {b0 + src, in % H_kv, n - 1 - in / H_kv};
+      return {b0 + src, in / n, n - 1 - in % n};
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return {-1, 0, 0};
+}
+
+// A CTA's block and its chunk of it, or (split -1) all of it.
+struct PagedWork {
+  int item, split;
+};
+__device__ __forceinline__ PagedWork paged_work(const PagedAttnArgs& a, int cta) {
+  if (cta < a.n_whole) return {cta, -1};
+  return {a.n_whole + (cta - a.n_whole) / a.n_split,
+          a.n_split > 1 ? (cta - a.n_whole) % a.n_split : -1};
+}
+// The row of the partial results that is row r of chunk `split` of block `item`.
+__device__ __forceinline__ long long paged_part(const PagedAttnArgs& a, int item, int split, int r) {
+  return ((long long)(item - a.n_whole) * a.n_split + split) * a.block_rows + r;
+}
+
 // The place of a row's log-sum.
 __device__ __forceinline__ long long paged_lse_at(const PagedAttnArgs& a, int b, int row, int t,
                                                   int h) {

@@ -17,51 +17,75 @@ long long tiles_seen(const PagedAttnArgs& a, int tile, long long T) {
   return seen < all ? seen : all;
 }
 
+// Rows of partial results.
+size_t parts(const PagedAttnArgs& a) {
+  return (size_t)(a.n_items - a.n_whole) * a.n_split * a.block_rows;
+}
+
 }  // namespace
 
 ra_status paged_attn_plan(PagedAttnArgs* a, size_t* bytes) {
   const int grp = a->H_q / a->p.H_kv;
   const long long R = (long long)a->T * grp;
-  long long n_rb, tiles, best = 1, least;
-  // Few rows: chunks that fill whole waves of resident CTAs best, two waves by
-  // preference (sequences of different lengths then even out), but none under two
-  // tiles, where joining would cost more than it spreads.
+  long long items, whole = 0, tiles, best = 1, least;
   if (R <= 16) {
+    // Few rows: chunks that fill whole waves of resident CTAs best, two waves by
+    // preference (sequences of different lengths then even out), but none under two
+    // tiles, where joining would cost more than it spreads.
     a->block_rows = R <= 8 ? 8 : 16;
-    n_rb = 1;
+    items = (long long)a->B * a->p.H_kv;
     const int tile = !a->p.quant && a->p.D == 128 ? 64 : 128;
     tiles = tiles_seen(*a, tile, a->T);
     least = 2;
-    const long long blocks = (long long)a->B * a->p.H_kv, wave = 2 * kSms;
+    const long long wave = 2 * kSms;
     long long best_full = 0;
     for (int w = 2; w >= 1; --w) {
-      const long long n = wave * w / blocks;
-      const long long full = n * blocks * 1000 / (wave * w);
+      const long long n = wave * w / items;
+      const long long full = n * items * 1000 / (wave * w);
       if (full > best_full + 20) {
         best = n;
         best_full = full;
       }
     }
   } else {
-    // Many rows: a CTA a multiprocessor; chunks only where blocks are fewer.
+    // Many rows: a CTA a multiprocessor, in whole waves; the blocks left over are cut
+    // into as many chunks as end first, counted in tiles: a CTA takes some 4 to begin
+    // and end, the join's launch and its rows some 6.
     a->block_rows = 256;
     const int block_tokens = 2 * (128 / grp);
-    n_rb = ((long long)a->T + block_tokens - 1) / block_tokens;
+    const long long n_rb = ((long long)a->T + block_tokens - 1) / block_tokens;
+    long long blocks = a->B * n_rb;
+    const long long most = a->rows / block_tokens + a->B;     // of packed sequences
+    if (a->packed && most < blocks) blocks = most;
+    items = blocks * a->p.H_kv;
+    if (items > 0x7fffffffLL) return RA_ERR_RANGE;
+    a->n_rb = (int)n_rb;
     tiles = tiles_seen(*a, 128, block_tokens < a->T ? block_tokens : a->T);
     least = 4;
-    const long long blocks = (long long)a->B * a->p.H_kv * n_rb;
-    if (blocks < kSms) best = kSms / blocks;
+    whole = items / kSms * kSms;
+    const long long rest = items - whole;
+    long long best_cost = tiles + 4;
+    for (long long s = 2; rest > 0 && s * least <= tiles; ++s) {
+      const long long cost = (rest * s + kSms - 1) / kSms * ((tiles + s - 1) / s + 4) + 6;
+      if (cost < best_cost) {
+        best = s;
+        best_cost = cost;
+      }
+      if (rest * s > 8 * kSms) break;
+    }
     // keys and values within half of the 126 MB L2
     a->rb_major = (long long)a->B * a->max_len * a->p.H_kv * a->p.D * 4 <= (64ll << 20);
   }
   long long chunk = (tiles + best - 1) / best;
   if (chunk < least) chunk = least;
   const long long n_split = tiles > chunk ? (tiles + chunk - 1) / chunk : 1;
-  if ((long long)a->B * a->p.H_kv * n_rb * n_split > 0x7fffffffLL) return RA_ERR_RANGE;
-  a->n_rb = (int)n_rb;
+  if (n_split == 1) whole = items;
+  if (whole + (items - whole) * n_split > 0x7fffffffLL) return RA_ERR_RANGE;
+  a->n_items = (int)items;
+  a->n_whole = (int)whole;
   a->chunk = (int)chunk;
   a->n_split = (int)n_split;
-  size_t n = n_split > 1 ? (size_t)n_split * a->rows * a->H_q * (a->p.D + 2) * sizeof(float) : 0;
+  size_t n = parts(*a) * (a->p.D + 2) * sizeof(float);
   if (a->block_rows == 256 && a->p.quant) {
     const long long e = tiles_seen(*a, 128, a->T);
     if ((long long)a->B * e * a->p.H_kv > 0x7fffffffLL) return RA_ERR_RANGE;
@@ -78,7 +102,7 @@ void paged_attn_place(PagedAttnArgs* a, void* workspace) {
   a->expanded_k = e;
   a->expanded_v = e + tensor;
   a->part_o = reinterpret_cast<float*>(e + 2 * tensor);
-  a->part_ml = a->part_o + (a->n_split > 1 ? (size_t)a->n_split * a->rows * a->H_q * a->p.D : 0);
+  a->part_ml = a->part_o + parts(*a) * a->p.D;
 }
 
 }  // namespace ra

@@ -6,8 +6,8 @@
 // for the whole group and a short piece still fills a tile. (A group that does not
 // divide 128 leaves the last rows unused.) One CTA owns two query tiles and walks
 // the tiles of 128 slots that some row of them sees; each tile of keys and values
-// serves both. Where query blocks are too few to fill the card the walk is cut into
-// chunks, joined by paged_join_kernel.
+// serves both. Of the blocks that do not fill a wave of CTAs the walks are cut into
+// chunks, joined by paged_join_kernel (paged_plan.cpp).
 //
 // bf16 pages are read where they lie: the producer warp looks a tile's pages up, a
 // lane for each, and asks for their boxes; a page that is not there, or that holds
@@ -138,28 +138,24 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- work item: two query tiles of one key/value head, one chunk of their walk.
-  // Blocks of late tokens (the longest walks) come first: across all heads and
-  // sequences when the keys and values fit in L2 anyway, else within each head.
+  // ---- work item: two query tiles of one key/value head, all of their walk or one
+  // chunk of it
   const int H_kv = a.p.H_kv, grp = a.H_q / H_kv;
   const int tt = kTile / grp;                     // tokens a query tile
-  int item = blockIdx.x;
-  const int split = item % a.n_split;
-  item /= a.n_split;
-  const int n_bh = a.B * H_kv;
-  const int rb = a.n_rb - 1 - (a.rb_major ? item / n_bh : item % a.n_rb);
-  const int bh = a.rb_major ? item % n_bh : item / a.n_rb;
-  const int b = bh / H_kv, hk = bh % H_kv;
+  const PagedWork work = paged_work(a, blockIdx.x);
+  const PagedBlock blk = paged_block(a, work.item);
+  const int b = blk.b, hk = blk.hk;
+  if (b < 0) return;                              // past the last block of the batch
   const PagedSeq sq = paged_seq(a, b);
-  const int t0 = rb * 2 * tt;                     // the block's first new token
-  if (t0 >= sq.n) return;                         // a shorter sequence of the batch
+  const int t0 = blk.rb * 2 * tt;                 // the block's first new token
+  if (t0 >= sq.n) return;
   const int n_tok = min(2 * tt, sq.n - t0);
   const bool two = n_tok > tt;
   const int first = sq.len - sq.n + t0;           // its position
   PagedSpan<kTile> sp;
   sp.init(a, first, first + n_tok - 1);
-  const int v_begin = split * a.chunk;
-  const int n = max(min(sp.n, v_begin + a.chunk) - v_begin, 0);   // tiles to walk
+  const int v_begin = max(work.split, 0) * a.chunk;
+  const int n = max((work.split < 0 ? sp.n : min(sp.n, v_begin + a.chunk)) - v_begin, 0);  // tiles
   auto tile_lo = [&](int j) -> int { return sp.tile(v_begin + j) * kTile; };
 
   // ---- set-up: barriers, abort flag, TMEM
@@ -492,7 +488,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
       const long long orow = (long long)(sq.row0 + t) * a.H_q + h;
       const uint32_t tO = tmem + t_lane + kOCol + (uint32_t)(qi * D + part * (D / 2));
       const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);   // 0: no slot; NaN stays
-      const long long prow = (long long)split * a.rows * a.H_q + orow;
+      const long long prow = paged_part(a, work.item, work.split, qi * kTile + row);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         uint32_t uo[32];
@@ -505,7 +501,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         if (!valid) continue;
         const int col = part * (D / 2) + c * 32;
-        if (a.n_split > 1) {
+        if (work.split >= 0) {
           if (n == 0) continue;
           uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + col);
 #pragma unroll
@@ -525,7 +521,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
       }
       if (valid && part == 0) {
-        if (a.n_split > 1) {
+        if (work.split >= 0) {
           a.part_ml[2 * prow] = ls == 0.f ? -INFINITY : m_run[qi];
           a.part_ml[2 * prow + 1] = ls;
         } else if (a.lse) {
@@ -617,7 +613,7 @@ ra_status launch_tiles(const PagedAttnArgs& a, cudaStream_t stream) {
   if (!make_query_map(&mq, a.q, a.rows, a.H_q, D, grp, tt) ||
       !make_page_map(&mk, p, p.k, p.page) || !make_page_map(&mv, p, p.v, p.page))
     return RA_ERR_LAUNCH;
-  const long long grid = (long long)a.B * a.p.H_kv * a.n_rb * a.n_split;
+  const long long grid = a.n_whole + (long long)(a.n_items - a.n_whole) * a.n_split;
   if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
   auto kern = paged_tiles_kernel<D, kExpanded>;
   static std::atomic<uint64_t> allowed;
