@@ -100,7 +100,8 @@ ra_status attn_sizes(const ra_pages& p, bool varlen, int B, int T, long long row
   if (H_q % p.H_kv != 0 || H_q / p.H_kv > 128) return RA_ERR_SHAPE;
   if (max_len <= 0 || max_len > (1 << 30) || window < 0 || n_sink < 0) return RA_ERR_RANGE;
   // a block's rows, and the launch's blocks, are counted in 32 bits
-  if ((long long)T * (H_q / p.H_kv) > (1 << 30)) return RA_ERR_RANGE;
+  if ((long long)T * (H_q / p.H_kv) > (1 << 30) || (long long)B * p.H_kv > kMaxElems)
+    return RA_ERR_RANGE;
   const ra_status st = check_tokens(rows, H_q, p.D);
   if (st != RA_OK) return st;
   a->p = pool_of(p);

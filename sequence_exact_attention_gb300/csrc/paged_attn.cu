@@ -32,11 +32,16 @@
 // masked, too (0 times a NaN is not 0); where tokens differ in what they see and a
 // value is not finite, such a tile is multiplied once for each of them (always doing
 // so took 26 instead of 20 us for 4 x 4 tokens under a window of 4096).
+//
+// Measured, replayed from a graph: 8 x 128K slots of 8 heads, D = 128, 8 bits 310 us,
+// 7.0 TB/s; 32 ragged sequences up to 8K slots, bf16 in pages of 16 110 us, 6.1 TB/s.
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "checks.cuh"
 #include "early_launch.cuh"
@@ -98,14 +103,13 @@ __device__ __forceinline__ float pow2_field(int f) { return __uint_as_float((uin
 // the join once all are done.
 template <int D, int NT, bool kQuant>
 struct Smem {
-  static constexpr int kTile = !kQuant && D == 128 ? 64 : 128;     // slots
-  static constexpr int kRowBytes = kQuant ? D : 128;               // of a box's row
-  static constexpr int kBoxes = kQuant ? 1 : D / 64;               // boxes a row takes
-  static constexpr int kPart = kTile * kRowBytes;
-  static constexpr int kKv = kBoxes * kPart;                       // keys, or values, of a tile
+  static constexpr int kTile = paged_rows_tile(D, kQuant);         // slots
+  static constexpr int kRowBytes = kQuant ? D : 128;               // of a part of a row
+  static constexpr int kParts = kQuant ? 1 : D / 64;               // a page's, one after the other
+  static constexpr int kKv = kTile * kParts * kRowBytes;           // keys, or values, of a tile
   static constexpr int kKs = 2 * kKv, kVs = kKs + (kQuant ? kTile : 0);
   static constexpr int kStage = (kVs + (kQuant ? kTile : 0) + 1023) / 1024 * 1024;
-  static constexpr int kStages = kStage <= 18 * 1024 ? 4 : 3;
+  static constexpr int kStages = 100 * 1024 / kStage;
   static constexpr int kRing = kStages * kStage;
   static constexpr int kOut = kWarps * 8 * NT * D * 4;
   static constexpr int kData = kRing > kOut ? kRing : kOut;
@@ -160,6 +164,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     *abort_flag = *never = 0;
     sm100::fence_mbar_init();
   }
+  let_dependents_start();
+  wait_for_prior_grid();
   const PagedSeq sq = paged_seq(a, b);
   const int R = sq.n * grp;                 // query rows of this head
   if (R == 0) return;                       // a sequence without new tokens
@@ -168,59 +174,63 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   sp.init(a, first, first + sq.n - 1);
   const int v_begin = max(work.split, 0) * a.chunk;
   const int n_tiles = max((work.split < 0 ? sp.n : min(sp.n, v_begin + a.chunk)) - v_begin, 0);
-  let_dependents_start();
   __syncthreads();
 
   if (warp == kWarps) {
     // ======================= producer =======================
+    // A lane for each page's box looks the page up, a tile ahead, and asks for its keys,
+    // values and scales. (Scales through registers, loaded a tile ahead and stored by
+    // the lanes, took 332 instead of 314 us for 8 x 128K slots.)
     const int box_rows = min(a.p.page, kTile);
     const int shift = 31 - __clz(a.p.page);
-    const int n_box = kTile / box_rows;     // at most 8: a lane for each
+    const int n_box = kTile / box_rows;     // at most 8
     const int at = lane * box_rows;
-    auto look_up = [&](int i) -> int {      // -1: nothing to load; -2: no such page
-      if (i >= n_tiles || lane >= n_box) return -1;
-      const int j = sp.tile(v_begin + i) * kTile + at;
-      if (j >= sp.hi || !sp.meets(a, j, box_rows)) return -1;
-      const int at_page = j >> shift;
-      if (at_page >= a.width) return -2;
-      const int id = __ldg(a.table + (size_t)b * a.width + at_page);
-      return id >= 0 && id < a.p.n_pages ? id : -2;
+    struct Box {
+      bool wanted;                          // some row sees some of it
+      int id, row;                          // id below 0: no such page
     };
-    int id = look_up(0);
+    auto look_up = [&](int i) -> Box {
+      Box x = {false, -1, 0};
+      if (i >= n_tiles || lane >= n_box) return x;
+      const int j = sp.tile(v_begin + i) * kTile + at;
+      if (j >= sp.hi || !sp.meets(a, j, box_rows)) return x;
+      x.wanted = true;
+      x.row = j & (a.p.page - 1);
+      if ((j >> shift) < a.width) x.id = __ldg(a.table + (size_t)b * a.width + (j >> shift));
+      return x;
+    };
+    Box next = look_up(0);
     int i = 0, stage = 0;
     uint32_t phase = 0;
     bool bad = false;
     for (; i < n_tiles; ++i) {
-      const int next = look_up(i + 1);
+      const Box cur = next;
+      next = look_up(i + 1);
       if (i >= S::kStages &&
           !sm100::mbar_wait_warp(free_ + 8 * stage, phase ^ 1, abort_flag, kTimeoutNs))
         break;
-      const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
-      const uint32_t missing = __ballot_sync(0xffffffffu, id == -2);
+      const bool held = cur.id >= 0 && cur.id < a.p.n_pages;
+      const uint32_t boxes = __ballot_sync(0xffffffffu, held);
+      const uint32_t missing = __ballot_sync(0xffffffffu, cur.wanted && !held);
       const uint32_t dst = ring + stage * S::kStage, bar = full + 8 * stage;
       if (lane == 0) {
-        gone[stage] = missing;
+        gone[stage] = missing;                // a bit for each box
         sm100::mbar_arrive_expect_tx(
-            bar, __popc(there) * box_rows * (2 * S::kBoxes * S::kRowBytes + (kQuant ? 2 : 0)));
+            bar, __popc(boxes) * box_rows * (2 * S::kParts * S::kRowBytes + (kQuant ? 2 : 0)));
       }
       bad |= missing != 0;
       __syncwarp();
-      if (id >= 0) {
-        const int row = (sp.tile(v_begin + i) * kTile + at) & (a.p.page - 1);
-        const int z = id * H_kv + hk;
-#pragma unroll
-        for (int x = 0; x < S::kBoxes; ++x)
-          tma_load_3d(dst + x * S::kPart + at * S::kRowBytes, &tm_k, bar, x * 64, row, z);
-#pragma unroll
-        for (int x = 0; x < S::kBoxes; ++x)
-          tma_load_3d(dst + S::kKv + x * S::kPart + at * S::kRowBytes, &tm_v, bar, x * 64, row, z);
+      if (held) {
+        const uint32_t to = dst + at * (S::kParts * S::kRowBytes);
+        const int z = cur.id * H_kv + hk;
+        sm100::tma_load_4d(to, &tm_k, bar, 0, cur.row, 0, z);
+        sm100::tma_load_4d(to + S::kKv, &tm_v, bar, 0, cur.row, 0, z);
         if (kQuant) {
-          const size_t from = (size_t)z * a.p.page + row;
+          const size_t from = (size_t)z * a.p.page + cur.row;
           sm100::bulk_load(dst + S::kKs + at, a.p.ks + from, box_rows, bar);
           sm100::bulk_load(dst + S::kVs + at, a.p.vs + from, box_rows, bar);
         }
       }
-      id = next;
       if (++stage == S::kStages) {
         stage = 0;
         phase ^= 1;
@@ -239,7 +249,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     // 16 k + 2 c, + 1, + 8, + 9 of step k; codes come four to a lane, 16 k + 4 c on
     uint32_t qf[NT][KS][2];
     float sl2[NT][2];                        // of rows 2c and 2c + 1
-    int pos[NT][2];                          // their positions; below 0: sees nothing
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g;
@@ -283,19 +292,19 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
                 ok ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * x + 2 * c) : 0u;
         sl2[nt][0] = sl2[nt][1] = a.scale_log2;
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int rr = nt * 8 + 2 * c + h;
-        pos[nt][h] = rr < R ? first + rr / grp : -1;
-      }
     }
+    // the position of row 2c + h; below 0: sees nothing
+    auto pos = [&](int nt, int h) -> int {
+      const int r = nt * 8 + 2 * c + h;
+      return r < R ? first + r / grp : -1;
+    };
 
     // Running state of rows 2c and 2c + 1. What the exponents subtract: the running
     // maximum in base 2, rounded down, so that raising it scales sums by a power of
-    // two; a score that passes `bound` raises it. (sub2, bound2: those of the
-    // weights, with the values' scales.)
+    // two, -inf until the row has seen a slot; a score kRescaleLog2 above raises it.
+    // (sub2: that of the weights, with the values' scales.)
     float o[NT][KS][4];
-    float sub[NT][2], bound[NT][2], sub2[NT][2], bound2[NT][2], l[NT][2];
+    float sub[NT][2], sub2[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -304,8 +313,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int i = 0; i < 4; ++i) o[nt][k][i] = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        sub[nt][h] = sub2[nt][h] = l[nt][h] = 0.f;
-        bound[nt][h] = bound2[nt][h] = -INFINITY;
+        l[nt][h] = 0.f;
+        sub[nt][h] = sub2[nt][h] = -INFINITY;
       }
     }
     auto scale_row = [&](int nt, int h, float mul) {
@@ -323,7 +332,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       return x;
     };
     constexpr int kSteps = kQuant ? KS / 2 : KS, kPer = kQuant ? 2 : 1;
-    const int box_shift = 31 - __clz(min(a.p.page, kTile));
 
     int stage = 0;
     uint32_t phase = 0;
@@ -334,31 +342,38 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         break;
       const uint32_t tile = ring + stage * S::kStage;
       const uint32_t missing = gone[stage];
+      const int box_rows = min(a.p.page, kTile), box_shift = 31 - __clz(box_rows);
       // 16 slots at a time, in a loop that is not unrolled: code that a short call runs
-      // once or twice costs it more to fetch than to run (two blocks side by side took
-      // 20 instead of 17 us for 4 x 4 tokens under a window of 4096)
+      // once or twice costs it more to fetch than to run (two at a time side by side:
+      // 31 instead of 25 us for 4 x 4 tokens under a window of 4096, and no less for 8
+      // x 128K slots)
 #pragma unroll 1
       for (int w0 = WS * warp; w0 < WS * (warp + 1); w0 += 16) {
         const int j0 = sp.tile(v_begin + it) * kTile + w0;
+        // where the first row of 16 lies, of the keys; from one part of it to the next
+        const uint32_t rows =
+            tile + (uint32_t)((w0 & ~(box_rows - 1)) * S::kParts * S::kRowBytes +
+                              (w0 & (box_rows - 1)) * S::kRowBytes);
+        const uint32_t next_part = (uint32_t)(box_rows * S::kRowBytes);
         // ---- scores: rows of s are slots, columns query rows
         float s[NT][4];
-        int ev[2];                           // the value scales' exponents
+        float ev[2];                     // the value scales' exponents
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-        const int slot = w0 + (lane & 15);
         if constexpr (kQuant) {
           float ks[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            ks[i] = pow2_byte(smem[stage * S::kStage + S::kKs + w0 + 8 * i + g]);
-            ev[i] = (int)smem[stage * S::kStage + S::kVs + w0 + 8 * i + g] - 127;
+            const uint8_t* at = smem + stage * S::kStage + w0 + 8 * i + g;
+            ks[i] = pow2_byte(at[S::kKs]);
+            ev[i] = (float)((int)at[S::kVs] - 127);
           }
 #pragma unroll
           for (int x = 0; x < KS / 2; ++x) {   // two chunks of 16 dimensions
             uint32_t w[4];
-            ldmatrix4(w, tile + swizzled<S::kRowBytes>(slot, 2 * x + (lane >> 4)));
+            ldmatrix4(w, rows + swizzled<S::kRowBytes>(lane & 15, 2 * x + (lane >> 4)));
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const uint32_t af[4] = {e4m3x2_half2(w[2 * y]), e4m3x2_half2(w[2 * y + 1]),
@@ -377,8 +392,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             uint32_t af[4];
-            ldmatrix4(af, tile + (k / 4) * S::kPart +
-                              swizzled<S::kRowBytes>(slot, 2 * (k % 4) + (lane >> 4)));
+            ldmatrix4(af, rows + (k / 4) * next_part +
+                              swizzled<S::kRowBytes>(lane & 15, 2 * (k % 4) + (lane >> 4)));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma16816<false>(s[nt], af, qf[nt][k][0], qf[nt][k][1]);
@@ -390,16 +405,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         // ---- slots that some row does not see
         const bool whole = missing == 0 && sp.whole(a, j0, 16);
+        auto lost = [&](int x) { return (missing >> ((w0 + x) >> box_shift) & 1u) != 0; };
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int x = 8 * i + g;
-            const bool lost = missing >> ((w0 + x) >> box_shift) & 1u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                if (lost || !paged_sees(a, pos[nt][h], j0 + x)) s[nt][2 * i + h] = -INFINITY;
+                if (lost(x) || !paged_sees(a, pos(nt, h), j0 + x)) s[nt][2 * i + h] = -INFINITY;
           }
         }
         // ---- raise the maxima when a score passes its bound: rare after the first tile
@@ -409,53 +424,49 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            top[nt][h] = fmaxf(s[nt][h], s[nt][2 + h]);
-            raise |= top[nt][h] > bound[nt][h];
-            if (kQuant) {
-              top2[nt][h] = fmaxf(s[nt][h] + (float)ev[0], s[nt][2 + h] + (float)ev[1]);
-              raise |= top2[nt][h] > bound2[nt][h];
+            top[nt][h] = top2[nt][h] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              top[nt][h] = fmaxf(top[nt][h], s[nt][2 * i + h]);
+              if (kQuant) top2[nt][h] = fmaxf(top2[nt][h], s[nt][2 * i + h] + ev[i]);
             }
+            raise |= top[nt][h] > sub[nt][h] + kRescaleLog2;
+            if (kQuant) raise |= top2[nt][h] > sub2[nt][h] + kRescaleLog2;
           }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float x = row_max(top[nt][h]);
-              if (x > bound[nt][h]) {
+              auto raise_to = [&](float x, float& sub_) -> float {   // what sums are multiplied by
+                if (!(x > sub_ + kRescaleLog2)) return 1.f;
                 const float to = floorf(x);
-                const float alpha = bound[nt][h] == -INFINITY ? 0.f : exp2f(sub[nt][h] - to);
-                sub[nt][h] = to;
-                bound[nt][h] = to + kRescaleLog2;
-                l[nt][h] *= alpha;
-                if (!kQuant) scale_row(nt, h, alpha);
-              }
-              if constexpr (kQuant) {
-                const float y = row_max(top2[nt][h]);
-                if (y > bound2[nt][h]) {
-                  const float to = floorf(y);
-                  const float alpha = bound2[nt][h] == -INFINITY ? 0.f : exp2f(sub2[nt][h] - to);
-                  sub2[nt][h] = to;
-                  bound2[nt][h] = to + kRescaleLog2;
-                  scale_row(nt, h, alpha);
-                }
-              }
+                const float alpha = sub_ == -INFINITY ? 0.f : exp2f(sub_ - to);
+                sub_ = to;
+                return alpha;
+              };
+              const float alpha = raise_to(row_max(top[nt][h]), sub[nt][h]);
+              l[nt][h] *= alpha;
+              scale_row(nt, h, kQuant ? raise_to(row_max(top2[nt][h]), sub2[nt][h]) : alpha);
             }
         }
         // ---- weights, as B operands: one half, or two bf16 numbers, what the first
         // leaves being the second
         uint32_t pf[NT][2], pl[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          // (a row that has seen nothing has scores of -inf alone)
+          const float less[2] = {fmaxf(sub[nt][0], -FLT_MAX), fmaxf(sub[nt][1], -FLT_MAX)};
+          const float less2[2] = {fmaxf(sub2[nt][0], -FLT_MAX), fmaxf(sub2[nt][1], -FLT_MAX)};
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float w[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float x = s[nt][2 * i + h];
-              const float p = sm100::ex2_approx(x - sub[nt][h]);
+              const float p = sm100::ex2_approx(x - less[h]);
               l[nt][h] += p;
-              w[h] = kQuant ? sm100::ex2_approx(x + ((float)ev[i] - sub2[nt][h])) : p;
+              w[h] = kQuant ? sm100::ex2_approx(x + (ev[i] - less2[h])) : p;
             }
             if constexpr (kQuant) {
               pf[nt][i] = transpose8x8(pack_half2(w[0], w[1]));
@@ -466,6 +477,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
                   w[0] - __uint_as_float(u << 16), w[1] - __uint_as_float(u & 0xffff0000u)));
             }
           }
+        }
         // ---- their products with the values: rows of o are dimensions
         // the halves of slots 2c, 2c + 1, and + 8 to keep: those that the row at p, or
         // (kAny) any row, sees
@@ -479,48 +491,64 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
               const int x = 8 * i + 2 * c + y;
               const bool see = p == kAny ? j0 + x < sp.hi && sp.meets(a, j0 + x, 1)
                                          : paged_sees(a, p, j0 + x);
-              if (!(missing >> ((w0 + x) >> box_shift) & 1u) && see) keep[i] |= 0xffffu << (16 * y);
+              if (see && !lost(x)) keep[i] |= 0xffffu << (16 * y);
             }
           }
         };
-        // the operand of the 16 slots and of 16 dimensions (8 bits: two steps' at once)
-        auto load_values = [&](int k, const uint32_t (&keep)[2], uint32_t (&af)[kPer][4]) {
+        // the operand of 16 slots and of 16 dimensions (8 bits: two steps' at once)
+        auto load_values = [&](int k, uint32_t (&af)[kPer][4]) {
           if constexpr (kQuant) {
             uint32_t w[4];
-            ldmatrix4_trans(w, tile + S::kKv + swizzled<S::kRowBytes>(slot, 2 * k + (lane >> 4)));
+            ldmatrix4_trans(w, rows + S::kKv +
+                                   swizzled<S::kRowBytes>(lane & 15, 2 * k + (lane >> 4)));
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               // bytes: (slot 2c, dimensions 2g, 2g + 1), (slot 2c + 1, the same)
               const uint32_t lo = __byte_perm(w[2 * y], 0, 0x3120);
               const uint32_t hi = __byte_perm(w[2 * y + 1], 0, 0x3120);
-              af[y][0] = e4m3x2_half2(lo) & keep[0];
-              af[y][1] = e4m3x2_half2(lo >> 16) & keep[0];
-              af[y][2] = e4m3x2_half2(hi) & keep[1];
-              af[y][3] = e4m3x2_half2(hi >> 16) & keep[1];
+              af[y][0] = e4m3x2_half2(lo);
+              af[y][1] = e4m3x2_half2(lo >> 16);
+              af[y][2] = e4m3x2_half2(hi);
+              af[y][3] = e4m3x2_half2(hi >> 16);
             }
           } else {
-            const int row = w0 + (lane & 7) + ((lane & 16) >> 1);
-            ldmatrix4_trans(af[0], tile + S::kKv + (k / 4) * S::kPart +
+            const int row = (lane & 7) + ((lane & 16) >> 1);
+            ldmatrix4_trans(af[0], rows + S::kKv + (k / 4) * next_part +
                                        swizzled<S::kRowBytes>(row, 2 * (k % 4) + ((lane >> 3) & 1)));
-#pragma unroll
-            for (int x = 0; x < 4; ++x) af[0][x] &= keep[x >> 1];
           }
+        };
+        auto mask = [&](const uint32_t (&keep)[2], uint32_t (&af)[kPer][4]) {
+#pragma unroll
+          for (int x = 0; x < kPer; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) af[x][i] &= keep[i >> 1];
         };
         auto multiply = [&](float (&acc)[4], const uint32_t (&af)[4], int nt) {
           mma16816<kQuant>(acc, af, pf[nt][0], pf[nt][1]);
           if (!kQuant) mma16816<kQuant>(acc, af, pl[nt][0], pl[nt][1]);
         };
-        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-        bool apart = false;
-        if (!whole) {
-          keep_slots(kAny, keep);
+        if (whole) {
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t af[kPer][4];
+            load_values(k, af);
+#pragma unroll
+            for (int x = 0; x < kPer; ++x)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) multiply(o[nt][kPer * k + x], af[x], nt);
+          }
+        } else {
           // where tokens differ in what they see, a value that is not finite would reach
           // the rows that do not see it
+          bool apart = false;
           if (sp.pmin != sp.pmax) {
+            uint32_t keep[2];
+            keep_slots(kAny, keep);
 #pragma unroll 1
             for (int k = 0; k < kSteps; ++k) {
               uint32_t af[kPer][4];
-              load_values(k, keep, af);
+              load_values(k, af);
+              mask(keep, af);
               constexpr uint32_t ones = kQuant ? 0x7c007c00u : 0x7f807f80u;   // exponents
 #pragma unroll
               for (int x = 0; x < kPer; ++x)
@@ -532,24 +560,28 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             apart = __any_sync(0xffffffffu, apart);
           }
-        }
-        if (!apart) {
+          if (!apart) {
+            uint32_t keep[2];
+            keep_slots(kAny, keep);
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            uint32_t af[kPer][4];
-            load_values(k, keep, af);
+            for (int k = 0; k < kSteps; ++k) {
+              uint32_t af[kPer][4];
+              load_values(k, af);
+              mask(keep, af);
 #pragma unroll
-            for (int x = 0; x < kPer; ++x)
+              for (int x = 0; x < kPer; ++x)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) multiply(o[nt][kPer * k + x], af[x], nt);
+                for (int nt = 0; nt < NT; ++nt) multiply(o[nt][kPer * k + x], af[x], nt);
+            }
           }
-        } else {
-          for (int p = max(sp.pmin, 0); p <= sp.pmax; ++p) {
+          for (int p = max(sp.pmin, 0); apart && p <= sp.pmax; ++p) {
+            uint32_t keep[2];
             keep_slots(p, keep);
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
               uint32_t af[kPer][4];
-              load_values(k, keep, af);
+              load_values(k, af);
+              mask(keep, af);
 #pragma unroll
               for (int x = 0; x < kPer; ++x)
 #pragma unroll
@@ -559,7 +591,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
                   multiply(y, af[x], nt);
 #pragma unroll
                   for (int i = 0; i < 4; ++i)
-                    if (pos[nt][i & 1] == p) acc[i] = y[i];
+                    if (pos(nt, i & 1) == p) acc[i] = y[i];
                 }
             }
           }
@@ -584,11 +616,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         for (int x = 4; x < 32; x *= 2) ls += __shfl_xor_sync(0xffffffffu, ls, x);
         const int r = nt * 8 + 2 * c + h;
         if (g == 0) {
-          // -inf where the row saw nothing
-          sM[warp * RB + r] = bound[nt][h] == -INFINITY ? -INFINITY : sub[nt][h];
+          sM[warp * RB + r] = sub[nt][h];    // -inf where the row saw nothing
           sL[warp * RB + r] = ls;
         }
-        const float mul = kQuant ? exp2f(sub2[nt][h] - sub[nt][h]) : 1.f;
+        const float mul = kQuant && sub[nt][h] > -INFINITY ? exp2f(sub2[nt][h] - sub[nt][h]) : 1.f;
         float* row = sO + (warp * RB + r) * D;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
@@ -796,15 +827,15 @@ ra_status launch_rows(const PagedAttnArgs& a, cudaStream_t stream) {
   using S = Smem<D, NT, kQuant>;
   CUtensorMap mk, mv;
   const int box_rows = a.p.page < S::kTile ? a.p.page : S::kTile;
-  if (!make_page_map(&mk, a.p, a.p.k, box_rows) || !make_page_map(&mv, a.p, a.p.v, box_rows))
+  if (!make_page_map(&mk, a.p, a.p.k, box_rows, S::kParts) ||
+      !make_page_map(&mv, a.p, a.p.v, box_rows, S::kParts))
     return RA_ERR_LAUNCH;
   const long long grid = (long long)a.n_items * a.n_split;
   if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
   auto kern = paged_attn_kernel<D, NT, kQuant>;
   static std::atomic<uint64_t> allowed;
   if (!allow_smem(kern, S::kBytes, allowed)) return RA_ERR_LAUNCH;
-  kern<<<(unsigned)grid, kThreads, S::kBytes, stream>>>(mk, mv, a);
-  return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_LAUNCH;
+  return launch_early(kern, grid, kThreads, S::kBytes, stream, mk, mv, a) ? RA_OK : RA_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -21,6 +21,7 @@
 
 #include "checks.cuh"
 #include "divisor.cuh"
+#include "early_launch.cuh"
 #include "paged_internal.h"
 #include "paged_ops.cuh"
 #include "sm100.cuh"
@@ -165,6 +166,8 @@ paged_append_kernel(const PagedRowArgs a, const Divisors by, uint32_t rows) {
   constexpr int D = kLanes * kVals;
   const uint32_t i = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes;
+  let_dependents_start();
+  wait_for_prior_grid();
   // a row's lanes leave or stay together: the shuffles name only them
   const uint32_t mask = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
   if (i >= rows) return;
@@ -227,6 +230,8 @@ paged_read_kernel(const PagedRowArgs a, const Divisors by, uint32_t rows) {
   constexpr int D = kLanes * kReadVals, kAtOnce = kThreads / kLanes;
   const uint32_t first = blockIdx.x * (kAtOnce * kReadRows) + threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes, d = lane * kReadVals;
+  let_dependents_start();
+  wait_for_prior_grid();
   Place r[kReadRows];
 #pragma unroll
   for (int x = 0; x < kReadRows; ++x) {
@@ -270,13 +275,13 @@ paged_read_kernel(const PagedRowArgs a, const Divisors by, uint32_t rows) {
 }
 
 // `per`: rows a CTA takes.
-template <typename Kernel>
-ra_status launch_rows(Kernel kern, const PagedRowArgs& a, int per, cudaStream_t stream) {
+ra_status launch_rows(void (*kern)(PagedRowArgs, Divisors, uint32_t), const PagedRowArgs& a,
+                      int per, cudaStream_t stream) {
   const long long rows = a.rows * a.p.H_kv;
   const long long blocks = (rows + per - 1) / per;
   const Divisors by = {Divisor((uint32_t)a.p.H_kv), Divisor((uint32_t)a.T)};
-  kern<<<(unsigned)blocks, kThreads, 0, stream>>>(a, by, (uint32_t)rows);
-  return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_LAUNCH;
+  return launch_early(kern, blocks, kThreads, 0, stream, a, by, (uint32_t)rows) ? RA_OK
+                                                                                : RA_ERR_LAUNCH;
 }
 
 template <typename T, int D>

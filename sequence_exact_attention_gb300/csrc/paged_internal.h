@@ -73,6 +73,9 @@ struct PagedAttnArgs {
   int* status;
 };
 
+// Few rows: slots of a tile, 32 KB of keys and values at most.
+constexpr int paged_rows_tile(int D, bool quant) { return !quant && D == 128 ? 64 : 128; }
+
 // Fills the plan fields for the sizes in `a`; bytes: the workspace
 // needed. paged_attn_place puts its parts there.
 ra_status paged_attn_plan(PagedAttnArgs* a, size_t* bytes);
@@ -82,10 +85,11 @@ ra_status launch_paged_rows(const PagedAttnArgs& a, cudaStream_t stream);
 ra_status launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t stream);
 ra_status launch_paged_join(const PagedAttnArgs& a, cudaStream_t stream);
 
-// TMA map of a pool's keys or values as [n_pages * H_kv, page, D]: a box is
-// `box_rows` rows of one page by 64 values (bfloat16) or D (codes), swizzled
-// over the bytes of its rows (128, or 64 where D is 64 and codes are held).
-bool make_page_map(CUtensorMap* m, const PagePool& p, const void* ptr, int box_rows);
+// TMA map of a pool's keys or values as [n_pages * H_kv, D / cols, page, cols], cols
+// being 64 values (bfloat16) or D (codes): a box is `box_rows` rows of one page and
+// `box_parts` of its parts of `cols` values, one part after the other, swizzled over
+// the bytes of a part's row (128, or 64 where D is 64 and codes are held).
+bool make_page_map(CUtensorMap* m, const PagePool& p, const void* ptr, int box_rows, int box_parts);
 // TMA map of bf16 queries [rows, H_q, D]: a box is 64 columns of `heads` heads of
 // `tokens` rows, a row of the box after the other, 128-byte swizzle.
 bool make_query_map(CUtensorMap* m, const void* q, int rows, int H_q, int D, int heads, int tokens);

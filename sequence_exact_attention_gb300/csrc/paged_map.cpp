@@ -27,15 +27,16 @@ EncodeTiledFn encoder() {
 
 }  // namespace
 
-bool make_page_map(CUtensorMap* m, const PagePool& p, const void* ptr, int box_rows) {
+bool make_page_map(CUtensorMap* m, const PagePool& p, const void* ptr, int box_rows,
+                   int box_parts) {
   EncodeTiledFn enc = encoder();
   if (!enc) return false;
-  const cuuint64_t row = (cuuint64_t)p.D * (p.quant ? 1 : 2);
-  cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.page, (cuuint64_t)p.n_pages * p.H_kv};
-  cuuint64_t strides[2] = {row, row * p.page};
-  cuuint32_t box[3] = {p.quant ? (cuuint32_t)p.D : 64u, (cuuint32_t)box_rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, p.quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+  const cuuint64_t size = p.quant ? 1 : 2, cols = p.quant ? p.D : 64;
+  cuuint64_t dims[4] = {cols, (cuuint64_t)p.page, p.D / cols, (cuuint64_t)p.n_pages * p.H_kv};
+  cuuint64_t strides[3] = {p.D * size, cols * size, p.D * size * p.page};
+  cuuint32_t box[4] = {(cuuint32_t)cols, (cuuint32_t)box_rows, (cuuint32_t)box_parts, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, p.quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
              const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              p.quant && p.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

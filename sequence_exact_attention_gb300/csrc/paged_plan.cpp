@@ -34,7 +34,7 @@ ra_status paged_attn_plan(PagedAttnArgs* a, size_t* bytes) {
     // tiles, where joining would cost more than it spreads.
     a->block_rows = R <= 8 ? 8 : 16;
     items = (long long)a->B * a->p.H_kv;
-    const int tile = !a->p.quant && a->p.D == 128 ? 64 : 128;
+    const int tile = paged_rows_tile(a->p.D, a->p.quant != 0);
     tiles = tiles_seen(*a, tile, a->T);
     least = 2;
     const long long wave = 2 * kSms;

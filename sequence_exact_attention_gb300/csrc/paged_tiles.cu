@@ -111,6 +111,11 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int from, in
                    : "memory");
 }
 
+// The columns below x, a bit each of 64.
+__device__ __forceinline__ uint64_t below(int x) {
+  return x <= 0 ? 0 : x >= 64 ? ~0ull : (1ull << x) - 1;
+}
+
 // The tiles of 128 slots that a sequence's new tokens see, all of them: their
 // places among the expanded ones.
 __device__ __forceinline__ PagedSpan<kTile> sequence_span(const PagedAttnArgs& a,
@@ -138,6 +143,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  let_dependents_start();
+  wait_for_prior_grid();
   // ---- work item: two query tiles of one key/value head, all of their walk or one
   // chunk of it
   const int H_kv = a.p.H_kv, grp = a.H_q / H_kv;
@@ -180,7 +187,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
     tmem_alloc(smem_u32(tmem_holder), kTmemCols);
     tmem_relinquish();
   }
-  let_dependents_start();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -225,13 +231,13 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
         const int t = sp.tile(v_begin + j);
         const int v = t < whole.n_sink_tiles ? t : t - whole.w0 + whole.n_sink_tiles;
         if (lane < C::kBoxes)
-          tma_load_3d(dst + lane * kBoxBytes, m, full, lane * 64, 0,
+          tma_load_4d(dst + lane * kBoxBytes, m, full, 0, 0, lane,
                       (b * a.n_expanded + v) * H_kv + hk);
       } else if (lane < n_box) {
         const int z = id >= 0 ? id * H_kv + hk : past;
 #pragma unroll
         for (int bx = 0; bx < C::kBoxes; ++bx)
-          tma_load_3d(dst + bx * kBoxBytes + at * 128, m, full, bx * 64, 0, z);
+          tma_load_4d(dst + bx * kBoxBytes + at * 128, m, full, 0, 0, bx, z);
       }
     };
     int id = look_up(0);
@@ -398,26 +404,19 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
         const bool all = lo + kTile - 1 <= p_first &&
                          (a.window <= 0 || lo > p_first + tt - 1 - a.window ||
                           lo + kTile <= a.n_sink);
-        if (!all) {
-          const int q_pos = p_first + tok;
-          const int lim = q_pos - lo + 1 - part * 64;         // columns from lim on are masked
-          if (a.window > 0) {
-            const int w_lo = q_pos - a.window + 1 - lo - part * 64;
-            const int s_hi = a.n_sink - lo - part * 64;       // and those in [s_hi, w_lo)
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c >= lim || (c >= s_hi && c < w_lo)) uu[c / 32][c % 32] = __float_as_uint(-INFINITY);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c >= lim) uu[c / 32][c % 32] = __float_as_uint(-INFINITY);
+        if (!all || missing) {
+          // a bit for each of this part's 64 columns that the row sees
+          const int q_pos = p_first + tok, c0 = lo + part * 64;
+          uint64_t see = below(q_pos + 1 - c0);
+          if (a.window > 0) see &= ~below(q_pos - a.window + 1 - c0) | below(a.n_sink - c0);
+          for (uint32_t rest = missing; rest; rest &= rest - 1) {
+            const int x = ((__ffs(rest) - 1) << shift) - part * 64;     // a page that is not there
+            see &= ~below(x + a.p.page) | below(x);
           }
-        }
-        if (missing) {
+          const uint32_t bits[2] = {(uint32_t)see, (uint32_t)(see >> 32)};
 #pragma unroll
           for (int c = 0; c < 64; ++c)
-            if (missing >> ((part * 64 + c) >> shift) & 1u)
-              uu[c / 32][c % 32] = __float_as_uint(-INFINITY);
+            if (!(bits[c / 32] >> (c % 32) & 1u)) uu[c / 32][c % 32] = __float_as_uint(-INFINITY);
         }
         float m8[8];
 #pragma unroll
@@ -552,6 +551,8 @@ constexpr int kExpandThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kExpandThreads)
 paged_expand_kernel(const PagedAttnArgs a) {
+  let_dependents_start();
+  wait_for_prior_grid();
   const int hk = blockIdx.x % a.p.H_kv;
   const int rest = blockIdx.x / a.p.H_kv;
   const int v = rest % a.n_expanded, b = rest / a.n_expanded;
@@ -602,8 +603,8 @@ ra_status launch_tiles(const PagedAttnArgs& a, cudaStream_t stream) {
   if (kExpanded) {
     const long long blocks = (long long)a.B * a.n_expanded * a.p.H_kv;
     if (blocks > 0x7fffffffLL) return RA_ERR_RANGE;
-    paged_expand_kernel<D><<<(unsigned)blocks, kExpandThreads, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return RA_ERR_LAUNCH;
+    if (!launch_early(paged_expand_kernel<D>, blocks, kExpandThreads, 0, stream, a))
+      return RA_ERR_LAUNCH;
     p.k = reinterpret_cast<uint8_t*>(a.expanded_k);
     p.v = reinterpret_cast<uint8_t*>(a.expanded_v);
     p.n_pages = a.B * a.n_expanded;
@@ -611,15 +612,15 @@ ra_status launch_tiles(const PagedAttnArgs& a, cudaStream_t stream) {
     p.quant = 0;
   }
   if (!make_query_map(&mq, a.q, a.rows, a.H_q, D, grp, tt) ||
-      !make_page_map(&mk, p, p.k, p.page) || !make_page_map(&mv, p, p.v, p.page))
+      !make_page_map(&mk, p, p.k, p.page, 1) || !make_page_map(&mv, p, p.v, p.page, 1))
     return RA_ERR_LAUNCH;
   const long long grid = a.n_whole + (long long)(a.n_items - a.n_whole) * a.n_split;
   if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
   auto kern = paged_tiles_kernel<D, kExpanded>;
   static std::atomic<uint64_t> allowed;
   if (!allow_smem(kern, Cfg<D>::kSmemBytes, allowed)) return RA_ERR_LAUNCH;
-  kern<<<(unsigned)grid, kThreads, Cfg<D>::kSmemBytes, stream>>>(mq, mk, mv, a);
-  return cudaGetLastError() == cudaSuccess ? RA_OK : RA_ERR_LAUNCH;
+  return launch_early(kern, grid, kThreads, Cfg<D>::kSmemBytes, stream, mq, mk, mv, a)
+             ? RA_OK : RA_ERR_LAUNCH;
 }
 
 }  // namespace
