@@ -225,8 +225,8 @@ def _stream(stream):
     the Stream object that torch.cuda.current_stream() builds: 3 us a call)."""
     if stream is not None:
         return stream.cuda_stream
-    torch = _T or _import_torch()
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    c = (_T or _import_torch())._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _dev(t, name):
@@ -849,7 +849,7 @@ def _with_cache(cache, tensors, names):
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             _dev(t, names[i])
             raise ValueError(f"{names[i]} and the cache are on different devices")
-    if dev != _T.cuda.current_device():
+    if dev != _T._C._cuda_getDevice():
         raise ValueError("the call's tensors must be on the current CUDA device")
 
 
@@ -1093,12 +1093,23 @@ def paged_cache(n_pages, H_kv, page, D, dtype=None, device="cuda"):
     return PagedCache(*parts)
 
 
-def _table(table, B):
-    """The width of a table int32 [B, width]."""
-    if table.dim() != 2:
+def _paged_args(cache, table, names, tensors, ints, dev_status):
+    """The checks that the paged calls share: ``table`` int32 [B, width], named
+    int32 tensors of n elements, and every tensor contiguous on the cache's
+    device. Returns the table's width."""
+    i32 = _T.int32
+    if table.dim() != 2 or table.dtype != i32:
         raise ValueError("table must be int32 [B, width]")
-    _like(table, "table", (B, table.shape[1]), (_T or _import_torch()).int32)
+    for t, name, n in ints:
+        if t is not None and (t.dtype != i32 or t.shape != (n,)):
+            _like(t, name, (n,), i32)
+    if dev_status is not None:
+        _int_buffer(dev_status, "dev_status", 1)
+    _with_cache(cache, tensors, names)
     return table.shape[1]
+
+
+_APPEND = ("table", "k", "v", "start", "n_new", "dev_status")
 
 
 def paged_append(cache, table, k, v, start, n_new=None, dev_status=None, stream=None):
@@ -1106,50 +1117,51 @@ def paged_append(cache, table, k, v, start, n_new=None, dev_status=None, stream=
     start[b] + 1, ... of the sequences whose pages ``table`` int32 [B, width]
     names; with ``n_new`` int32 [B] only the first n_new[b] tokens of a padded
     batch. start: int32 [B]. All CUDA tensors."""
-    lib = load()
+    lib = _lib or load()
     _, H_kv, _, D = cache.dims
-    if k.dim() != 4:
-        raise ValueError("k must be [B, T, H_kv, D]")
-    B, T = k.shape[:2]
-    _like(k, "k", (B, T, H_kv, D), k.dtype)
-    _like(v, "v", (B, T, H_kv, D), k.dtype)
-    width = _table(table, B)
-    _ints(start, "start", B)
-    _ints(n_new, "n_new", B)
-    _int_buffer(dev_status, "dev_status", 1)
-    code = _dtype_code(k.dtype)
-    _with_cache(cache, (table, k, v, start, n_new, dev_status),
-                ("table", "k", "v", "start", "n_new", "dev_status"))
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 4 or shape[2] != H_kv or shape[3] != D:
+        raise ValueError(f"k must be [B, T, {H_kv}, {D}]")
+    if v.shape != shape or v.dtype != dtype:
+        _like(v, "v", shape, dtype)
+    B, T = shape[0], shape[1]
+    code = _dtype_code(dtype)
+    if table.shape[0] != B:
+        raise ValueError(f"table must be int32 [{B}, width]")
+    width = _paged_args(cache, table, _APPEND, (table, k, v, start, n_new, dev_status),
+                        ((start, "start", B), (n_new, "n_new", B)), dev_status)
     st = lib.paged_append(cache._ref, table.data_ptr(), width, k.data_ptr(), v.data_ptr(),
                           start.data_ptr(), _ptr(n_new), B, T, code, _ptr(dev_status),
                           _stream(stream))
-    _check(st, "paged_append")
+    if st:
+        _check(st, "paged_append")
+
+
+_APPEND_VARLEN = ("table", "k", "v", "cu_seqlens", "start", "dev_status")
 
 
 def paged_append_varlen(cache, table, k, v, cu_seqlens, start, dev_status=None, stream=None):
     """``paged_append`` of packed tokens k, v [total, H_kv, D]: sequence b's are
     rows [cu_seqlens[b], cu_seqlens[b + 1]) (int32 [B + 1], CUDA)."""
-    torch = _T or _import_torch()
-    lib = load()
+    lib = _lib or load()
     _, H_kv, _, D = cache.dims
-    if k.dim() != 3:
-        raise ValueError("k must be [total, H_kv, D]")
-    total = k.shape[0]
-    _like(k, "k", (total, H_kv, D), k.dtype)
-    _like(v, "v", (total, H_kv, D), k.dtype)
-    if cu_seqlens.dim() != 1 or cu_seqlens.dtype != torch.int32:
-        raise ValueError("cu_seqlens must be a 1-D int32 CUDA tensor")
-    B = cu_seqlens.numel() - 1
-    width = _table(table, B)
-    _ints(start, "start", B)
-    _int_buffer(dev_status, "dev_status", 1)
-    code = _dtype_code(k.dtype)
-    _with_cache(cache, (table, k, v, cu_seqlens, start, dev_status),
-                ("table", "k", "v", "cu_seqlens", "start", "dev_status"))
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or shape[1] != H_kv or shape[2] != D:
+        raise ValueError(f"k must be [total, {H_kv}, {D}]")
+    if v.shape != shape or v.dtype != dtype:
+        _like(v, "v", shape, dtype)
+    B = table.shape[0]
+    code = _dtype_code(dtype)
+    width = _paged_args(cache, table, _APPEND_VARLEN, (table, k, v, cu_seqlens, start, dev_status),
+                        ((start, "start", B), (cu_seqlens, "cu_seqlens", B + 1)), dev_status)
     st = lib.paged_append_varlen(cache._ref, table.data_ptr(), width, k.data_ptr(), v.data_ptr(),
-                                 start.data_ptr(), cu_seqlens.data_ptr(), B, total, code,
+                                 start.data_ptr(), cu_seqlens.data_ptr(), B, shape[0], code,
                                  _ptr(dev_status), _stream(stream))
-    _check(st, "paged_append_varlen")
+    if st:
+        _check(st, "paged_append_varlen")
+
+
+_READ = ("table", "k", "v", "start", "dev_status")
 
 
 def paged_read(cache, table, start, T, dtype=None, k=None, v=None, dev_status=None, stream=None):
@@ -1157,7 +1169,7 @@ def paged_read(cache, table, start, T, dtype=None, k=None, v=None, dev_status=No
     (start None: from slot 0), bf16 unless ``dtype`` or a given k or v says
     float32; zeros where ``table`` int32 [B, width] names no page."""
     torch = _T or _import_torch()
-    lib = load()
+    lib = _lib or load()
     _, H_kv, _, D = cache.dims
     if dtype is None:
         given = k if k is not None else v
@@ -1167,22 +1179,25 @@ def paged_read(cache, table, start, T, dtype=None, k=None, v=None, dev_status=No
     if T <= 0:
         raise ValueError("T must be positive")
     B = table.shape[0]
-    width = _table(table, B)
     shape = (B, T, H_kv, D)
-    _like(k, "k", shape, dtype)
-    _like(v, "v", shape, dtype)
-    _ints(start, "start", B)
-    _int_buffer(dev_status, "dev_status", 1)
-    _with_cache(cache, (table, k, v, start, dev_status), ("table", "k", "v", "start", "dev_status"))
-    T = _int32(T)
-    with _on_stream(stream):
-        if k is None:
-            k = torch.empty(shape, dtype=dtype, device=table.device)
-        if v is None:
-            v = torch.empty(shape, dtype=dtype, device=table.device)
+    if k is not None:
+        _like(k, "k", shape, dtype)
+    if v is not None:
+        _like(v, "v", shape, dtype)
+    width = _paged_args(cache, table, _READ, (table, k, v, start, dev_status),
+                        ((start, "start", B),), dev_status)
+    if k is None or v is None:
+        if stream is None:
+            k = torch.empty(shape, dtype=dtype, device=table.device) if k is None else k
+            v = torch.empty_like(k) if v is None else v
+        else:
+            with torch.cuda.stream(stream):
+                k = torch.empty(shape, dtype=dtype, device=table.device) if k is None else k
+                v = torch.empty_like(k) if v is None else v
     st = lib.paged_read(cache._ref, table.data_ptr(), width, _ptr(start), k.data_ptr(),
-                        v.data_ptr(), B, T, code, _ptr(dev_status), _stream(stream))
-    _check(st, "paged_read")
+                        v.data_ptr(), B, _int32(T), code, _ptr(dev_status), _stream(stream))
+    if st:
+        _check(st, "paged_read")
     return k, v
 
 
@@ -1206,47 +1221,56 @@ def paged_attn_workspace_bytes(cache, B, S_q, H_q, max_len, window=0, n_sink=0, 
                             int(total is not None))
 
 
+_ATTN = ("q", "table", "lens", "cu_seqlens", "out", "lse", "workspace", "dev_status")
+
+
 def _paged_attn(q, cache, table, lens, cu_seqlens, B, S_q, total, max_len, window, n_sink, scale,
                 out, lse, workspace, dev_status, stream):
     """Both forms of the attention; ``cu_seqlens`` None: [B, S_q, H_q, D]."""
     torch = _T or _import_torch()
-    lib = load()
-    D = cache.dims[3]
+    lib = _lib or load()
     H_q = q.shape[-2]
-    width = _table(table, B)
-    max_len = width * cache.dims[2] if max_len is None else max_len
-    S_q, max_len, window, n_sink = _int32(S_q), _int32(max_len), _int32(window), _int32(n_sink)
-    lse_shape = (B, H_q, S_q) if cu_seqlens is None else (H_q, total)
-    _like(out, "out", q.shape, q.dtype)
-    _like(lse, "lse", lse_shape, torch.float32)
-    _ints(lens, "lens", B)
-    _int_buffer(dev_status, "dev_status", 1)
+    packed = cu_seqlens is not None
+    lse_shape = (H_q, total) if packed else (B, H_q, S_q)
+    code = _dtype_code(q.dtype)
+    if out is not None:
+        _like(out, "out", q.shape, q.dtype)
+    if lse is not None:
+        _like(lse, "lse", lse_shape, torch.float32)
     if workspace is not None and workspace.dtype != torch.uint8:
         raise ValueError("workspace must be a uint8 tensor")
-    code = _dtype_code(q.dtype)
-    _with_cache(cache, (q, table, lens, cu_seqlens, out, lse, workspace, dev_status),
-                ("q", "table", "lens", "cu_seqlens", "out", "lse", "workspace", "dev_status"))
-    with _on_stream(stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
-        if workspace is None:
-            need = _paged_workspace(cache.dims, len(cache) > 2, B, S_q, total, H_q, max_len, window,
-                                    n_sink, int(cu_seqlens is not None))
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    sizes = (H_q, max_len, window, n_sink, 0.0 if scale is None else float(scale), code,
-             _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(dev_status),
-             _stream(stream))
-    if cu_seqlens is None:
-        st = lib.paged_attn(q.data_ptr(), cache._ref, table.data_ptr(), width, lens.data_ptr(),
-                            out.data_ptr(), lse.data_ptr(), B, S_q, *sizes)
-    else:
+    if table.shape[0] != B:
+        raise ValueError(f"table must be int32 [{B}, width]")
+    width = _paged_args(cache, table, _ATTN,
+                        (q, table, lens, cu_seqlens, out, lse, workspace, dev_status),
+                        ((lens, "lens", B), (cu_seqlens, "cu_seqlens", B + 1)), dev_status)
+    # (lengths are counted in 30 bits, whatever a table is wide)
+    max_len = min(width * cache.dims[2], 1 << 30) if max_len is None else _int32(max_len)
+    S_q, window, n_sink = _int32(S_q), _int32(window), _int32(n_sink)
+    if out is None or lse is None or workspace is None:
+        with _on_stream(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if lse is None:
+                lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+            if workspace is None:
+                need = _paged_workspace(cache.dims, len(cache) > 2, B, S_q, total, H_q, max_len,
+                                        window, n_sink, packed)
+                if need:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    sc = 0.0 if scale is None else float(scale)
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    if packed:
         st = lib.paged_attn_varlen(q.data_ptr(), cache._ref, table.data_ptr(), width,
                                    lens.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(),
-                                   lse.data_ptr(), B, total, S_q, *sizes)
-    _check(st, "paged_attn" if cu_seqlens is None else "paged_attn_varlen")
+                                   lse.data_ptr(), B, total, S_q, H_q, max_len, window, n_sink, sc,
+                                   code, ws, ws_bytes, _ptr(dev_status), _stream(stream))
+    else:
+        st = lib.paged_attn(q.data_ptr(), cache._ref, table.data_ptr(), width, lens.data_ptr(),
+                            out.data_ptr(), lse.data_ptr(), B, S_q, H_q, max_len, window, n_sink,
+                            sc, code, ws, ws_bytes, _ptr(dev_status), _stream(stream))
+    if st:
+        _check(st, "paged_attn_varlen" if packed else "paged_attn")
     return out, lse
 
 
@@ -1262,9 +1286,10 @@ def paged_attn(q, cache, table, lens, max_len=None, window=0, n_sink=0, scale=No
     [B, H_q, S_q]). A ``workspace`` (uint8, ``paged_attn_workspace_bytes``) is
     allocated here when not given; calls that may overlap need their own.
     """
-    if q.dim() != 4 or q.shape[3] != cache.dims[3]:
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != cache.dims[3]:
         raise ValueError("q must be [B, S_q, H_q, D] matching the cache")
-    B, S_q = q.shape[:2]
+    B, S_q = shape[0], shape[1]
     return _paged_attn(q, cache, table, lens, None, B, S_q, B * S_q, max_len, window, n_sink, scale,
                        out, lse, workspace, dev_status, stream)
 
@@ -1276,14 +1301,11 @@ def paged_attn_varlen(q, cache, table, lens, cu_seqlens, max_seqlen, max_len=Non
     at most ``max_seqlen``, are rows [cu_seqlens[b], cu_seqlens[b + 1]) (int32
     [B + 1], CUDA): pieces of prompts behind what is cached, and single tokens.
     Returns (out [total, H_q, D], lse [H_q, total])."""
-    torch = _T or _import_torch()
-    if q.dim() != 3 or q.shape[2] != cache.dims[3]:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.dims[3]:
         raise ValueError("q must be [total, H_q, D] matching the cache")
-    if cu_seqlens.dim() != 1 or cu_seqlens.dtype != torch.int32:
-        raise ValueError("cu_seqlens must be a 1-D int32 CUDA tensor")
-    return _paged_attn(q, cache, table, lens, cu_seqlens, cu_seqlens.numel() - 1, max_seqlen,
-                       q.shape[0], max_len, window, n_sink, scale, out, lse, workspace, dev_status,
-                       stream)
+    return _paged_attn(q, cache, table, lens, cu_seqlens, table.shape[0], max_seqlen, shape[0],
+                       max_len, window, n_sink, scale, out, lse, workspace, dev_status, stream)
 
 
 def expiry_test(q, k, v, out, lse, dev_status, stream=None):

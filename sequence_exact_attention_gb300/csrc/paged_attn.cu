@@ -764,12 +764,14 @@ paged_join_few_kernel(const PagedAttnArgs a, int rows) {
   store_row<D>(a, blk, sq, r / grp, r % grp, d, y, m, l);
 }
 
-// Many rows: a CTA joins `rows` rows of one block (a power of two), first all their
-// weights, then all their outputs, so that what it looks up and waits for comes once.
-// (A warp for every row took 25 us of 19456 rows of two chunks, a CTA 32.)
-template <int D>
+// Many rows: a CTA joins some rows of one block, kAtOnce outputs of four values a
+// thread, first all the rows' weights, then their outputs, so that what it looks up and
+// waits for comes once. (A CTA for every row took 32 us of 19456 rows of two chunks, a
+// warp 25, one output after the other 18, four at once 11.)
+template <int D, int kAtOnce>
 __global__ void __launch_bounds__(kJoinThreads)
-paged_join_many_kernel(const PagedAttnArgs a, int rows) {
+paged_join_many_kernel(const PagedAttnArgs a) {
+  constexpr int rows = kAtOnce * kJoinThreads / (D / 4);
   extern __shared__ float2 sW[];             // [n_split][rows] (weight, sum), [rows] (maximum, sum)
   let_dependents_start();
   const int per = a.block_rows / rows;
@@ -801,24 +803,33 @@ paged_join_many_kernel(const PagedAttnArgs a, int rows) {
     sW[a.n_split * rows + threadIdx.x] = make_float2(m, l);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kJoinThreads) {
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
-    const int t = token(r0 + r);
-    if (t < 0) continue;
-    const float* o = a.part_o + paged_part(a, item, 0, r0 + r) * D + d;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* o[kAtOnce];
+  float4 y[kAtOnce];
+  const int d = threadIdx.x % (D / 4) * 4, first = threadIdx.x / (D / 4);
+  constexpr int kStep = kJoinThreads / (D / 4);       // rows that the CTA's threads make at a time
+#pragma unroll
+  for (int e = 0; e < kAtOnce; ++e) {
+    o[e] = a.part_o + paged_part(a, item, 0, r0 + first + e * kStep) * D + d;
+    y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
 #pragma unroll 4
-    for (int s = 0; s < a.n_split; ++s) {
-      const float4 f = *reinterpret_cast<const float4*>(o + (size_t)s * a.block_rows * D);
-      const float w = sW[s * rows + r].x;
-      if (w < 0.f) continue;
-      y.x = fmaf(w, f.x, y.x);
-      y.y = fmaf(w, f.y, y.y);
-      y.z = fmaf(w, f.z, y.z);
-      y.w = fmaf(w, f.w, y.w);
+  for (int s = 0; s < a.n_split; ++s)
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) {
+      const float4 f = *reinterpret_cast<const float4*>(o[e] + (size_t)s * a.block_rows * D);
+      const float x = sW[s * rows + first + e * kStep].x;
+      const bool seen = !(x < 0.f);
+      y[e].x = fmaf(seen ? x : 0.f, seen ? f.x : 0.f, y[e].x);
+      y[e].y = fmaf(seen ? x : 0.f, seen ? f.y : 0.f, y[e].y);
+      y[e].z = fmaf(seen ? x : 0.f, seen ? f.z : 0.f, y[e].z);
+      y[e].w = fmaf(seen ? x : 0.f, seen ? f.w : 0.f, y[e].w);
     }
+#pragma unroll
+  for (int e = 0; e < kAtOnce; ++e) {
+    const int r = first + e * kStep, t = token(r0 + r);
+    if (t < 0) continue;
     const float2 ml = sW[a.n_split * rows + r];
-    store_row<D>(a, blk, sq, t, ((r0 + r) & 127) % grp, d, y, ml.x, ml.y);
+    store_row<D>(a, blk, sq, t, ((r0 + r) & 127) % grp, d, y[e], ml.x, ml.y);
   }
 }
 
@@ -851,21 +862,24 @@ ra_status launch_paged_rows(const PagedAttnArgs& a, cudaStream_t stream) {
 
 ra_status launch_paged_join(const PagedAttnArgs& a, cudaStream_t stream) {
   const long long items = a.n_items - a.n_whole;
-  int rows, smem = 0;
-  long long grid;
-  auto kern = a.p.D == 64 ? paged_join_few_kernel<64> : paged_join_few_kernel<128>;
   if (a.block_rows <= 16) {
-    rows = a.T * (a.H_q / a.p.H_kv);         // those that may hold a token
-    grid = items * rows;
-  } else {
-    kern = a.p.D == 64 ? paged_join_many_kernel<64> : paged_join_many_kernel<128>;
-    rows = 64;                               // fewer where CTAs would be, too
-    while (rows > 8 && items * (a.block_rows / rows) < 2 * 152) rows /= 2;
-    grid = items * (a.block_rows / rows);
-    smem = (a.n_split + 1) * rows * (int)sizeof(float2);
+    const int rows = a.T * (a.H_q / a.p.H_kv);           // those that may hold a token
+    const long long grid = items * rows;
+    if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
+    auto kern = a.p.D == 64 ? paged_join_few_kernel<64> : paged_join_few_kernel<128>;
+    return launch_early(kern, grid, kJoinThreads, 0, stream, a, rows) ? RA_OK : RA_ERR_LAUNCH;
   }
+  // a quarter of the rows a CTA where CTAs would be few
+  int rows = 4 * kJoinThreads / (a.p.D / 4);
+  auto kern = a.p.D == 64 ? paged_join_many_kernel<64, 4> : paged_join_many_kernel<128, 4>;
+  if (items * (a.block_rows / rows) < 2 * 152) {
+    rows /= 4;
+    kern = a.p.D == 64 ? paged_join_many_kernel<64, 1> : paged_join_many_kernel<128, 1>;
+  }
+  const long long grid = items * (a.block_rows / rows);
   if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
-  return launch_early(kern, grid, kJoinThreads, smem, stream, a, rows) ? RA_OK : RA_ERR_LAUNCH;
+  const int smem = (a.n_split + 1) * rows * (int)sizeof(float2);
+  return launch_early(kern, grid, kJoinThreads, smem, stream, a) ? RA_OK : RA_ERR_LAUNCH;
 }
 
 }  // namespace ra

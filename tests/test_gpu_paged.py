@@ -138,6 +138,12 @@ CASES = [
     ("prompt_tiles", [640, 257], [640, 257], 4, 4, 64, 128, 5, 0, 0),
     ("prompt_few_rows_long", [6000], [40], 4, 1, 128, 128, 47, 0, 0),
     ("prompt_window_d128", [900, 520], [400, 520], 4, 2, 128, 64, 15, 200, 10),
+    ("group_of_128", [70, 3], [1, 1], 128, 1, 64, 16, 5, 0, 0),
+    ("group_of_100", [70, 40], [3, 2], 100, 1, 128, 32, 3, 0, 0),
+    ("a_wide_table", [300, 129, 40], [200, 1, 40], 4, 2, 64, 16, 20000, 0, 0),
+    ("many_sequences", [3 * i % 50 for i in range(70)], [(3 * i % 50) * (i % 3) // 2 for i in range(70)], 2, 1, 64, 16, 4, 0,
+     0),
+    ("many_single_tokens", [7 * i % 90 for i in range(67)], [1] * 67, 2, 2, 64, 32, 3, 20, 1),
 ]
 
 
@@ -518,3 +524,99 @@ def test_both_libraries_agree():
                 binding.use_library(prev)
         for x, y in zip(res["release"], res["debug"]):
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def reference(q, cache, table, lens, news, rows, window, n_sink):
+    """(out, lse, terms) of sampled packed rows in float64 on the GPU; terms are
+    the sums that the tolerances are made of: of |s|'s addends, of p |v|."""
+    page, D = cache.dims[2], cache.dims[3]
+    H_kv, H_q = cache.dims[1], q.shape[1]
+    k, v = (t.double() if len(cache) == 2 else t.view(torch.uint8).view(E4M3).double() for t in cache[:2])
+    if len(cache) > 2:
+        k, v = (t * torch.exp2(e.double() - 127)[..., None] for t, e in zip((k, v), cache[2:]))
+    first = np.concatenate([[0], np.cumsum(news)])
+    res = []
+    for r in rows:
+        b = int(np.searchsorted(first, r, side="right") - 1)
+        p = lens[b] - news[b] + (r - first[b])
+        j = torch.arange(p + 1, device=DEV)
+        if window:
+            j = j[(j > p - window) | (j < n_sink)]
+        at, row = table[b, j // page].long(), j % page
+        kk, vv = (x[at, :, row].repeat_interleave(H_q // H_kv, 1) for x in (k, v))      # [n, H_q, D]
+        x = q[r].double()
+        s = (kk * x).sum(-1) * D ** -0.5                                                # [n, H_q]
+        lse = torch.logsumexp(s, 0)
+        w = torch.exp(s - lse)
+        e = ((kk * x).abs().sum(-1) * D ** -0.5).amax(0) * (D + 8) * 2.0 ** -23
+        rel = 2 * e + 2.0 ** -20 * (1 + s.abs().amax(0)) + j.numel() * 2.0 ** -24
+        res.append(((w[..., None] * vv).sum(0), lse, rel, (w[..., None] * vv.abs()).sum(0)))
+    return res
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", [
+    # lens, new tokens, H_q, H_kv, D, page, window, n_sink, max_len: what the launch is cut by
+    ([10000], [10000], 4, 4, 64, 64, 0, 0, None),                   # more blocks than multiprocessors, and a rest
+    ([9000, 5000], [3000, 5000], 16, 4, 128, 16, 0, 0, None),       # packed, a rest
+    ([9000, 5000], [3000, 5000], 8, 4, 128, 128, 700, 5, 1 << 20),  # head by head
+    ([40000, 40000], [100, 100], 8, 1, 128, 128, 0, 0, None),       # a few blocks, cut many times
+    ([70000, 50, 33000, 1], [1, 1, 1, 1], 8, 2, 64, 32, 0, 0, None),
+    ([70000, 50, 33000, 2], [2, 2, 2, 2], 16, 2, 128, 16, 0, 0, None),
+], ids=str)
+def test_large_calls(case, kind):
+    lens, news, H_q, H_kv, D, page, window, n_sink, max_len = case
+    g = torch.Generator(device=DEV).manual_seed(sum(lens))
+    width = -(-max(lens) // page)
+    held = [-(-n // page) for n in lens]
+    table = torch.full((len(lens), max(width, -(-(max_len or 0) // page))), -1, dtype=torch.int32, device=DEV)
+    ids, at = torch.randperm(sum(held), generator=g, device=DEV).int(), 0
+    for b, n in enumerate(held):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    cache = binding.paged_cache(sum(held), H_kv, page, D, dtype=torch.bfloat16 if kind == "bf16" else E4M3)
+    n = max(lens)
+    for lo in range(0, n, 8192):            # the whole axis, appended in pieces
+        t = min(8192, n - lo)
+        k, v = (torch.randn(len(lens), t, H_kv, D, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+        left = ints([min(max(x - lo, 0), t) for x in lens])
+        binding.paged_append(cache, table, k, v, ints([lo] * len(lens)), n_new=left)
+    q = torch.randn(sum(news), H_q, D, generator=g, device=DEV).to(torch.bfloat16)
+    cu = ints(np.concatenate([[0], np.cumsum(news)]).tolist())
+    st = status_word()
+    out, lse = binding.paged_attn_varlen(q, cache, table, ints(lens), cu, max(news), max_len=max_len, window=window,
+                                         n_sink=n_sink, dev_status=st)
+    again, again_l = binding.paged_attn_varlen(q, cache, table, ints(lens), cu, max(news), max_len=max_len, window=window,
+                                               n_sink=n_sink)
+    assert int(st.item()) == 0
+    assert torch.equal(out, again) and torch.equal(lse, again_l)
+    ends = np.cumsum(news)
+    rows = sorted(set(np.random.default_rng(0).integers(0, sum(news), 40).tolist()) | {0} | set((ends - 1).tolist()) |
+                  {x for x in (127, 128, 255, 256, 5119) if x < sum(news)})
+    u_w = 2.0 ** -8 if kind == "bf16" or max(news) * H_q // H_kv > 16 else 2.0 ** -11
+    for r, (want, want_l, rel, pv) in zip(rows, reference(q, cache, table, lens, news, rows, window, n_sink)):
+        assert bool(((out[r].double() - want).abs() <= want.abs() * 2.0 ** -8 + (rel + u_w)[:, None] * pv).all()), r
+        assert bool(((lse[:, r].double() - want_l).abs() <= rel).all()), r
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_values_outside_the_block_may_be_anything(kind):
+    """Many rows: values that no row of a block of tokens sees (the next
+    block's, those behind every window, past the end) change no bit of its
+    results, finite or not."""
+    H, D, page = 1, 64, 16
+    lens, n_new, group = 700, 400, 2                        # blocks of 128 tokens
+    pool = Pool(kind, H, page, D, [lens], 50, seed=21)
+    q = torch.randn(1, n_new, H * group, D, device=DEV).to(torch.bfloat16)
+    kw = dict(window=150, n_sink=3)
+    out, lse = binding.paged_attn(q, pool.cache, pool.table_d, ints([lens]), **kw)
+    # the second block's tokens are at 428 to 555, the first sees 279 (151 + 128) to 427
+    for slots in (range(428, lens), range(3, 300 - 150 + 1)):
+        for j in slots:
+            at, row = pool.table[0, j // page], j % page
+            pool.cache.v.view(torch.uint8)[at, :, row] = 0x7f          # NaN in e4m3, in bf16 0x7f7f is finite
+            if kind == "bf16":
+                pool.cache.v[at, :, row] = float("nan")
+    got, got_l = binding.paged_attn(q, pool.cache, pool.table_d, ints([lens]), **kw)
+    assert torch.equal(got[:, :128], out[:, :128]) and torch.equal(got_l, lse)
+    assert bool(got[:, 128:].isnan().all())
