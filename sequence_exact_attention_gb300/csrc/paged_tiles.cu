@@ -16,9 +16,11 @@
 // workspace: exact, as a code times its row's power of two is a bf16 number. It
 // moves 5 bytes a value where the products take 4 D flops a row and value pair.
 //
-// Roles (320 threads): warps 0-7 softmax, two threads a query row, 64 columns each,
+// Roles (384 threads): warps 0-7 softmax, two threads a query row, 64 columns each,
 // for Q0 and then Q1 at every tile; a producer warp; an issuer warp whose elected
-// lane issues every MMA. Tensor memory: S_i (128 f32 columns) at 128 i, over whose
+// lane issues every MMA; two warps that keep values that are not finite from rows that
+// do not see them (in the softmax warps' hands this took 4 to 8 us of 90 under a
+// window). Tensor memory: S_i (128 f32 columns) at 128 i, over whose
 // first 64 the weights are written as bf16; O_i (D columns) at 256 + D i. Per tile
 // j the tensor core runs PV0(j) S0(j+1) PV1(j) S1(j+1), one tile's products under
 // the other's softmax. Barriers:
@@ -26,7 +28,7 @@
 //   kfull/vfull[s]   keys / values of a tile landed in slot s
 //   done[j mod kKBuf] every MMA up to S1(j) is done: K_j's and V_{j-1}'s slots are free
 //   sfull[i]         S_i(j) done; it covers PV_i(j-1)
-//   pfull[i]         P_i(j) written, O_i rescaled (256 arrivals)
+//   pfull[i]         P_i(j) written, O_i rescaled (256 arrivals), V_j checked (64, i = 0)
 //   odone[i]         the last PV_i done
 // Every wait is bounded: after kTimeoutNs a thread raises the CTA's abort flag, all
 // roles fall through to the teardown, which waits (bounded) for copies and MMAs in
@@ -56,8 +58,8 @@ using tc::kBoxBytes;
 using tc::kTile;
 
 constexpr int kSoftmaxWarps = 8;
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 32 * 10;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kCheckWarp = 10, kCheckWarps = 2;
+constexpr int kThreads = 32 * (kCheckWarp + kCheckWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;
 constexpr float kRescaleLog2 = 8.0f;       // O is rescaled when the maximum grows by more
@@ -78,7 +80,13 @@ struct Cfg {
   // maxima [2 parities][2 parts][128 rows], sums [2 tiles][2 parts][128 rows]
   static constexpr int kRedOff = kBarOff + kBarBytes;
   static constexpr int kRedBytes = (512 + 512) * 4;
-  static constexpr int kUsed = kRedOff + kRedBytes + 1024;   // + alignment slack
+  // values that are not finite, of tiles that rows differ in: a bit each, [kEdges][128
+  // slots][D / 32]. The block's 256 positions make at most three such tiles at each end
+  // of a window, the first slots' last tile one more.
+  static constexpr int kEdges = 7;
+  static constexpr int kOddOff = kRedOff + kRedBytes;
+  static constexpr int kOddBytes = kEdges * kTile * (D / 32) * 4;
+  static constexpr int kUsed = kOddOff + kOddBytes + 1024;   // + alignment slack
   // more than half an SM's shared memory: one CTA an SM, so the allocation of all
   // tensor memory never waits for another CTA
   static constexpr int kSmemBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
@@ -91,7 +99,9 @@ struct Cfg {
   static constexpr int bODone = bPFull + 2;         // [2]
   static constexpr int bFinal = bODone + 2;
   static constexpr int kNumBars = bFinal + 1;
-  static constexpr int kGoneOff = kBarBytes - 48;     // [8] pages not there, of tile j at j mod 8
+  static constexpr int kGoneOff = kBarBytes - 88;     // [8] pages not there, of tile j at j mod 8
+  static constexpr int kEdgeOff = kBarBytes - 56;     // [kEdges] first slots of the tiles of kOddOff
+  static constexpr int kAnyOff = kBarBytes - 24;      // how many of them have a bit set, or 0
   static constexpr int kHolderOff = kBarBytes - 16;   // tensor memory's address
   static constexpr int kNeverOff = kBarBytes - 12;    // stays 0: waits that ignore aborts
   static constexpr int kAbortOff = kBarBytes - 8;     // abort flag
@@ -101,10 +111,57 @@ struct Cfg {
   static_assert(kOCol + 2 * D <= kTmemCols, "tensor memory budget");
 };
 
-// Rows [from, to) of a tile of 64-column boxes, as 0, by the 256 softmax threads.
+// Notes the values of a tile's rows [from, to) that are not finite, but not those of
+// rows [skip_from, skip_to), in `odd` [128][D / 32] and makes them 0: a row that does
+// not see them has the weight 0 for them. By the checking threads.
+// Says whether this thread found any.
+template <int D>
+__device__ __forceinline__ bool take_odd_values(uint8_t* tile, int to, int skip_from, int skip_to,
+                                                uint32_t* odd, int thread) {
+  constexpr uint32_t kOnes = 0x7f807f80u;              // two exponents
+  // first whether there are any: an exponent of ones carries into its sign
+  constexpr int kEach = kTile * (D / 8) / (32 * kCheckWarps);
+  uint32_t found = 0;
+#pragma unroll 8
+  for (int x = 0; x < kEach; ++x) {
+    const uint4 v = reinterpret_cast<const uint4*>(tile)[thread + x * 32 * kCheckWarps];
+    found |= ((v.x & kOnes) + 0x00800080u) | ((v.y & kOnes) + 0x00800080u) |
+             ((v.z & kOnes) + 0x00800080u) | ((v.w & kOnes) + 0x00800080u);
+  }
+  if (!__any_sync(0xffffffffu, found & 0x80008000u)) return false;
+  bool noted = false;
+  for (int x = 0; x < kEach; ++x) {
+    const int i = thread + x * 32 * kCheckWarps;       // 16 bytes, eight values
+    const int row = i / 8 % kTile, chunk = i / (8 * kTile) * 8 + ((i ^ row) & 7);
+    if (row >= to || (row >= skip_from && row < skip_to)) continue;
+    uint4* at = reinterpret_cast<uint4*>(tile) + i;
+    const uint4 v = *at;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, bits = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t e = w[k] & kOnes;
+      if ((e & 0xffffu) == (kOnes & 0xffffu)) {
+        bits |= 1u << (2 * k);
+        w[k] &= 0xffff0000u;
+      }
+      if ((e >> 16) == (kOnes >> 16)) {
+        bits |= 2u << (2 * k);
+        w[k] &= 0x0000ffffu;
+      }
+    }
+    if (bits) {
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
+      atomicOr(odd + row * (D / 32) + chunk / 4, bits << (8 * (chunk % 4)));
+      noted = true;
+    }
+  }
+  return noted;
+}
+
+// Rows [from, to) of a tile of 64-column boxes, as 0, by the checking threads.
 __device__ __forceinline__ void zero_rows(uint32_t tile, int boxes, int from, int to, int thread) {
   for (int bx = 0; bx < boxes; ++bx)
-    for (int i = thread; i < (to - from) * 8; i += 32 * kSoftmaxWarps)
+    for (int i = thread; i < (to - from) * 8; i += 32 * kCheckWarps)
       asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                        tile + (uint32_t)(bx * kBoxBytes + from * 128 + i * 16)),
                    "r"(0)
@@ -141,6 +198,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(base_ptr + C::kBarOff + C::kHolderOff);
   volatile uint32_t* gone = reinterpret_cast<volatile uint32_t*>(base_ptr + C::kBarOff + C::kGoneOff);
 
+  uint32_t* odd = reinterpret_cast<uint32_t*>(base_ptr + C::kOddOff);
+  volatile int* edge_lo = reinterpret_cast<volatile int*>(base_ptr + C::kBarOff + C::kEdgeOff);
+  volatile int* any_odd = reinterpret_cast<volatile int*>(base_ptr + C::kBarOff + C::kAnyOff);
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   let_dependents_start();
@@ -170,7 +231,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::bQFull + i), 1);
       mbar_init(bar(C::bSFull + i), 1);
-      mbar_init(bar(C::bPFull + i), 32 * kSoftmaxWarps);
+      mbar_init(bar(C::bPFull + i), 32 * (kSoftmaxWarps + (i == 0 ? kCheckWarps : 0)));
       mbar_init(bar(C::bODone + i), 1);
     }
     for (int i = 0; i < C::kKBuf; ++i) {
@@ -181,8 +242,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
     mbar_init(bar(C::bFinal), 1);
     *abort_flag = 0;
     *never = 0;
+    *any_odd = 0;
     fence_mbar_init();
   }
+  for (int i = threadIdx.x; i < C::kOddBytes / 16; i += kThreads)
+    reinterpret_cast<uint4*>(base_ptr + C::kOddOff)[i] = make_uint4(0, 0, 0, 0);
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(tmem_holder), kTmemCols);
     tmem_relinquish();
@@ -348,6 +412,42 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
       mbar_wait(bar(C::bFinal), 0, never, kTimeoutNs);
     }
     __syncwarp();
+  } else if (warp >= kCheckWarp) {
+    // ======================= values that rows must not see =======================
+    // Where rows differ in what they see, hidden values have weight 0, which NaN and
+    // infinities would survive: those that no row of the block sees are made 0, others
+    // that are not finite are noted for the rows that see them.
+    const int thread = threadIdx.x - 32 * kCheckWarp;
+    // no row sees the slots from n_sink to dead_to, nor from sp.hi on
+    const int dead_to = a.window > 0 ? first - a.window + 1 : 0;
+    int n_edges = 0;
+    bool found = false;
+    for (int j = 0; j < n; ++j) {
+      const int lo = tile_lo(j);
+      if (!sp.whole(a, lo, kTile)) {
+        const int vs = j % C::kVBuf;
+        if (!mbar_wait_warp(bar(C::bVFull + vs), (uint32_t)(j / C::kVBuf) & 1, abort_flag,
+                            kTimeoutNs))
+          break;
+        const int z0 = max(a.n_sink - lo, 0), z1 = min(dead_to - lo, kTile);
+        const int z2 = min(max(sp.hi - lo, 0), kTile);
+        uint8_t* tile = base_ptr + C::kVOff + vs * C::kTileBytes;
+        if (z0 < z1) zero_rows(smem_u32(tile), C::kBoxes, z0, z1, thread);
+        if (z2 < kTile) zero_rows(smem_u32(tile), C::kBoxes, z2, kTile, thread);
+        if (n_edges < C::kEdges) {
+          found |= take_odd_values<D>(tile, z2, z0, z1, odd + n_edges * kTile * (D / 32), thread);
+          if (thread == 0) edge_lo[n_edges] = lo;
+          ++n_edges;
+        }
+        fence_proxy_async_smem();
+      }
+      // an arrival a phase: the next one's follows when this one is over
+      mbar_arrive(bar(C::bPFull));
+      if (j + 1 < n && !mbar_wait_warp(bar(C::bPFull), (uint32_t)j & 1, abort_flag, kTimeoutNs))
+        break;
+    }
+    if (found) *any_odd = n_edges;                // of those noted, one writes at least
+    tc::named_bar_sync(5, 32 * (kSoftmaxWarps + kCheckWarps));
   } else {
     // ============ softmax: two threads a query row, Q0 and Q1 in turn ============
     // Warps w and w + 4 share TMEM lane quarter w % 4 (the same 32 rows of each
@@ -365,8 +465,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
     float* red = reinterpret_cast<float*>(base_ptr + C::kRedOff);
     const int tok = row / grp;                    // the row's token in its tile
     const int shift = 31 - __clz(a.p.page);
-    // no row of the block sees the slots from n_sink to dead_to, nor from sp.hi on
-    const int dead_to = a.window > 0 ? first - a.window + 1 : 0;
     int ex = 0;                                   // exchanges so far (buffer parity)
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     bool ok = true;
@@ -450,20 +548,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
         // parts take the same decision for a row.
         if (__any_sync(0xffffffffu, resc) && j > 0)
           tc::scale_cols<D / 2>(tmem + t_lane + kOCol + (uint32_t)(qi * D + part * (D / 2)), alpha);
-        // values that no row of the block sees have weight 0, which NaN would survive
-        if (qi == 0) {
-          const int z0 = max(a.n_sink - lo, 0), z1 = min(dead_to - lo, kTile);
-          const int z2 = max(sp.hi - lo, 0);
-          if (z0 < z1 || z2 < kTile) {
-            const int vs = j % C::kVBuf;
-            ok = mbar_wait_warp(bar(C::bVFull + vs), (uint32_t)(j / C::kVBuf) & 1, abort_flag,
-                                kTimeoutNs);
-            const uint32_t tile = base + C::kVOff + vs * C::kTileBytes;
-            if (ok && z0 < z1) zero_rows(tile, C::kBoxes, z0, z1, threadIdx.x);
-            if (ok && z2 < kTile) zero_rows(tile, C::kBoxes, z2, kTile, threadIdx.x);
-            fence_proxy_async_smem();
-          }
-        }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar(C::bPFull + qi));
@@ -473,7 +557,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
     // ---- epilogue: out = O / l, lse = ln2 (m + log2 l), l = sum of both parts
     float* red_l = red + 512;
     for (int qi = 0; qi < ntile; ++qi) red_l[(qi * 2 + part) * 128 + row] = l_run[qi];
-    tc::named_bar_sync(pair_bar, 64);
+    tc::named_bar_sync(5, 32 * (kSoftmaxWarps + kCheckWarps));     // what those noted is there
     for (int qi = 0; qi < ntile; ++qi) {
       const float ls = red_l[qi * 256 + row] + red_l[qi * 256 + 128 + row];
       const int t = t0 + qi * tt + tok;
@@ -487,6 +571,16 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
       const long long orow = (long long)(sq.row0 + t) * a.H_q + h;
       const uint32_t tO = tmem + t_lane + kOCol + (uint32_t)(qi * D + part * (D / 2));
       const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);   // 0: no slot; NaN stays
+      // this part's dimensions in which the row sees a value that is not finite
+      uint32_t bad[D / 64] = {};
+      if (*any_odd) {
+        const int q_pos = first + qi * tt + tok;
+        for (int i = 0; i < *any_odd * kTile; ++i) {
+          if (!paged_sees(a, q_pos, edge_lo[i / kTile] + i % kTile)) continue;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) bad[c] |= odd[i * (D / 32) + part * (D / 64) + c];
+        }
+      }
       const long long prow = paged_part(a, work.item, work.split, qi * kTile + row);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -499,6 +593,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
           for (int i = 0; i < 32; ++i) uo[i] = 0u;
         }
         if (!valid) continue;
+        if (bad[c]) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (bad[c] >> i & 1u) uo[i] = 0x7fc00000u;
+        }
         const int col = part * (D / 2) + c * 32;
         if (work.split >= 0) {
           if (n == 0) continue;

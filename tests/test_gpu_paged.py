@@ -600,6 +600,38 @@ def test_large_calls(case, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D,group,window", [(64, 1, 0), (128, 3, 0), (128, 4, 90), (64, 2, 200)])
+def test_many_rows_keep_apart_too(kind, D, group, window):
+    """Many rows: values that are not finite, in their tokens' own block and at
+    the windows' edges, change no bit of the rows that do not see them, and
+    reach their own dimensions of the rows that do."""
+    lens, n_new, page, n_sink = 900, 330, 32, 5
+    pool = Pool(kind, 1, page, D, [lens], 29, seed=22)
+    q = torch.randn(1, n_new, group, D, device=DEV).to(torch.bfloat16)
+    kw = dict(window=window, n_sink=n_sink)
+    out, lse = binding.paged_attn(q, pool.cache, pool.table_d, ints([lens]), **kw)
+    bad = [560, 575, 640, 703, 704, 899, 500, 433, 2]
+    for j in bad:
+        at, row = pool.table[0, j // page], j % page
+        if kind == "bf16":
+            pool.cache.v[at, 0, row, 1::5] = float("inf") if j % 2 else float("nan")
+        else:
+            pool.cache.v.view(torch.uint8)[at, 0, row, 1::5] = 0x7f
+    got, got_l = binding.paged_attn(q, pool.cache, pool.table_d, ints([lens]), **kw)
+    assert torch.equal(got_l, lse)
+    for t in range(n_new):
+        p = lens - n_new + t
+        seen = any(j <= p and (window == 0 or j > p - window or j < n_sink) for j in bad)
+        if seen:
+            hit = torch.zeros(D, dtype=torch.bool, device=DEV)
+            hit[1::5] = True
+            assert not bool(got[0, t][:, hit].isfinite().any()), t
+            assert torch.equal(got[0, t][:, ~hit], out[0, t][:, ~hit]), t
+        else:
+            assert torch.equal(got[0, t], out[0, t]), t
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_values_outside_the_block_may_be_anything(kind):
     """Many rows: values that no row of a block of tokens sees (the next
     block's, those behind every window, past the end) change no bit of its
