@@ -644,53 +644,49 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 // 8-bit pages to bf16 tiles [B][n_expanded][H_kv][128][D], keys and values: the
 // tiles that the sequences' new tokens see, in order; slots past the last and those
-// that no token sees as zeros. A CTA makes one tile of one head, 16 values a thread
-// and step. Bound by the bytes.
+// that no token sees as zeros. A CTA makes some rows of one tile and head, 16 values a
+// thread. Bound by the bytes, and by the chain of look-ups before them.
 constexpr int kExpandThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kExpandThreads)
 paged_expand_kernel(const PagedAttnArgs a) {
+  constexpr int kLanes = D / 16, kRows = kExpandThreads / kLanes, kShares = kTile / kRows;
+  const size_t tile = blockIdx.x / kShares;      // ((b, v), hk) in order
+  const int hk = (int)(tile % a.p.H_kv), rest = (int)(tile / a.p.H_kv);
+  const int v = rest % a.n_expanded, b = rest / a.n_expanded;
   let_dependents_start();
   wait_for_prior_grid();
-  const int hk = blockIdx.x % a.p.H_kv;
-  const int rest = blockIdx.x / a.p.H_kv;
-  const int v = rest % a.n_expanded, b = rest / a.n_expanded;
   const PagedSeq sq = paged_seq(a, b);
   if (sq.n <= 0) return;
   const PagedSpan<kTile> sp = sequence_span(a, sq);
   if (v >= sp.n) return;
-  const int lo = sp.tile(v) * kTile;
   const int shift = 31 - __clz(a.p.page);
-  constexpr int kLanes = D / 16;                 // threads a row
-  const size_t tile = (size_t)blockIdx.x;        // ((b, v), hk) in order
+  const int r = blockIdx.x % kShares * kRows + threadIdx.x / kLanes;
+  const int d = threadIdx.x % kLanes * 16;
+  const int slot = sp.tile(v) * kTile + r;
+  long long from = -1;
+  if (slot < sp.hi && sp.meets(a, slot, 1) && (slot >> shift) < a.width) {
+    const int id = __ldg(a.table + (size_t)b * a.width + (slot >> shift));
+    if (id >= 0 && id < a.p.n_pages)
+      from = (((long long)id * a.p.H_kv + hk) << shift) + (slot & (a.p.page - 1));
+  }
 #pragma unroll
-  for (int i = threadIdx.x; i < kTile * kLanes; i += kExpandThreads) {
-    const int r = i / kLanes, d = (i % kLanes) * 16;
-    const int slot = lo + r;
-    long long from = -1;
-    if (slot < sp.hi && sp.meets(a, slot, 1) && (slot >> shift) < a.width) {
-      const int id = __ldg(a.table + (size_t)b * a.width + (slot >> shift));
-      if (id >= 0 && id < a.p.n_pages)
-        from = (((long long)id * a.p.H_kv + hk) << shift) + (slot & (a.p.page - 1));
-    }
+  for (int side = 0; side < 2; ++side) {
+    uint32_t w[8] = {};
+    if (from >= 0) {
+      const uint4 c = *reinterpret_cast<const uint4*>((side ? a.p.v : a.p.k) + from * D + d);
+      const float scale = pow2_byte((side ? a.p.vs : a.p.ks)[from]);
+      const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      uint32_t w[8] = {};
-      if (from >= 0) {
-        const uint4 c = *reinterpret_cast<const uint4*>((side ? a.p.v : a.p.k) + from * D + d);
-        const float scale = pow2_byte((side ? a.p.vs : a.p.ks)[from]);
-        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const float2 f = half2_values(e4m3x2_half2(cw[x / 2] >> (16 * (x % 2))));
-          w[x] = pack_bf16x2(f.x * scale, f.y * scale);
-        }
+      for (int x = 0; x < 8; ++x) {
+        const float2 f = half2_values(e4m3x2_half2(cw[x / 2] >> (16 * (x % 2))));
+        w[x] = pack_bf16x2(f.x * scale, f.y * scale);
       }
-      uint4* dst = reinterpret_cast<uint4*>((side ? a.expanded_v : a.expanded_k) +
-                                            (tile * kTile + r) * D + d);
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
+    uint4* dst = reinterpret_cast<uint4*>((side ? a.expanded_v : a.expanded_k) +
+                                          (tile * kTile + r) * D + d);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -700,7 +696,7 @@ ra_status launch_tiles(const PagedAttnArgs& a, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
   PagePool p = a.p;
   if (kExpanded) {
-    const long long blocks = (long long)a.B * a.n_expanded * a.p.H_kv;
+    const long long blocks = (long long)a.B * a.n_expanded * a.p.H_kv * (kTile * (D / 16) / kExpandThreads);
     if (blocks > 0x7fffffffLL) return RA_ERR_RANGE;
     if (!launch_early(paged_expand_kernel<D>, blocks, kExpandThreads, 0, stream, a))
       return RA_ERR_LAUNCH;
