@@ -20,8 +20,8 @@
 // outputs' rounding alone makes 1.7e-3). Sums and statistics are float32.
 //
 // For up to 16 query rows a sequence and key/value head (new tokens times the heads
-// that share it; more: paged_tiles.cu). A CTA takes one chunk of the slots of one
-// sequence and key/value head. A producer warp looks the pages up, a lane for each, and asks
+// that share it), over 8-bit pages up to 48 in blocks of 16; more: paged_tiles.cu. A CTA
+// takes one chunk of the slots that a block sees. A producer warp looks the pages up, a lane for each, and asks
 // for their boxes (TMA, swizzled, so that ldmatrix meets no bank conflict); four
 // warps share a tile's slots and keep running maxima, sums and outputs of their own,
 // joined in shared memory at the end. Chunks of a long axis are joined by a second
@@ -154,8 +154,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int H_kv = a.p.H_kv, grp = a.H_q / H_kv;
-  const PagedWork work = paged_work(a, blockIdx.x);
-  const int b = work.item / H_kv, hk = work.item % H_kv;
+  // the blocks of a sequence and head run side by side, chunk by chunk: what one of them
+  // reads the others find in L2
+  const int rb = blockIdx.x % a.n_rb, rest = blockIdx.x / a.n_rb;
+  const int split = rest % a.n_split, bh = rest / a.n_split;
+  const int b = bh / H_kv, hk = bh % H_kv, item = bh * a.n_rb + rb;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       sm100::mbar_init(full + 8 * i, 1);
@@ -167,13 +170,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   let_dependents_start();
   wait_for_prior_grid();
   const PagedSeq sq = paged_seq(a, b);
-  const int R = sq.n * grp;                 // query rows of this head
-  if (R == 0) return;                       // a sequence without new tokens
+  const int r0 = rb * RB;                   // the block's first of the head's query rows
+  const int R = min(sq.n * grp - r0, RB);   // and how many
+  if (R <= 0) return;                       // a sequence of fewer new tokens
   const int first = sq.len - sq.n;          // position of the first new token
   PagedSpan<kTile> sp;
-  sp.init(a, first, first + sq.n - 1);
-  const int v_begin = max(work.split, 0) * a.chunk;
-  const int n_tiles = max((work.split < 0 ? sp.n : min(sp.n, v_begin + a.chunk)) - v_begin, 0);
+  sp.init(a, first + r0 / grp, first + (r0 + R - 1) / grp);
+  const int v_begin = split * a.chunk;
+  const int n_tiles = max(min(sp.n, v_begin + a.chunk) - v_begin, 0);
   __syncthreads();
 
   if (warp == kWarps) {
@@ -254,7 +258,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int r = nt * 8 + g;
       const bool row_ok = r < R;
       const long long off =
-          row_ok ? ((long long)(sq.row0 + r / grp) * a.H_q + hk * grp + r % grp) * D : 0;
+          row_ok ? ((long long)(sq.row0 + (r0 + r) / grp) * a.H_q + hk * grp + (r0 + r) % grp) * D : 0;
       const bool ok = row_ok && in_range(off, D, (long long)a.rows * a.H_q * D, a.status);
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + off;
       if constexpr (kQuant) {
@@ -296,7 +300,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     // the position of row 2c + h; below 0: sees nothing
     auto pos = [&](int nt, int h) -> int {
       const int r = nt * 8 + 2 * c + h;
-      return r < R ? first + r / grp : -1;
+      return r < R ? first + (r0 + r) / grp : -1;
     };
 
     // Running state of rows 2c and 2c + 1. What the exponents subtract: the running
@@ -656,10 +660,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       y.w = fmaf(f, x.w, y.w);
       ls = fmaf(f, lw, ls);
     }
-    const int t = r / grp, h = hk * grp + r % grp;
+    const int t = (r0 + r) / grp, h = hk * grp + (r0 + r) % grp;
     const long long row = (long long)(sq.row0 + t) * a.H_q + h;
-    if (work.split >= 0) {
-      const long long part = paged_part(a, work.item, work.split, r);
+    if (a.n_split > 1) {
+      const long long part = paged_part(a, item, split, r);
       if (d == 0) {
         a.part_ml[2 * part] = mx;
         a.part_ml[2 * part + 1] = ls;
@@ -720,7 +724,8 @@ paged_join_few_kernel(const PagedAttnArgs a, int rows) {
   const int grp = a.H_q / a.p.H_kv;
   const PagedSeq sq = paged_seq(a, blk.b);
   wait_for_prior_grid();
-  if (r / grp >= sq.n) return;
+  const int r_head = blk.rb * a.block_rows + r;        // of the head's rows
+  if (r_head >= sq.n * grp) return;
   const int part = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + paged_part(a, item, 0, r);
   const float* o = a.part_o + paged_part(a, item, 0, r) * D + d;
@@ -761,7 +766,7 @@ paged_join_few_kernel(const PagedAttnArgs a, int rows) {
     y.z = fmaf(f, x.z, y.z);
     y.w = fmaf(f, x.w, y.w);
   }
-  store_row<D>(a, blk, sq, r / grp, r % grp, d, y, m, l);
+  store_row<D>(a, blk, sq, r_head / grp, r_head % grp, d, y, m, l);
 }
 
 // Many rows: a CTA joins some rows of one block, kAtOnce outputs of four values a
@@ -863,7 +868,8 @@ ra_status launch_paged_rows(const PagedAttnArgs& a, cudaStream_t stream) {
 ra_status launch_paged_join(const PagedAttnArgs& a, cudaStream_t stream) {
   const long long items = a.n_items - a.n_whole;
   if (a.block_rows <= 16) {
-    const int rows = a.T * (a.H_q / a.p.H_kv);           // those that may hold a token
+    const long long R = (long long)a.T * (a.H_q / a.p.H_kv);
+    const int rows = R < a.block_rows ? (int)R : a.block_rows;    // those that may hold a token
     const long long grid = items * rows;
     if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
     auto kern = a.p.D == 64 ? paged_join_few_kernel<64> : paged_join_few_kernel<128>;

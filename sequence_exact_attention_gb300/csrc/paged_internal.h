@@ -58,12 +58,12 @@ struct PagedAttnArgs {
   int window, n_sink;      // window 0: every slot up to the query's own
   float scale_log2;        // softmax scale * log2(e)
   // plan (paged_attn_plan): a sequence's new tokens give n * H_q / H_kv query rows
-  // a key/value head. Few (block_rows 8 or 16: paged_attn.cu) are one block; many
-  // (256: paged_tiles.cu) are cut into blocks. Of the n_items blocks the first
+  // a key/value head, cut into blocks, few rows (block_rows 8 or 16: paged_attn.cu) or
+  // many (256: paged_tiles.cu). Of the n_items blocks the first
   // n_whole go to one CTA each, the visible tiles of the others are cut into n_split
   // chunks of `chunk` tiles.
   int block_rows, n_items, n_whole, n_split, chunk;
-  int n_rb;                // many rows: blocks of the longest sequence and head
+  int n_rb;                // blocks of the longest sequence and head
   int rb_major;            // many rows: the blocks' order, see there
   int n_expanded;          // many rows over 8-bit pages: tiles a sequence's rows see at most
   float* part_o;           // [n_items - n_whole][n_split][block_rows][D]

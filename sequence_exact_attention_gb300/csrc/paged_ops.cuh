@@ -92,7 +92,7 @@ struct PagedSpan {
 };
 
 // The block of query rows that item `item` is; every lane of a warp calls it. Few
-// rows: a sequence and head is one block. Many: blocks of late tokens (the longest
+// rows: by sequence and head. Many: blocks of late tokens (the longest
 // walks) come first, across all heads of a sequence (and the sequences, where all
 // have T new tokens) when keys and values fit in L2 anyway, else within each head.
 // Packed sequences are looked up among their numbers of blocks: the launch knows
@@ -102,7 +102,7 @@ struct PagedBlock {
 };
 __device__ __forceinline__ PagedBlock paged_block(const PagedAttnArgs& a, int item) {
   const int H_kv = a.p.H_kv;
-  if (a.block_rows <= 16) return {item / H_kv, item % H_kv, 0};
+  if (a.block_rows <= 16) return {item / a.n_rb / H_kv, item / a.n_rb % H_kv, item % a.n_rb};
   if (!a.cu) {
     if (a.rb_major) {
       const int bh = item % (a.B * H_kv);

@@ -138,6 +138,8 @@ CASES = [
     ("prompt_tiles", [640, 257], [640, 257], 4, 4, 64, 128, 5, 0, 0),
     ("prompt_few_rows_long", [6000], [40], 4, 1, 128, 128, 47, 0, 0),
     ("prompt_window_d128", [900, 520], [400, 520], 4, 2, 128, 64, 15, 200, 10),
+    ("several_blocks_of_few_rows", [515, 40, 129], [5, 5, 5], 18, 2, 128, 16, 33, 0, 0),
+    ("several_blocks_window", [515, 40, 300], [3, 1, 12], 8, 2, 64, 64, 9, 70, 3),
     ("group_of_128", [70, 3], [1, 1], 128, 1, 64, 16, 5, 0, 0),
     ("group_of_100", [70, 40], [3, 2], 100, 1, 128, 32, 3, 0, 0),
     ("a_wide_table", [300, 129, 40], [200, 1, 40], 4, 2, 64, 16, 20000, 0, 0),
@@ -321,7 +323,7 @@ def test_slots_without_a_page():
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-@pytest.mark.parametrize("group", [1, 4])
+@pytest.mark.parametrize("group", [1, 4, 10])
 def test_a_row_is_not_touched_by_what_it_does_not_see(kind, group):
     """A later drafted token's keys and values that are not finite change no
     bit of the rows before it; slots that a window hides none of any."""
