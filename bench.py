@@ -52,7 +52,7 @@ MERGE_METRIC = "LSE merge GB/s (algorithmic bytes)"
 # stored with it (see _kernel_digest). window_iter.cuh, which attn_tc.cu
 # includes too, is not among them: only the windowed instantiations use it.
 TRAFFIC = {
-    "attn_tc": {"sha256_16": "d5b0d24472603a27", "bytes_per_launch": {
+    "attn_tc": {"sha256_16": "b749e08ed261dd8c", "bytes_per_launch": {
         "bf16_s32k_causal_zigzag": 844381696 + 255606272,
         "bf16_s16k_d64": 403381248 + 119772160,
         "bf16_s128k_gqa_causal": 2729674752 + 1058758656,
@@ -69,7 +69,7 @@ TRAFFIC = {
 }
 KERNEL_SOURCES = {
     "attn_tc": ("attn_tc.cu", "checks.cuh", "fastmath.cuh", "ring_iter.cuh", "sm100.cuh",
-                "ra_internal.h", "tensor_map.cpp"),
+                "tc_tiles.cuh", "ra_internal.h", "tensor_map.cpp"),
     "merge": ("merge.cu", "ra_internal.h"),
 }
 

@@ -681,9 +681,12 @@ ra_status paged_attn_workspace(const ra_pages* pages, int B, int S_q, int total,
  * cu_seqlens[b + 1]) of q, out [total, H_q, D], lse [H_q, total]; max_seqlen bounds
  * their numbers. Malformed offsets are brought into range; rows that no sequence
  * has are left as they were.
- * Slots past lens[b] and those that no row of the call sees may hold anything,
- * NaN included. A slot whose page is not there is not seen, and sets RA_ERR_RANGE
- * in `dev_status` where a row would have seen it.
+ * A row's results depend on the slots that it sees alone, to the bit, whatever the
+ * others hold (slots past lens[b], behind the windows, later tokens' slots): NaN and
+ * infinities included. A value that is not finite makes its own dimension of the rows
+ * that see it NaN or infinite. A slot whose page is not there is not seen, and sets
+ * RA_ERR_RANGE in `dev_status` where a row would have seen it; pages that every window
+ * has left behind may be taken out of the table.
  * dtype RA_BF16. scale <= 0 means 1 / sqrt(D). The workspace is the caller's,
  * 16-byte aligned; its contents do not matter. Calls that may overlap on the GPU
  * need workspaces of their own. Results repeat bit for bit.

@@ -7,7 +7,7 @@
 // divide 128 leaves the last rows unused.) One CTA owns two query tiles and walks
 // the tiles of 128 slots that some row of them sees; each tile of keys and values
 // serves both. Of the blocks that do not fill a wave of CTAs the walks are cut into
-// chunks, joined by paged_join_kernel (paged_plan.cpp).
+// chunks, joined by paged_join_many_kernel (paged_plan.cpp).
 //
 // bf16 pages are read where they lie: the producer warp looks a tile's pages up, a
 // lane for each, and asks for their boxes; a page that is not there, or that holds
@@ -20,10 +20,18 @@
 // for Q0 and then Q1 at every tile; a producer warp; an issuer warp whose elected
 // lane issues every MMA; two warps that keep values that are not finite from rows that
 // do not see them (in the softmax warps' hands this took 4 to 8 us of 90 under a
-// window). Tensor memory: S_i (128 f32 columns) at 128 i, over whose
-// first 64 the weights are written as bf16; O_i (D columns) at 256 + D i. Per tile
-// j the tensor core runs PV0(j) S0(j+1) PV1(j) S1(j+1), one tile's products under
-// the other's softmax. Barriers:
+// window). Tensor memory: S_i (128 f32 columns) at 128 i, over whose first 64 the
+// weights are written as bf16; O_i (D columns) at 256 + D i. Per tile j the tensor core
+// runs PV0(j) S0(j+1) PV1(j) S1(j+1), one tile's products under the other's softmax.
+//
+// What bounds it: the softmax, as in the forward kernel (attn_tc.cu), some 1.55 us a
+// tile of two times 128 x 128 scores at D = 128 where the products take 1.1; and 7 us a
+// CTA outside its tiles (look-ups 1.2, the first tile's way 2 to 3, the end 3). Measured,
+// replayed from a graph: 4096 tokens behind 12288 slots, 32 heads on 8, D = 128: 646 us,
+// 1490 TFLOP/s; 64 tokens behind 100000 slots: 94 us.
+//
+// Roundings: weights to bf16 (2^-8 of a weight at most); sums and statistics float32.
+// Barriers:
 //   qfull[i]         Q_i landed
 //   kfull/vfull[s]   keys / values of a tile landed in slot s
 //   done[j mod kKBuf] every MMA up to S1(j) is done: K_j's and V_{j-1}'s slots are free
@@ -379,7 +387,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (!ok) break;
       tc_fence_after();
       if (leader) {
-        tc::issue_pv<D>(tO0, tS0, vd, j > 0);
+        tc::issue_pv<D, false>(tO0, tS0, vd, j > 0);
         if (last) {
           umma_commit(bar(C::bODone));
         } else {
@@ -393,7 +401,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          tc::issue_pv<D>(tO1, tS1, vd, j > 0);
+          tc::issue_pv<D, false>(tO1, tS1, vd, j > 0);
           if (last) {
             umma_commit(bar(C::bODone + 1));
           } else {

@@ -91,17 +91,18 @@ __device__ __forceinline__ void issue_s(uint32_t d_tmem, uint64_t q_desc, uint64
   }
 }
 
-// O_i (+)= P_i V: A = P_i (bf16, TMEM, in the first 64 columns of S_i), B = V
-// (MN-major), M = 128, N = D, K = 128 keys in steps of 16 (8 TMEM columns of bf16
-// pairs each).
-template <int D>
+// O_i (+)= P_i V: A = P_i (bf16, TMEM), B = V (MN-major), M = 128, N = D,
+// K = 128 keys in steps of 16 (8 TMEM columns of bf16 pairs each). P_i lies
+// in the first 64 columns of S_i, or (kOwnCols) in the first 32 of each
+// part's 64.
+template <int D, bool kOwnCols>
 __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint64_t v_desc,
                                          bool accumulate) {
   constexpr uint32_t idesc = sm100::idesc_bf16_f32(128, D, true);
 #pragma unroll
   for (int kk = 0; kk < kTile / 16; ++kk)
-    sm100::umma_ts(o_tmem, p_tmem + kk * 8, v_desc + (uint64_t)((kk * 2048) >> 4), idesc,
-                   (accumulate || kk > 0) ? 1u : 0u);
+    sm100::umma_ts(o_tmem, p_tmem + (kOwnCols ? (kk / 4) * 64 + (kk % 4) * 8 : kk * 8),
+                   v_desc + (uint64_t)((kk * 2048) >> 4), idesc, (accumulate || kk > 0) ? 1u : 0u);
 }
 
 }  // namespace tc
