@@ -15,6 +15,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 
 import numpy as np
 
@@ -144,19 +145,20 @@ def load():
     lib.kv4_attn.argtypes = [vp] * 9 + [c_int] * 9 + [c_float, c_int, vp, ctypes.c_size_t, vp, vp]
     lib.kv4_evict.restype = c_int
     lib.kv4_evict.argtypes = [vp] * 13 + [c_int] * 8 + [vp, vp]
+    pages = ctypes.c_char_p          # a struct, as bytes
     lib.paged_append.restype = c_int
-    lib.paged_append.argtypes = [vp, vp, c_int] + [vp] * 4 + [c_int] * 3 + [vp, vp]
+    lib.paged_append.argtypes = [pages, vp, c_int] + [vp] * 4 + [c_int] * 3 + [vp, vp]
     lib.paged_append_varlen.restype = c_int
-    lib.paged_append_varlen.argtypes = [vp, vp, c_int] + [vp] * 4 + [c_int] * 3 + [vp, vp]
+    lib.paged_append_varlen.argtypes = [pages, vp, c_int] + [vp] * 4 + [c_int] * 3 + [vp, vp]
     lib.paged_read.restype = c_int
-    lib.paged_read.argtypes = [vp, vp, c_int] + [vp] * 3 + [c_int] * 3 + [vp, vp]
+    lib.paged_read.argtypes = [pages, vp, c_int] + [vp] * 3 + [c_int] * 3 + [vp, vp]
     lib.paged_attn_workspace.restype = c_int
-    lib.paged_attn_workspace.argtypes = [vp] + [c_int] * 8 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.paged_attn_workspace.argtypes = [pages] + [c_int] * 8 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.paged_attn.restype = c_int
-    lib.paged_attn.argtypes = ([vp, vp, vp, c_int] + [vp] * 3 + [c_int] * 6 +
+    lib.paged_attn.argtypes = ([vp, pages, vp, c_int] + [vp] * 3 + [c_int] * 6 +
                                [c_float, c_int, vp, ctypes.c_size_t, vp, vp])
     lib.paged_attn_varlen.restype = c_int
-    lib.paged_attn_varlen.argtypes = ([vp, vp, vp, c_int] + [vp] * 4 + [c_int] * 7 +
+    lib.paged_attn_varlen.argtypes = ([vp, pages, vp, c_int] + [vp] * 4 + [c_int] * 7 +
                                       [c_float, c_int, vp, ctypes.c_size_t, vp, vp])
     lib.ring_attn_plan.restype = c_int
     lib.ring_attn_plan.argtypes = [c_int, c_int, c_int, c_int, ip, ctypes.c_size_t]
@@ -1028,11 +1030,14 @@ def kv4_evict(cache, score, lens, budget, n_sink=0, n_recent=0, dst=None, dst_sc
 
 # ------------------------------------------------------------------ paged key/value cache
 
-class _Pages(ctypes.Structure):
-    """ra_pages of ``include/ring_attn.h``."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("H_kv", ctypes.c_int),
-                ("page", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int)]
+# ra_pages of include/ring_attn.h, as bytes
+_PAGES = struct.Struct("4P5i")
+
+
+def _pages(ptrs, dims, quant):
+    if quant:
+        return _PAGES.pack(*ptrs, *dims, RA_E4M3)
+    return _PAGES.pack(*ptrs, 0, 0, *dims, RA_BF16)
 
 
 class PagedCache(tuple):
@@ -1041,37 +1046,44 @@ class PagedCache(tuple):
     k_scale and v_scale uint8 [n_pages, H_kv, page].
 
     A tuple of its tensors, whose shapes, dtypes and layout are checked here,
-    once, and not again by the calls that take the cache.
+    once, and not again by the calls that take the cache: memory behind them may
+    be given back and taken again in between, their shapes stay.
     """
 
     def __new__(cls, k, v, k_scale=None, v_scale=None):
         torch = _T or _import_torch()
-        quant = k.dtype == torch.float8_e4m3fn
-        if not quant and k.dtype != torch.bfloat16:
-            raise ValueError(f"pages must be bfloat16 or float8_e4m3fn, got {k.dtype}")
-        if k.dim() != 4:
+        shape, dtype, dev = k.shape, k.dtype, k.get_device()
+        quant = dtype is torch.float8_e4m3fn
+        if not quant and dtype is not torch.bfloat16:
+            raise ValueError(f"pages must be bfloat16 or float8_e4m3fn, got {dtype}")
+        if len(shape) != 4:
             raise ValueError("k must be [n_pages, H_kv, page, D]")
         if quant != (k_scale is not None) or quant != (v_scale is not None):
             raise ValueError("k_scale and v_scale belong to pages of 8 bits")
-        shape = tuple(k.shape)
-        _like(v, "v", shape, k.dtype)
-        _like(k_scale, "k_scale", shape[:3], torch.uint8)
-        _like(v_scale, "v_scale", shape[:3], torch.uint8)
-        parts = (k, v, k_scale, v_scale) if quant else (k, v)
-        self = super().__new__(cls, parts)
-        self.dims = shape
-        self.dtype = k.dtype
-        self.device = dev = k.get_device()
-        for t, n in zip(parts, ("k", "v", "k_scale", "v_scale")):
+        _like(v, "v", shape, dtype)
+        parts = (k, v)
+        if quant:
+            _like(k_scale, "k_scale", shape[:3], torch.uint8)
+            _like(v_scale, "v_scale", shape[:3], torch.uint8)
+            parts = (k, v, k_scale, v_scale)
+        for i, t in enumerate(parts):
             if not t.is_contiguous():
-                raise ValueError(f"{n} must be contiguous")
+                raise ValueError(f"{('k', 'v', 'k_scale', 'v_scale')[i]} must be contiguous")
             if t.get_device() != dev:
                 raise ValueError("the cache's tensors are on several devices")
-        if max(shape[:3]) > 0x7fffffff:
+        if max(shape) > 0x7fffffff:
             _check(RA_ERR_RANGE, "PagedCache")
-        self._c = _Pages(*map(_ptr, (k, v, k_scale, v_scale)), *shape, RA_E4M3 if quant else RA_BF16)
-        self._ref = ctypes.addressof(self._c)
+        self = super().__new__(cls, parts)
+        self.dims = tuple(shape)
+        self.dtype = dtype
+        self.device = dev
         return self
+
+    def __reduce__(self):
+        return PagedCache, tuple(self)
+
+    def _c(self):
+        return _pages([t.data_ptr() for t in self], self.dims, len(self) > 2)
 
     k = property(lambda self: self[0])
     v = property(lambda self: self[1])
@@ -1130,7 +1142,7 @@ def paged_append(cache, table, k, v, start, n_new=None, dev_status=None, stream=
         raise ValueError(f"table must be int32 [{B}, width]")
     width = _paged_args(cache, table, _APPEND, (table, k, v, start, n_new, dev_status),
                         ((start, "start", B), (n_new, "n_new", B)), dev_status)
-    st = lib.paged_append(cache._ref, table.data_ptr(), width, k.data_ptr(), v.data_ptr(),
+    st = lib.paged_append(cache._c(), table.data_ptr(), width, k.data_ptr(), v.data_ptr(),
                           start.data_ptr(), _ptr(n_new), B, T, code, _ptr(dev_status),
                           _stream(stream))
     if st:
@@ -1154,7 +1166,7 @@ def paged_append_varlen(cache, table, k, v, cu_seqlens, start, dev_status=None, 
     code = _dtype_code(dtype)
     width = _paged_args(cache, table, _APPEND_VARLEN, (table, k, v, cu_seqlens, start, dev_status),
                         ((start, "start", B), (cu_seqlens, "cu_seqlens", B + 1)), dev_status)
-    st = lib.paged_append_varlen(cache._ref, table.data_ptr(), width, k.data_ptr(), v.data_ptr(),
+    st = lib.paged_append_varlen(cache._c(), table.data_ptr(), width, k.data_ptr(), v.data_ptr(),
                                  start.data_ptr(), cu_seqlens.data_ptr(), B, shape[0], code,
                                  _ptr(dev_status), _stream(stream))
     if st:
@@ -1194,7 +1206,7 @@ def paged_read(cache, table, start, T, dtype=None, k=None, v=None, dev_status=No
             with torch.cuda.stream(stream):
                 k = torch.empty(shape, dtype=dtype, device=table.device) if k is None else k
                 v = torch.empty_like(k) if v is None else v
-    st = lib.paged_read(cache._ref, table.data_ptr(), width, _ptr(start), k.data_ptr(),
+    st = lib.paged_read(cache._c(), table.data_ptr(), width, _ptr(start), k.data_ptr(),
                         v.data_ptr(), B, _int32(T), code, _ptr(dev_status), _stream(stream))
     if st:
         _check(st, "paged_read")
@@ -1205,9 +1217,9 @@ def paged_read(cache, table, start, T, dtype=None, k=None, v=None, dev_status=No
 @functools.lru_cache(maxsize=256)
 def _paged_workspace(dims, quant, B, S_q, total, H_q, max_len, window, n_sink, varlen):
     n = ctypes.c_size_t()
-    pages = _Pages(None, None, None, None, *dims, RA_E4M3 if quant else RA_BF16)
-    _check(load().paged_attn_workspace(ctypes.addressof(pages), B, S_q, total, H_q, max_len, window,
-                                       n_sink, varlen, ctypes.byref(n)), "paged_attn_workspace")
+    pages = _pages((0,) * (4 if quant else 2), dims, quant)
+    _check(load().paged_attn_workspace(pages, B, S_q, total, H_q, max_len, window, n_sink, varlen,
+                                       ctypes.byref(n)), "paged_attn_workspace")
     return n.value
 
 
@@ -1261,12 +1273,12 @@ def _paged_attn(q, cache, table, lens, cu_seqlens, B, S_q, total, max_len, windo
     sc = 0.0 if scale is None else float(scale)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     if packed:
-        st = lib.paged_attn_varlen(q.data_ptr(), cache._ref, table.data_ptr(), width,
+        st = lib.paged_attn_varlen(q.data_ptr(), cache._c(), table.data_ptr(), width,
                                    lens.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(),
                                    lse.data_ptr(), B, total, S_q, H_q, max_len, window, n_sink, sc,
                                    code, ws, ws_bytes, _ptr(dev_status), _stream(stream))
     else:
-        st = lib.paged_attn(q.data_ptr(), cache._ref, table.data_ptr(), width, lens.data_ptr(),
+        st = lib.paged_attn(q.data_ptr(), cache._c(), table.data_ptr(), width, lens.data_ptr(),
                             out.data_ptr(), lse.data_ptr(), B, S_q, H_q, max_len, window, n_sink,
                             sc, code, ws, ws_bytes, _ptr(dev_status), _stream(stream))
     if st:

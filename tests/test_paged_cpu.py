@@ -1,5 +1,6 @@
 """Refusals of the paged cache's entry points, before anything reaches a GPU."""
 
+import copy
 import ctypes
 
 import pytest
@@ -17,12 +18,13 @@ def addr(i, off=0):     # apart by more than any tensor below
 
 
 def pages(k=1, v=2, ks=0, vs=0, n=64, H=2, page=16, D=64, dtype=0, off=0):
-    return binding._Pages(addr(k, off).value, addr(v).value, addr(ks).value, addr(vs).value, n, H, page, D, dtype)
+    p = [a.value or 0 for a in (addr(k, off), addr(v), addr(ks), addr(vs))]
+    return binding._PAGES.pack(*p, n, H, page, D, dtype)
 
 
 def append(lib, table=5, width=8, k=6, v=7, start=8, n_new=0, B=2, T=3, dtype=0, off=0, p=None, **kw):
     pg = pages(**kw) if p is None else p
-    return lib.paged_append(ctypes.addressof(pg), addr(table), width, addr(k, off), addr(v), addr(start),
+    return lib.paged_append(pg, addr(table), width, addr(k, off), addr(v), addr(start),
                             addr(n_new), B, T, dtype, None, None)
 
 
@@ -44,7 +46,7 @@ def test_append_refusals(lib):
 
 def append_packed(lib, cu=8, n_seq=2, total=5, dtype=0):
     pg = pages()
-    return lib.paged_append_varlen(ctypes.addressof(pg), addr(5), 8, addr(6), addr(7), addr(9), addr(cu), n_seq, total,
+    return lib.paged_append_varlen(pg, addr(5), 8, addr(6), addr(7), addr(9), addr(cu), n_seq, total,
                                    dtype, None, None)
 
 
@@ -57,7 +59,7 @@ def test_packed_append_refusals(lib):
 
 def read(lib, k=6, v=7, T=3, dtype=0, **kw):
     pg = pages(**kw)
-    return lib.paged_read(ctypes.addressof(pg), addr(5), 8, None, addr(k), addr(v), 2, T, dtype, None, None)
+    return lib.paged_read(pg, addr(5), 8, None, addr(k), addr(v), 2, T, dtype, None, None)
 
 
 def test_read_refusals(lib):
@@ -69,7 +71,7 @@ def test_read_refusals(lib):
 
 def need(lib, B=2, S_q=1, total=0, H_q=4, max_len=128, window=0, n_sink=0, varlen=0, **kw):
     n, pg = ctypes.c_size_t(), pages(**kw)
-    st = lib.paged_attn_workspace(ctypes.addressof(pg), B, S_q, total, H_q, max_len, window, n_sink, varlen,
+    st = lib.paged_attn_workspace(pg, B, S_q, total, H_q, max_len, window, n_sink, varlen,
                                   ctypes.byref(n))
     return st, n.value
 
@@ -77,13 +79,13 @@ def need(lib, B=2, S_q=1, total=0, H_q=4, max_len=128, window=0, n_sink=0, varle
 def attn(lib, q=6, table=5, width=8, lens=7, out=8, lse=9, B=2, S_q=1, H_q=4, max_len=128, window=0, n_sink=0, dtype=0,
          ws=10, ws_bytes=1 << 34, off=0, **kw):
     pg = pages(**kw)
-    return lib.paged_attn(addr(q, off), ctypes.addressof(pg), addr(table), width, addr(lens), addr(out), addr(lse), B,
+    return lib.paged_attn(addr(q, off), pg, addr(table), width, addr(lens), addr(out), addr(lse), B,
                           S_q, H_q, max_len, window, n_sink, 0.0, dtype, addr(ws), ws_bytes, None, None)
 
 
 def attn_packed(lib, cu=11, n_seq=2, total=7, max_seqlen=4, **kw):
     pg = pages(**kw)
-    return lib.paged_attn_varlen(addr(6), ctypes.addressof(pg), addr(5), 8, addr(7), addr(cu), addr(8), addr(9), n_seq,
+    return lib.paged_attn_varlen(addr(6), pg, addr(5), 8, addr(7), addr(cu), addr(8), addr(9), n_seq,
                                  total, max_seqlen, 4, 128, 0, 0, 0.0, 0, addr(10), 1 << 34, None, None)
 
 
@@ -112,7 +114,7 @@ def test_attention_refusals(lib):
 
 def test_workspace_refusals(lib):
     pg = pages()
-    assert lib.paged_attn_workspace(ctypes.addressof(pg), 2, 1, 0, 4, 128, 0, 0, 0, None) == NULL
+    assert lib.paged_attn_workspace(pg, 2, 1, 0, 4, 128, 0, 0, 0, None) == NULL
     assert need(lib, page=24)[0] == SHAPE and need(lib, max_len=0)[0] == RANGE
     assert need(lib, varlen=1, total=0)[0] == SHAPE
     assert need(lib, B=1, S_q=1 << 24, H_q=128, H=1)[0] == RANGE
@@ -161,3 +163,21 @@ def test_an_oversized_window_or_sink_stays_out_of_range_or_means_all():
     for bad in (dict(window=-(1 << 40)), dict(n_sink=-1)):
         with pytest.raises(binding.RingAttnError, match="out of range"):
             binding.paged_attn_workspace_bytes(cache, 1, 1, 4, 40, **bad)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+def test_a_cache_follows_its_memory_and_can_be_copied(dtype):
+    """Memory given back and taken again lies elsewhere; copies have their own."""
+    cache = binding.paged_cache(4, 2, 16, 64, dtype=dtype, device="cpu")
+
+    def pointers(c):
+        return binding._PAGES.unpack(c._c())[:4]
+
+    want = [t.data_ptr() for t in cache] + [0] * (4 - len(cache))
+    assert list(pointers(cache)) == want
+    cache.v.set_(torch.zeros_like(cache.v))
+    assert pointers(cache)[0] == want[0] and pointers(cache)[1] == cache.v.data_ptr() != want[1]
+    assert binding._PAGES.unpack(cache._c())[4:] == (4, 2, 16, 64, {torch.bfloat16: 0}.get(dtype, 2))
+    other = copy.deepcopy(cache)
+    assert type(other) is binding.PagedCache and other.dims == cache.dims and other.dtype == dtype
+    assert not set(pointers(other)) & set(pointers(cache)) - {0}
