@@ -205,7 +205,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (j >= sp.hi || !sp.meets(a, j, box_rows)) return x;
       x.wanted = true;
       x.row = j & (a.p.page - 1);
-      if ((j >> shift) < a.width) x.id = __ldg(a.table + (size_t)b * a.width + (j >> shift));
+      if ((j >> shift) < a.width) x.id = a.table[(size_t)b * a.width + (j >> shift)];
       return x;
     };
     Box next = look_up(0);
@@ -690,7 +690,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
 }
 
 // ---- Joining chunks. A chunk without a visible slot has the sum 0, and outputs that
-// nobody wrote: they may be read, never used.
+// nobody wrote: they may be read, never used. Every CTA waits for the grid before it,
+// as the next one takes this one's end for the end of both, and before it reads
+// offsets, which may come from a grid that that one has waited for.
 
 __device__ __forceinline__ float chunk_weight(float2 ml, float m) {     // below 0: nothing there
   if (ml.x == -INFINITY && ml.y == 0.f) return -1.f;
@@ -724,11 +726,12 @@ paged_join_few_kernel(const PagedAttnArgs a, int rows) {
   __shared__ float4 sO[kParts][kLanes];
   __shared__ float sM[kParts], sL[kParts];
   let_dependents_start();
+  if (a.cu) wait_for_prior_grid();
   const int item = (int)(blockIdx.x / (uint32_t)rows), r = (int)(blockIdx.x % (uint32_t)rows);
   const PagedBlock blk = paged_block(a, item);
   const int grp = a.H_q / a.p.H_kv;
   const PagedSeq sq = paged_seq(a, blk.b);
-  wait_for_prior_grid();
+  if (!a.cu) wait_for_prior_grid();
   const int r_head = blk.rb * a.block_rows + r;        // of the head's rows
   if (r_head >= sq.n * grp) return;
   const int part = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
@@ -784,13 +787,14 @@ paged_join_many_kernel(const PagedAttnArgs a) {
   constexpr int rows = kAtOnce * kJoinThreads / (D / 4);
   extern __shared__ float2 sW[];             // [n_split][rows] (weight, sum), [rows] (maximum, sum)
   let_dependents_start();
+  if (a.cu) wait_for_prior_grid();
   const int per = a.block_rows / rows;
   const int item = a.n_whole + blockIdx.x / per, r0 = blockIdx.x % per * rows;
   const PagedBlock blk = paged_block(a, item);
   if (blk.b < 0) return;                     // past the last block of the batch
   const int grp = a.H_q / a.p.H_kv, tt = 128 / grp;
   const PagedSeq sq = paged_seq(a, blk.b);
-  wait_for_prior_grid();
+  if (!a.cu) wait_for_prior_grid();
   // row r's token; below 0: it has none
   auto token = [&](int r) -> int {
     const int t = (2 * blk.rb + (r >> 7)) * tt + (r & 127) / grp;

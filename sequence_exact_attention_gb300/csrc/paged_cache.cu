@@ -102,22 +102,22 @@ __device__ __forceinline__ Place locate(const PagedRowArgs& a, const Divisors& b
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(a.cu + mid) <= (int)token) lo = mid;
+      if (a.cu[mid] <= (int)token) lo = mid;
       else hi = mid;
     }
     b = lo;
-    t = (int)token - __ldg(a.cu + b);
-    x.counts = t >= 0 && (int)token < __ldg(a.cu + b + 1);
+    t = (int)token - a.cu[b];
+    x.counts = t >= 0 && (int)token < a.cu[b + 1];
   } else {
     b = (int)by.tokens.of(token);
     t = (int)(token - (uint32_t)b * by.tokens.d);
-    x.counts = !a.n_new || t < __ldg(a.n_new + b);
+    x.counts = !a.n_new || t < a.n_new[b];
   }
   if (!x.counts) return x;
-  const long long slot = (long long)(a.start ? __ldg(a.start + b) : 0) + t;
+  const long long slot = (long long)(a.start ? a.start[b] : 0) + t;
   const int shift = 31 - __clz(a.p.page);
   if (slot < 0 || (slot >> shift) >= a.width) return x;
-  const int id = __ldg(a.table + (size_t)b * a.width + (slot >> shift));
+  const int id = a.table[(size_t)b * a.width + (slot >> shift)];
   if (id < 0 || id >= a.p.n_pages) return x;
   x.row = ((((long long)id * a.p.H_kv + h) << shift)) + (slot & (a.p.page - 1));
   x.held = in_range(x.row, 1, (long long)a.p.n_pages * a.p.H_kv * a.p.page, a.status);

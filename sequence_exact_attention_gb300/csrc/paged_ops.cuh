@@ -45,13 +45,13 @@ struct PagedSeq {
 __device__ __forceinline__ PagedSeq paged_seq(const PagedAttnArgs& a, int b) {
   PagedSeq s;
   if (a.cu) {
-    s.row0 = min(max(__ldg(a.cu + b), 0), a.rows);
-    s.n = min(min(max(__ldg(a.cu + b + 1) - s.row0, 0), a.T), a.rows - s.row0);
+    s.row0 = min(max(a.cu[b], 0), a.rows);
+    s.n = min(min(max(a.cu[b + 1] - s.row0, 0), a.T), a.rows - s.row0);
   } else {
     s.row0 = b * a.T;
     s.n = a.T;
   }
-  s.len = min(max(__ldg(a.lens + b), 0), a.max_len);
+  s.len = min(max(a.lens[b], 0), a.max_len);
   return s;
 }
 

@@ -293,7 +293,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (slot >= sp.hi || !sp.meets(a, slot, a.p.page)) return -1;
       const int p = slot >> shift;
       if (p >= a.width) return -2;
-      const int id = __ldg(a.table + (size_t)b * a.width + p);
+      const int id = a.table[(size_t)b * a.width + p];
       return id >= 0 && id < a.p.n_pages ? id : -2;
     };
     auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t full, int id, int j) {
@@ -694,7 +694,7 @@ paged_expand_kernel(const PagedAttnArgs a) {
   const int slot = sp.tile(v) * kTile + r;
   long long from = -1;
   if (slot < sp.hi && sp.meets(a, slot, 1) && (slot >> shift) < a.width) {
-    const int id = __ldg(a.table + (size_t)b * a.width + (slot >> shift));
+    const int id = a.table[(size_t)b * a.width + (slot >> shift)];
     if (id >= 0 && id < a.p.n_pages)
       from = (((long long)id * a.p.H_kv + hk) << shift) + (slot & (a.p.page - 1));
   }

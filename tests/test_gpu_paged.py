@@ -654,3 +654,48 @@ def test_values_outside_the_block_may_be_anything(kind):
     got, got_l = binding.paged_attn(q, pool.cache, pool.table_d, ints([lens]), **kw)
     assert torch.equal(got[:, :128], out[:, :128]) and torch.equal(got_l, lse)
     assert bool(got[:, 128:].isnan().all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_packed_calls_follow_each_other_without_waits(kind):
+    """A packed call that may be long but is short (its offsets have fewer blocks than
+    the launch makes whole ones, so that nothing is left to join), then the same slots
+    written anew at once, offsets and lengths changing in place in between: each call
+    sees what was there at its turn, as calls with waits between them do."""
+    H, page, D, width, total = 16, 64, 64, 512, 4096
+    g = torch.Generator(device=DEV).manual_seed(44)
+    dtype = torch.bfloat16 if kind == "bf16" else E4M3
+    q = torch.randn(total, H, D, generator=g, device=DEV).to(torch.bfloat16)
+    news = [torch.randn(512, H, D, generator=g, device=DEV).to(torch.bfloat16) for _ in range(4)]
+    steps = [([0, 300], 512), ([0, 30], 32768), ([0, 300], 32768), ([0, 4096], 9000), ([5, 6], 40), ([0, 300], 32768)]
+    steps = [(ints(cu), ints([n])) for cu, n in steps]
+    table = torch.randperm(width, generator=g, device=DEV).to(torch.int32)[None]
+    full = torch.randn(1, width * page, H, D, generator=g, device=DEV).to(torch.bfloat16)
+
+    def run(wait):
+        cache = binding.paged_cache(width, H, page, D, dtype=dtype)
+        binding.paged_append(cache, table, full, full, ints([0]))
+        cu, lens, zero, rows = ints([0, 0]), ints([0]), ints([0]), ints([0, 512])
+        res = []
+        torch.cuda.synchronize()
+        for i, (c, n) in enumerate(steps):
+            cu.copy_(c)
+            lens.copy_(n)
+            binding.paged_append_varlen(cache, table, news[i % 4], news[(i + 1) % 4], rows, zero)
+            if wait:
+                torch.cuda.synchronize()
+            out = torch.zeros_like(q)
+            lse = torch.zeros(H, total, device=DEV)
+            if wait:
+                torch.cuda.synchronize()
+            binding.paged_attn_varlen(q, cache, table, lens, cu, total, out=out, lse=lse)
+            if wait:
+                torch.cuda.synchronize()
+            res += [out, lse]
+        torch.cuda.synchronize()
+        return res
+
+    want = run(True)
+    for _ in range(3):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
