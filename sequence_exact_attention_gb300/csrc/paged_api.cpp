@@ -117,6 +117,11 @@ ra_status attn_sizes(const ra_pages& p, bool varlen, int B, int T, long long row
   return RA_OK;
 }
 
+ra_status launch(const PagedAttnArgs& a, cudaStream_t s) {
+  const ra_status st = a.block_rows <= 16 ? launch_paged_rows(a, s) : launch_paged_tiles(a, s);
+  return st != RA_OK || a.n_split == 1 ? st : launch_paged_join(a, s);
+}
+
 ra_status attn(const void* q, const ra_pages* pages, const int* table, int width, const int* lens,
                const int* cu, bool varlen, void* out, float* lse, int B, int T, long long rows,
                int H_q, int max_len, int window, int n_sink, float scale, int dtype,
@@ -125,16 +130,24 @@ ra_status attn(const void* q, const ra_pages* pages, const int* table, int width
   if (dtype != RA_BF16) return RA_ERR_DTYPE;
   ra_status st = check_pages(pages, table, width);
   if (st != RA_OK) return st;
-  PagedAttnArgs a = {};
+  PagedAttnArgs a = {}, few = {};
   st = attn_sizes(*pages, varlen, B, T, rows, H_q, max_len, window, n_sink, &a);
   if (st != RA_OK) return st;
   if (max_len > (long long)width * pages->page) return RA_ERR_RANGE;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16)) return RA_ERR_ALIGN;
   if (!aligned(lens, 4) || !aligned(cu, 4) || !aligned(lse, 4) || !aligned(status, 4))
     return RA_ERR_ALIGN;
-  size_t need = 0;
+  a.q = q;
+  a.table = table;
+  a.width = width;
+  a.lens = lens;
   a.cu = cu;
-  st = paged_attn_plan(&a, &need);
+  a.out = out;
+  a.lse = lse;
+  a.scale_log2 = (scale > 0.f ? scale : 1.0f / __builtin_sqrtf((float)pages->D)) * 1.4426950408889634f;
+  a.status = status;
+  size_t need = 0;
+  st = paged_attn_plan(&a, &few, &need);
   if (st != RA_OK) return st;
   if (need > 0 && !workspace) return RA_ERR_NULL;
   if (workspace_bytes < need) return RA_ERR_BUFFER;
@@ -147,18 +160,13 @@ ra_status attn(const void* q, const ra_pages* pages, const int* table, int width
   if (overlap(outs, ins)) return RA_ERR_BUFFER;
   st = check_device(nullptr);
   if (st != RA_OK) return st;
-  a.q = q;
-  a.table = table;
-  a.width = width;
-  a.lens = lens;
-  a.out = out;
-  a.lse = lse;
-  a.scale_log2 = (scale > 0.f ? scale : 1.0f / __builtin_sqrtf((float)pages->D)) * 1.4426950408889634f;
-  a.status = status;
-  paged_attn_place(&a, workspace);
+  paged_attn_place(&a, &few, workspace);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  st = a.block_rows <= 16 ? launch_paged_rows(a, s) : launch_paged_tiles(a, s);
-  return st != RA_OK || a.n_split == 1 ? st : launch_paged_join(a, s);
+  if (few.n_items > 0) {
+    st = launch(few, s);
+    if (st != RA_OK) return st;
+  }
+  return launch(a, s);
 }
 
 }  // namespace
@@ -219,11 +227,11 @@ ra_status paged_attn_workspace(const ra_pages* pages, int B, int S_q, int total,
   if (!bytes) return RA_ERR_NULL;
   ra_status st = check_sizes(pages);
   if (st != RA_OK) return st;
-  PagedAttnArgs a = {};
+  PagedAttnArgs a = {}, few = {};
   st = attn_sizes(*pages, varlen != 0, B, S_q, varlen ? total : (long long)B * S_q, H_q, max_len,
                   window, n_sink, &a);
   if (st != RA_OK) return st;
-  return paged_attn_plan(&a, bytes);
+  return paged_attn_plan(&a, &few, bytes);
 }
 
 ra_status paged_attn(const void* q, const ra_pages* pages, const int* table, int width,

@@ -20,7 +20,8 @@
 // outputs' rounding alone makes 1.7e-3). Sums and statistics are float32.
 //
 // For up to 16 query rows a sequence and key/value head (new tokens times the heads
-// that share it), over 8-bit pages up to 48 in blocks of 16; more: paged_tiles.cu. A
+// that share it), over 8-bit pages up to 48 in blocks of 16; more: paged_tiles.cu. (Of
+// packed sequences of both kinds over 8-bit pages each kernel takes its own.) A
 // CTA takes one chunk of the slots that a block sees. A producer warp looks the pages
 // up, a lane for each, and asks for their boxes (TMA, swizzled, so that ldmatrix meets
 // no bank conflict; a page's row is one box, as some 30 cycles a box are what small
@@ -177,7 +178,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
   const PagedSeq sq = paged_seq(a, b);
   const int r0 = rb * RB;                   // the block's first of the head's query rows
   const int R = min(sq.n * grp - r0, RB);   // and how many
-  if (R <= 0) return;                       // a sequence of fewer new tokens
+  if (R <= 0 || !paged_mine(a, sq)) return; // a sequence of fewer new tokens, or of many
   const int first = sq.len - sq.n;          // position of the first new token
   PagedSpan<kTile> sp;
   sp.init(a, first + r0 / grp, first + (r0 + R - 1) / grp);
@@ -733,7 +734,7 @@ paged_join_few_kernel(const PagedAttnArgs a, int rows) {
   const PagedSeq sq = paged_seq(a, blk.b);
   if (!a.cu) wait_for_prior_grid();
   const int r_head = blk.rb * a.block_rows + r;        // of the head's rows
-  if (r_head >= sq.n * grp) return;
+  if (r_head >= sq.n * grp || !paged_mine(a, sq)) return;
   const int part = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + paged_part(a, item, 0, r);
   const float* o = a.part_o + paged_part(a, item, 0, r) * D + d;
@@ -875,9 +876,9 @@ ra_status launch_paged_rows(const PagedAttnArgs& a, cudaStream_t stream) {
 }
 
 ra_status launch_paged_join(const PagedAttnArgs& a, cudaStream_t stream) {
-  const long long items = a.n_items - a.n_whole;
+  const long long items = a.n_cut;
   if (a.block_rows <= 16) {
-    const long long R = (long long)a.T * (a.H_q / a.p.H_kv);
+    const long long R = a.few_rows > 0 ? a.few_rows : (long long)a.T * (a.H_q / a.p.H_kv);
     const int rows = R < a.block_rows ? (int)R : a.block_rows;    // those that may hold a token
     const long long grid = items * rows;
     if (grid > 0x7fffffffLL) return RA_ERR_RANGE;

@@ -59,15 +59,17 @@ struct PagedAttnArgs {
   float scale_log2;        // softmax scale * log2(e)
   // plan (paged_attn_plan): a sequence's new tokens give n * H_q / H_kv query rows
   // a key/value head, cut into blocks, few rows (block_rows 8 or 16: paged_attn.cu) or
-  // many (256: paged_tiles.cu). Of the n_items blocks the first
-  // n_whole go to one CTA each, the visible tiles of the others are cut into n_split
-  // chunks of `chunk` tiles.
-  int block_rows, n_items, n_whole, n_split, chunk;
+  // many (256: paged_tiles.cu). Of the n_items blocks n_cut, behind the first n_whole,
+  // have their visible tiles cut into n_split chunks of `chunk` tiles; the others go to
+  // one CTA each.
+  int block_rows, n_items, n_whole, n_cut, n_split, chunk;
   int n_rb;                // blocks of the longest sequence and head
+  int few_rows;            // packed: sequences of up to so many rows a head are the few rows'
+                           // kernel's, longer ones the other's; 0: all are this one's
   int rb_major;            // many rows: the blocks' order, see there
   int n_expanded;          // many rows over 8-bit pages: tiles a sequence's rows see at most
-  float* part_o;           // [n_items - n_whole][n_split][block_rows][D]
-  float* part_ml;          // [n_items - n_whole][n_split][block_rows][2]: maximum (base 2), sum
+  float* part_o;           // [n_cut][n_split][block_rows][D]
+  float* part_ml;          // [n_cut][n_split][block_rows][2]: maximum (base 2), sum
   __nv_bfloat16* expanded_k;     // [B][n_expanded][H_kv][128][D]
   __nv_bfloat16* expanded_v;
   int* status;
@@ -76,10 +78,11 @@ struct PagedAttnArgs {
 // Few rows: slots of a tile, 32 KB of keys and values at most.
 constexpr int paged_rows_tile(int D, bool quant) { return !quant && D == 128 ? 64 : 128; }
 
-// Fills the plan fields for the sizes in `a`; bytes: the workspace
-// needed. paged_attn_place puts its parts there.
-ra_status paged_attn_plan(PagedAttnArgs* a, size_t* bytes);
-void paged_attn_place(PagedAttnArgs* a, void* workspace);
+// Fills the plan fields for the sizes in `a`, and, where short sequences of a packed
+// call have a launch of their own, makes `few` that launch's arguments (else its n_items
+// is 0); bytes: the workspace needed. paged_attn_place puts their parts there.
+ra_status paged_attn_plan(PagedAttnArgs* a, PagedAttnArgs* few, size_t* bytes);
+void paged_attn_place(PagedAttnArgs* a, PagedAttnArgs* few, void* workspace);
 // The launchers of the two kernels and of the join of their chunks.
 ra_status launch_paged_rows(const PagedAttnArgs& a, cudaStream_t stream);
 ra_status launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t stream);

@@ -55,6 +55,12 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttnArgs& a, int b) {
   return s;
 }
 
+// Whether a sequence of a packed call is the launch's that `a` is of.
+__device__ __forceinline__ bool paged_mine(const PagedAttnArgs& a, const PagedSeq& s) {
+  if (a.few_rows == 0) return true;
+  return (s.n * (a.H_q / a.p.H_kv) <= a.few_rows) == (a.block_rows <= 16);
+}
+
 // Whether the row at position p sees slot j.
 __device__ __forceinline__ bool paged_sees(const PagedAttnArgs& a, int p, int j) {
   return j <= p && (a.window <= 0 || j > p - a.window || j < a.n_sink);
@@ -91,6 +97,16 @@ struct PagedSpan {
   }
 };
 
+// Sums of x over a warp's lanes up to each.
+__device__ __forceinline__ int warp_prefix(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
 // The block of query rows that item `item` is; every lane of a warp calls it. Few
 // rows: by sequence and head. Many: blocks of late tokens (the longest
 // walks) come first, across all heads of a sequence (and the sequences, where all
@@ -115,13 +131,12 @@ __device__ __forceinline__ PagedBlock paged_block(const PagedAttnArgs& a, int it
   int before = 0;                                  // blocks of a head before these 32 sequences
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
-    const int nb = b < a.B ? (paged_seq(a, b).n + tokens - 1) / tokens : 0;
-    int sum = nb;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int x = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += x;
+    int nb = 0;
+    if (b < a.B) {
+      const PagedSeq s = paged_seq(a, b);
+      if (paged_mine(a, s)) nb = (s.n + tokens - 1) / tokens;
     }
+    const int sum = warp_prefix(nb, lane);
     const uint32_t past = __ballot_sync(0xffffffffu, item < (long long)(before + sum) * H_kv);
     if (past) {
       const int src = __ffs(past) - 1;
@@ -141,8 +156,9 @@ struct PagedWork {
 };
 __device__ __forceinline__ PagedWork paged_work(const PagedAttnArgs& a, int cta) {
   if (cta < a.n_whole) return {cta, -1};
-  return {a.n_whole + (cta - a.n_whole) / a.n_split,
-          a.n_split > 1 ? (cta - a.n_whole) % a.n_split : -1};
+  const int x = cta - a.n_whole, cut = a.n_cut * a.n_split;
+  if (x < cut) return {a.n_whole + x / a.n_split, x % a.n_split};
+  return {a.n_whole + a.n_cut + x - cut, -1};
 }
 // The row of the partial results that is row r of chunk `split` of block `item`.
 __device__ __forceinline__ long long paged_part(const PagedAttnArgs& a, int item, int split, int r) {

@@ -673,48 +673,68 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
 // 8-bit pages to bf16 tiles [B][n_expanded][H_kv][128][D], keys and values: the
 // tiles that the sequences' new tokens see, in order; slots past the last and those
 // that no token sees as zeros. A CTA makes some rows of one tile and head, 16 values a
-// thread. Bound by the bytes, and by the chain of look-ups before them.
+// thread, and goes on where there are more of them than the card has places: a launch
+// for all that there may be takes 100 us of CTAs that only leave, for 64 sequences of 8K
+// slots. Bound by the bytes, and by the chain of look-ups before them.
 constexpr int kExpandThreads = 256;
+constexpr long long kExpandCtas = 2 * 8 * 152;
 template <int D>
 __global__ void __launch_bounds__(kExpandThreads)
-paged_expand_kernel(const PagedAttnArgs a) {
+paged_expand_kernel(const PagedAttnArgs a, uint32_t shares) {
   constexpr int kLanes = D / 16, kRows = kExpandThreads / kLanes, kShares = kTile / kRows;
-  const size_t tile = blockIdx.x / kShares;      // ((b, v), hk) in order
-  const int hk = (int)(tile % a.p.H_kv), rest = (int)(tile / a.p.H_kv);
-  const int v = rest % a.n_expanded, b = rest / a.n_expanded;
   let_dependents_start();
   wait_for_prior_grid();
-  const PagedSeq sq = paged_seq(a, b);
-  if (sq.n <= 0) return;
-  const PagedSpan<kTile> sp = sequence_span(a, sq);
-  if (v >= sp.n) return;
-  const int shift = 31 - __clz(a.p.page);
-  const int r = blockIdx.x % kShares * kRows + threadIdx.x / kLanes;
+  const int shift = 31 - __clz(a.p.page), lane = threadIdx.x & 31;
   const int d = threadIdx.x % kLanes * 16;
-  const int slot = sp.tile(v) * kTile + r;
-  long long from = -1;
-  if (slot < sp.hi && sp.meets(a, slot, 1) && (slot >> shift) < a.width) {
-    const int id = a.table[(size_t)b * a.width + (slot >> shift)];
-    if (id >= 0 && id < a.p.n_pages)
-      from = (((long long)id * a.p.H_kv + hk) << shift) + (slot & (a.p.page - 1));
-  }
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    uint32_t w[8] = {};
-    if (from >= 0) {
-      const uint4 c = *reinterpret_cast<const uint4*>((side ? a.p.v : a.p.k) + from * D + d);
-      const float scale = pow2_byte((side ? a.p.vs : a.p.ks)[from]);
-      const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float2 f = half2_values(e4m3x2_half2(cw[x / 2] >> (16 * (x % 2))));
-        w[x] = pack_bf16x2(f.x * scale, f.y * scale);
+  for (uint32_t share = blockIdx.x; share < shares; share += gridDim.x) {
+    // which tile of which sequence and head: looked up among their numbers of tiles
+    const int x = (int)(share / kShares);
+    int b0 = 0, before = 0;                        // tiles of the sequences before these 32
+    uint32_t past = 0;
+    int sum, nv;
+    for (;; b0 += 32) {
+      if (b0 >= a.B) return;                       // past the last
+      nv = 0;
+      if (b0 + lane < a.B) {
+        const PagedSeq sq = paged_seq(a, b0 + lane);
+        if (sq.n > 0 && paged_mine(a, sq)) nv = min(sequence_span(a, sq).n, a.n_expanded);
       }
+      sum = warp_prefix(nv, lane);
+      past = __ballot_sync(0xffffffffu, x < (before + sum) * a.p.H_kv);
+      if (past) break;
+      before += __shfl_sync(0xffffffffu, sum, 31);
     }
-    uint4* dst = reinterpret_cast<uint4*>((side ? a.expanded_v : a.expanded_k) +
-                                          (tile * kTile + r) * D + d);
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    const int src = __ffs(past) - 1, b = b0 + src;
+    const int in = x - (before + __shfl_sync(0xffffffffu, sum - nv, src)) * a.p.H_kv;
+    const int v = in / a.p.H_kv, hk = in % a.p.H_kv;
+    const size_t tile = ((size_t)b * a.n_expanded + v) * a.p.H_kv + hk;
+    const PagedSpan<kTile> sp = sequence_span(a, paged_seq(a, b));
+    const int r = share % kShares * kRows + threadIdx.x / kLanes;
+    const int slot = sp.tile(v) * kTile + r;
+    long long from = -1;
+    if (slot < sp.hi && sp.meets(a, slot, 1) && (slot >> shift) < a.width) {
+      const int id = a.table[(size_t)b * a.width + (slot >> shift)];
+      if (id >= 0 && id < a.p.n_pages)
+        from = (((long long)id * a.p.H_kv + hk) << shift) + (slot & (a.p.page - 1));
+    }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      uint32_t w[8] = {};
+      if (from >= 0) {
+        const uint4 c = *reinterpret_cast<const uint4*>((side ? a.p.v : a.p.k) + from * D + d);
+        const float scale = pow2_byte((side ? a.p.vs : a.p.ks)[from]);
+        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float2 f = half2_values(e4m3x2_half2(cw[x / 2] >> (16 * (x % 2))));
+          w[x] = pack_bf16x2(f.x * scale, f.y * scale);
+        }
+      }
+      uint4* dst = reinterpret_cast<uint4*>((side ? a.expanded_v : a.expanded_k) +
+                                            (tile * kTile + r) * D + d);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   }
 }
 
@@ -724,9 +744,11 @@ ra_status launch_tiles(const PagedAttnArgs& a, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
   PagePool p = a.p;
   if (kExpanded) {
-    const long long blocks = (long long)a.B * a.n_expanded * a.p.H_kv * (kTile * (D / 16) / kExpandThreads);
-    if (blocks > 0x7fffffffLL) return RA_ERR_RANGE;
-    if (!launch_early(paged_expand_kernel<D>, blocks, kExpandThreads, 0, stream, a))
+    const long long shares =
+        (long long)a.B * a.n_expanded * a.p.H_kv * (kTile * (D / 16) / kExpandThreads);
+    if (shares > 0x7fffffffLL) return RA_ERR_RANGE;
+    const long long ctas = shares < kExpandCtas ? shares : kExpandCtas;
+    if (!launch_early(paged_expand_kernel<D>, ctas, kExpandThreads, 0, stream, a, (uint32_t)shares))
       return RA_ERR_LAUNCH;
     p.k = reinterpret_cast<uint8_t*>(a.expanded_k);
     p.v = reinterpret_cast<uint8_t*>(a.expanded_v);
@@ -737,7 +759,7 @@ ra_status launch_tiles(const PagedAttnArgs& a, cudaStream_t stream) {
   if (!make_query_map(&mq, a.q, a.rows, a.H_q, D, grp, tt) ||
       !make_page_map(&mk, p, p.k, p.page, 1) || !make_page_map(&mv, p, p.v, p.page, 1))
     return RA_ERR_LAUNCH;
-  const long long grid = a.n_whole + (long long)(a.n_items - a.n_whole) * a.n_split;
+  const long long grid = a.n_items + (long long)a.n_cut * (a.n_split - 1);
   if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
   auto kern = paged_tiles_kernel<D, kExpanded>;
   static std::atomic<uint64_t> allowed;

@@ -145,6 +145,14 @@ CASES = [
     ("a_wide_table", [300, 129, 40], [200, 1, 40], 4, 2, 64, 16, 20000, 0, 0),
     ("many_sequences", [3 * i % 50 for i in range(70)], [(3 * i % 50) * (i % 3) // 2 for i in range(70)], 2, 1, 64, 16, 4, 0,
      0),
+    # wide tables: short and long ones in two launches over 8-bit pages
+    ("short_beside_long", [900, 1, 64, 700, 0, 2, 33, 17, 500, 1], [1, 1, 4, 300, 0, 2, 1, 17, 5, 1], 8, 2, 128, 16, 1000, 0, 0),
+    ("short_beside_long_window", [15000, 131, 64, 15900, 5, 222, 330, 177, 129], [3, 5, 6, 30, 5, 2, 1, 10, 7], 12, 4, 64, 64,
+     250, 14500, 300),
+    ("short_beside_long_split", [5000, 4999, 1, 4097, 130, 3000, 64, 2049], [1, 2, 1, 60, 1, 1, 4, 1], 4, 1, 128, 128, 260, 0, 0),
+    ("short_beside_long_group_of_20", [300, 40, 200, 129, 7, 64, 90, 1], [1, 1, 100, 2, 1, 3, 1, 1], 20, 1, 64, 32, 2048, 0, 0),
+    ("short_beside_one_of_30", [60 + i for i in range(40)], [1] * 39 + [30], 16, 2, 128, 16, 240, 0, 0),
+    ("none_of_them_long", [3 * i for i in range(12)], [0, 1, 1, 2, 1, 0, 1, 2, 1, 1, 1, 1], 8, 2, 64, 16, 3, 0, 0),
     ("many_single_tokens", [7 * i % 90 for i in range(67)], [1] * 67, 2, 2, 64, 32, 3, 20, 1),
 ]
 
@@ -699,3 +707,45 @@ def test_packed_calls_follow_each_other_without_waits(kind):
     for _ in range(3):
         for a, b in zip(run(False), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [[1] * 9, [40] * 9, [0] * 9, [1, 50] * 5 + [0] * 8], ids=["short", "long", "empty", "both"])
+def test_short_sequences_have_their_own_launch(kind, news):
+    """A bound on new tokens far above their mean: sequences of a few and of many rows
+    are launched apart, and here one of the launches may find nothing. Pages that are not
+    there are reported from both; rows of no sequence stay as they were."""
+    H_q, H_kv, D, page, B, mx = 8, 2, 64, 16, len(news), 500
+    lens = [max(n, 37 * (i + 1) % 300) for i, n in enumerate(news)]
+    pool = Pool(kind, H_kv, page, D, lens, 2000, seed=46)
+    g = torch.Generator().manual_seed(47)
+    total = sum(news) + 5
+    q = torch.randn(total, H_q, D, generator=g).to(torch.bfloat16)
+    parts = [x.numpy() for x in torch.split(q[:-5].float(), news)]
+    q = q.to(DEV)
+    cu = np.concatenate([[0], np.cumsum(news)])
+    n_bytes = binding.paged_attn_workspace_bytes(pool.cache, B, mx, H_q, 2000 * page, total=total)
+    ws = torch.full((n_bytes,), 255, dtype=torch.uint8, device=DEV)      # NaN
+    out, lse = torch.full_like(q, 7.0), torch.full((H_q, total), 7.0, device=DEV)
+    st = status_word()
+    binding.paged_attn_varlen(q, pool.cache, pool.table_d, ints(lens), ints(cu.tolist()), mx, out=out, lse=lse, workspace=ws,
+                              dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert bool((out[cu[-1]:] == 7).all()) and bool((lse[:, cu[-1]:] == 7).all())
+    k, v, has = pool.rows(max(lens))
+    k, v = np.nan_to_num(k), np.nan_to_num(v)
+    want, want_l = paged.attention(parts, k, v, lens, news, has, 0, 0)
+    t_out, t_lse = bounds(parts, k, v, lens, news, has, 0, 0, want, 2.0 ** -8, D ** -0.5)
+    for b, n in enumerate(news):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        check(out[rows], want[b], t_out[b], f"out of {b}")
+        check(lse[:, rows], want_l[b], t_lse[b], f"lse of {b}")
+    for gone in {int(np.argmax(news)), int(np.argmin([n if n else 1 << 20 for n in news]))}:
+        if news[gone] == 0:
+            continue
+        table = pool.table_d.clone()
+        table[gone, 0] = -1
+        st = status_word()
+        binding.paged_attn_varlen(q, pool.cache, table, ints(lens), ints(cu.tolist()), mx, workspace=ws, dev_status=st)
+        assert int(st.item()) == RANGE
