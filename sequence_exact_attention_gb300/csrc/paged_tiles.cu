@@ -27,8 +27,8 @@
 // What bounds it: the softmax, as in the forward kernel (attn_tc.cu), some 1.55 us a
 // tile of two times 128 x 128 scores at D = 128 where the products take 1.1; and 7 us a
 // CTA outside its tiles (look-ups 1.2, the first tile's way 2 to 3, the end 3). Measured,
-// replayed from a graph: 4096 tokens behind 12288 slots, 32 heads on 8, D = 128: 646 us,
-// 1490 TFLOP/s; 64 tokens behind 100000 slots: 94 us.
+// replayed from a graph: 4096 tokens behind 12288 slots, 32 heads on 8, D = 128: 650 us,
+// 1480 TFLOP/s; 64 tokens behind 100000 slots: 96 us.
 //
 // Roundings: weights to bf16 (2^-8 of a weight at most); sums and statistics float32.
 // Barriers:
