@@ -14,7 +14,9 @@
 // in base 2, with a maximum m' of their own: the row's largest weight is between
 // 1 and 2^5, whatever the scales. Queries become halves times a power of two a row
 // (exact for values down to 2^-17 of the row's largest).
-// Roundings: weights to half (2^-11 of a weight at most). A bf16 page's values may
+// Roundings: weights to half (2^-11 of a weight at most; of weights below 2^-14, half's
+// least normal number, 2^-25, where the row's largest is 1 or more and its codes reach
+// 224: beside what that adds to the row's outputs nothing). A bf16 page's values may
 // pass half's range, so there a weight is the sum of two bf16 numbers (2^-16) in two
 // products (one, rounded at 2^-8, made the error against 64 bits 2.3e-3 where the
 // outputs' rounding alone makes 1.7e-3). Sums and statistics are float32.
