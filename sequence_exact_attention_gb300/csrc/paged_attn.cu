@@ -704,20 +704,19 @@ __device__ __forceinline__ float chunk_weight(float2 ml, float m) {     // below
   return ml.x == m ? 1.f : exp2f(ml.x - m);
 }
 
+// Four outputs of row `row` of q and of head h, from d on.
 template <int D>
-__device__ __forceinline__ void store_row(const PagedAttnArgs& a, const PagedBlock& blk,
-                                          const PagedSeq& sq, int t, int g, int d, float4 y,
+__device__ __forceinline__ void store_row(const PagedAttnArgs& a, int row, int h, int d, float4 y,
                                           float m, float l) {
-  const int h = blk.hk * (a.H_q / a.p.H_kv) + g;
-  const long long row = (long long)(sq.row0 + t) * a.H_q + h;
+  const long long at = ((long long)row * a.H_q + h) * D + d;
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);     // 0: no slot; NaN stays
-  if (in_range(row * D + d, 4, (long long)a.rows * a.H_q * D, a.status))
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d) =
+  if (in_range(at, 4, (long long)a.rows * a.H_q * D, a.status))
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
         make_uint2(sm100::pack_bf16x2(y.x * inv, y.y * inv), sm100::pack_bf16x2(y.z * inv, y.w * inv));
   if (d == 0 && a.lse) {
-    const long long at = paged_lse_at(a, blk.b, sq.row0 + t, t, h);
-    if (in_range(at, 1, (long long)a.rows * a.H_q, a.status))
-      a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    const long long to = paged_lse_at(a, a.cu ? 0 : row / a.T, row, a.cu ? 0 : row % a.T, h);
+    if (in_range(to, 1, (long long)a.rows * a.H_q, a.status))
+      a.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -779,76 +778,110 @@ paged_join_few_kernel(const PagedAttnArgs a, int rows) {
     y.z = fmaf(f, x.z, y.z);
     y.w = fmaf(f, x.w, y.w);
   }
-  store_row<D>(a, blk, sq, r_head / grp, r_head % grp, d, y, m, l);
+  store_row<D>(a, sq.row0 + r_head / grp, blk.hk * grp + r_head % grp, d, y, m, l);
 }
 
-// Many rows: a CTA joins some rows of one block, kAtOnce outputs of four values a
-// thread, first all the rows' weights, then their outputs, so that what it looks up and
-// waits for comes once. (A CTA for every row took 32 us of 19456 rows of two chunks, a
-// warp 25, one output after the other 18, four at once 11.)
+// Many rows: a warp joins kAtOnce rows (D = 64: pairs of rows) of one block, a float4 of
+// the output a lane. Its lanes look at the chunks' maxima and sums, 32 at a time, while
+// the first kPre chunks' outputs are on their way; which rows they are the block's first
+// chunk has noted, as looking a packed block up would take as long as the rest. What
+// bounds it is that way, and code that runs once. Attention of 64 tokens behind 100000
+// slots (19 chunks of 2048 rows) 90.5 us, of two sequences under a window of 2048 (2
+// chunks of 18432) 85 (weights made for the whole CTA first, in shared memory: 96.5 and
+// 88; four rows a warp and four chunks: 91 and 90; one row: 91 and 89).
 template <int D, int kAtOnce>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_many_kernel(const PagedAttnArgs a) {
-  constexpr int rows = kAtOnce * kJoinThreads / (D / 4);
-  extern __shared__ float2 sW[];             // [n_split][rows] (weight, sum), [rows] (maximum, sum)
+  constexpr int kLanes = D / 4, kPer = 32 / kLanes;           // lanes a row, rows side by side
+  constexpr int kRows = kAtOnce * kPer * (kJoinThreads / 32);  // of a CTA
+  constexpr int kPre = kAtOnce == 1 ? 8 : 2;
   let_dependents_start();
-  if (a.cu) wait_for_prior_grid();
-  const int per = a.block_rows / rows;
-  const int item = a.n_whole + blockIdx.x / per, r0 = blockIdx.x % per * rows;
-  const PagedBlock blk = paged_block(a, item);
-  if (blk.b < 0) return;                     // past the last block of the batch
-  const int grp = a.H_q / a.p.H_kv, tt = 128 / grp;
-  const PagedSeq sq = paged_seq(a, blk.b);
-  if (!a.cu) wait_for_prior_grid();
-  // row r's token; below 0: it has none
-  auto token = [&](int r) -> int {
-    const int t = (2 * blk.rb + (r >> 7)) * tt + (r & 127) / grp;
-    return (r & 127) < tt * grp && t < sq.n ? t : -1;
-  };
-  for (int i = threadIdx.x; i < rows * a.n_split; i += kJoinThreads) {
-    const int s = i / rows, r = i & (rows - 1);
-    sW[i] = token(r0 + r) < 0 ? make_float2(-INFINITY, 0.f)
-                              : reinterpret_cast<const float2*>(a.part_ml)[paged_part(a, item, s, r0 + r)];
-  }
-  __syncthreads();
-  if (threadIdx.x < rows) {
-    float m = -INFINITY, l = 0.f;
-    for (int s = 0; s < a.n_split; ++s) m = fmaxf(m, sW[s * rows + threadIdx.x].x);
-    for (int s = 0; s < a.n_split; ++s) {
-      float2& x = sW[s * rows + threadIdx.x];
-      x.x = chunk_weight(x, m);
-      if (!(x.x < 0.f)) l = fmaf(x.x, x.y, l);
-    }
-    sW[a.n_split * rows + threadIdx.x] = make_float2(m, l);
-  }
-  __syncthreads();
-  const float* o[kAtOnce];
+  wait_for_prior_grid();
+  const int cut = blockIdx.x / (256 / kRows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane / kLanes;
+  const int d = lane % kLanes * 4;
+  const int r0 = blockIdx.x % (256 / kRows) * kRows + warp * (kAtOnce * kPer);   // the warp's first
+  const int4 blk = a.part_block[cut];
+  // chunk s of row r is part s * 256 + r of the block's
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (size_t)cut * a.n_split * 256;
+  const float* o = a.part_o + ((size_t)cut * a.n_split * 256 + r0 + half) * D + d;
+  float4 pre[kPre][kAtOnce];
+#pragma unroll
+  for (int s = 0; s < kPre; ++s)
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e)
+      if (s < a.n_split)
+        pre[s][e] = *reinterpret_cast<const float4*>(o + ((size_t)s * 256 + e * kPer) * D);
+  float m[kAtOnce][kPer], l[kAtOnce][kPer], w[kAtOnce][kPer];
   float4 y[kAtOnce];
-  const int d = threadIdx.x % (D / 4) * 4, first = threadIdx.x / (D / 4);
-  constexpr int kStep = kJoinThreads / (D / 4);       // rows that the CTA's threads make at a time
+  auto chunk = [&](int s, int e, int p) -> float2 {
+    return s < a.n_split ? ml[(size_t)s * 256 + r0 + e * kPer + p] : make_float2(-INFINITY, 0.f);
+  };
 #pragma unroll
   for (int e = 0; e < kAtOnce; ++e) {
-    o[e] = a.part_o + paged_part(a, item, 0, r0 + first + e * kStep) * D + d;
     y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-#pragma unroll 4
-  for (int s = 0; s < a.n_split; ++s)
 #pragma unroll
-    for (int e = 0; e < kAtOnce; ++e) {
-      const float4 f = *reinterpret_cast<const float4*>(o[e] + (size_t)s * a.block_rows * D);
-      const float x = sW[s * rows + first + e * kStep].x;
-      const bool seen = !(x < 0.f);
-      y[e].x = fmaf(seen ? x : 0.f, seen ? f.x : 0.f, y[e].x);
-      y[e].y = fmaf(seen ? x : 0.f, seen ? f.y : 0.f, y[e].y);
-      y[e].z = fmaf(seen ? x : 0.f, seen ? f.z : 0.f, y[e].z);
-      y[e].w = fmaf(seen ? x : 0.f, seen ? f.w : 0.f, y[e].w);
+    for (int p = 0; p < kPer; ++p) {
+      l[e][p] = 0.f;
+      m[e][p] = -INFINITY;
+      for (int s = lane; s < a.n_split; s += 32) m[e][p] = fmaxf(m[e][p], chunk(s, e, p).x);
+#pragma unroll
+      for (int x = 16; x > 0; x /= 2)
+        m[e][p] = fmaxf(m[e][p], __shfl_xor_sync(0xffffffffu, m[e][p], x));
     }
+  }
+  auto add = [&](int s, int e, float4 f) {
+    float x = __shfl_sync(0xffffffffu, w[e][0], s & 31);
+    if (kPer == 2) {
+      const float x1 = __shfl_sync(0xffffffffu, w[e][kPer - 1], s & 31);
+      if (half) x = x1;
+    }
+    if (x < 0.f) return;
+    y[e].x = fmaf(x, f.x, y[e].x);
+    y[e].y = fmaf(x, f.y, y[e].y);
+    y[e].z = fmaf(x, f.z, y[e].z);
+    y[e].w = fmaf(x, f.w, y[e].w);
+  };
+  for (int s0 = 0; s0 < a.n_split; s0 += 32) {
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e)
+#pragma unroll
+      for (int p = 0; p < kPer; ++p) {
+        const float2 x = chunk(s0 + lane, e, p);
+        w[e][p] = chunk_weight(x, m[e][p]);
+        if (!(w[e][p] < 0.f)) l[e][p] = fmaf(w[e][p], x.y, l[e][p]);
+      }
+    if (s0 == 0) {
+#pragma unroll
+      for (int s = 0; s < kPre; ++s)
+        if (s < a.n_split)
+#pragma unroll
+          for (int e = 0; e < kAtOnce; ++e) add(s, e, pre[s][e]);
+    }
+    const int end = min(s0 + 32, a.n_split);
+#pragma unroll 4
+    for (int s = s0 > 0 ? s0 : kPre; s < end; ++s)
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e)
+        add(s, e, *reinterpret_cast<const float4*>(o + ((size_t)s * 256 + e * kPer) * D));
+  }
+  const int grp = a.H_q / a.p.H_kv, tt = 128 / grp;
 #pragma unroll
   for (int e = 0; e < kAtOnce; ++e) {
-    const int r = first + e * kStep, t = token(r0 + r);
-    if (t < 0) continue;
-    const float2 ml = sW[a.n_split * rows + r];
-    store_row<D>(a, blk, sq, t, ((r0 + r) & 127) % grp, d, y[e], ml.x, ml.y);
+    float lr = 0.f, mr = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+#pragma unroll
+      for (int x = 16; x > 0; x /= 2) l[e][p] += __shfl_xor_sync(0xffffffffu, l[e][p], x);
+      if (p == half) {
+        lr = l[e][p];
+        mr = m[e][p];
+      }
+    }
+    const int r = r0 + e * kPer + half, in = r & 127;
+    const int t = (r >> 7) * tt + in / grp;
+    if (in >= tt * grp || t >= blk.y) continue;                // no token's
+    store_row<D>(a, blk.x + t, blk.z * grp + in % grp, d, y[e], mr, lr);
   }
 }
 
@@ -889,17 +922,16 @@ ra_status launch_paged_join(const PagedAttnArgs& a, cudaStream_t stream) {
     auto kern = a.p.D == 64 ? paged_join_few_kernel<64> : paged_join_few_kernel<128>;
     return launch_early(kern, grid, kJoinThreads, 0, stream, a, rows) ? RA_OK : RA_ERR_LAUNCH;
   }
-  // a quarter of the rows a CTA where CTAs would be few
-  int rows = 4 * kJoinThreads / (a.p.D / 4);
-  auto kern = a.p.D == 64 ? paged_join_many_kernel<64, 4> : paged_join_many_kernel<128, 4>;
-  if (items * (a.block_rows / rows) < 2 * 152) {
-    rows /= 4;
+  // half the rows a CTA where CTAs would be few
+  int rows = 2 * kJoinThreads / (a.p.D / 4);
+  auto kern = a.p.D == 64 ? paged_join_many_kernel<64, 2> : paged_join_many_kernel<128, 2>;
+  if (items * (256 / rows) < 2 * 152) {
+    rows /= 2;
     kern = a.p.D == 64 ? paged_join_many_kernel<64, 1> : paged_join_many_kernel<128, 1>;
   }
-  const long long grid = items * (a.block_rows / rows);
+  const long long grid = items * (256 / rows);
   if (grid > 0x7fffffffLL) return RA_ERR_RANGE;
-  const int smem = (a.n_split + 1) * rows * (int)sizeof(float2);
-  return launch_early(kern, grid, kJoinThreads, smem, stream, a) ? RA_OK : RA_ERR_LAUNCH;
+  return launch_early(kern, grid, kJoinThreads, 0, stream, a) ? RA_OK : RA_ERR_LAUNCH;
 }
 
 }  // namespace ra

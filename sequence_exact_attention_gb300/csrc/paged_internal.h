@@ -70,6 +70,8 @@ struct PagedAttnArgs {
   int n_expanded;          // many rows over 8-bit pages: tiles a sequence's rows see at most
   float* part_o;           // [n_cut][n_split][block_rows][D]
   float* part_ml;          // [n_cut][n_split][block_rows][2]: maximum (base 2), sum
+  int4* part_block;        // many rows: [n_cut] the block's first row in q, its tokens (0: there
+                           // is no such block), its key/value head
   __nv_bfloat16* expanded_k;     // [B][n_expanded][H_kv][128][D]
   __nv_bfloat16* expanded_v;
   int* status;

@@ -104,7 +104,9 @@ ra_status plan_many(PagedAttnArgs* a) {
   return cut(a, items, whole, rest, tiles, best, 4);
 }
 
-size_t part_bytes(const PagedAttnArgs& a) { return parts(a) * (a.p.D + 2) * sizeof(float); }
+size_t part_bytes(const PagedAttnArgs& a) {
+  return parts(a) * (a.p.D + 2) * sizeof(float) + (size_t)a.n_cut * sizeof(int4);
+}
 // One of the two expanded tensors' values.
 size_t expanded(const PagedAttnArgs& a) {
   return (size_t)a.B * a.n_expanded * a.p.H_kv * 128 * a.p.D;
@@ -156,7 +158,8 @@ void paged_attn_place(PagedAttnArgs* a, PagedAttnArgs* few, void* workspace) {
     if (x->n_items == 0) continue;
     x->part_o = at;
     x->part_ml = at + parts(*x) * x->p.D;
-    at = x->part_ml + parts(*x) * 2;
+    x->part_block = reinterpret_cast<int4*>(x->part_ml + parts(*x) * 2);
+    at = reinterpret_cast<float*>(x->part_block + x->n_cut);
   }
 }
 

@@ -27,8 +27,8 @@
 // What bounds it: the softmax, as in the forward kernel (attn_tc.cu), some 1.55 us a
 // tile of two times 128 x 128 scores at D = 128 where the products take 1.1; and 7 us a
 // CTA outside its tiles (look-ups 1.2, the first tile's way 2 to 3, the end 3). Measured,
-// replayed from a graph: 4096 tokens behind 12288 slots, 32 heads on 8, D = 128: 650 us,
-// 1480 TFLOP/s; 64 tokens behind 100000 slots: 96 us.
+// replayed from a graph: 4096 tokens behind 12288 slots, 32 heads on 8, D = 128: 647 us,
+// 1490 TFLOP/s; 64 tokens behind 100000 slots: 90 us.
 //
 // Roundings: weights to bf16 (2^-8 of a weight at most); sums and statistics float32.
 // Barriers:
@@ -221,11 +221,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
   const PagedWork work = paged_work(a, blockIdx.x);
   const PagedBlock blk = paged_block(a, work.item);
   const int b = blk.b, hk = blk.hk;
-  if (b < 0) return;                              // past the last block of the batch
-  const PagedSeq sq = paged_seq(a, b);
+  const PagedSeq sq = b >= 0 ? paged_seq(a, b) : PagedSeq{0, 0, 0};
   const int t0 = blk.rb * 2 * tt;                 // the block's first new token
-  if (t0 >= sq.n) return;
   const int n_tok = min(2 * tt, sq.n - t0);
+  if (work.split == 0 && threadIdx.x == 0)        // for the join
+    a.part_block[work.item - a.n_whole] = make_int4(sq.row0 + t0, max(n_tok, 0), hk, 0);
+  if (n_tok <= 0) return;                         // past the last block of the batch
   const bool two = n_tok > tt;
   const int first = sq.len - sq.n + t0;           // its position
   PagedSpan<kTile> sp;
