@@ -726,7 +726,7 @@ constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_few_kernel(const PagedAttnArgs a, int rows) {
-  constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes;
+  constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes, kPre = 4;
   __shared__ float4 sO[kParts][kLanes];
   __shared__ float sM[kParts], sL[kParts];
   let_dependents_start();
@@ -743,19 +743,35 @@ paged_join_few_kernel(const PagedAttnArgs a, int rows) {
   const float* o = a.part_o + paged_part(a, item, 0, r) * D + d;
   float m = -INFINITY, l = 0.f;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = part; s < a.n_split; s += kParts) m = fmaxf(m, ml[s * a.block_rows].x);
-#pragma unroll 4
-  for (int s = part; s < a.n_split; s += kParts) {
-    const float2 x = ml[s * a.block_rows];
-    const float4 f = *reinterpret_cast<const float4*>(o + (size_t)s * a.block_rows * D);
+  auto chunk = [&](int s) -> float2 { return ml[s * a.block_rows]; };
+  auto outputs = [&](int s) -> float4 {
+    return *reinterpret_cast<const float4*>(o + (size_t)s * a.block_rows * D);
+  };
+  auto add = [&](float2 x, float4 f) {
     const float w = chunk_weight(x, m);
-    if (w < 0.f) continue;
+    if (w < 0.f) return;
     l = fmaf(w, x.y, l);
     y.x = fmaf(w, f.x, y.x);
     y.y = fmaf(w, f.y, y.y);
     y.z = fmaf(w, f.z, y.z);
     y.w = fmaf(w, f.w, y.w);
+  };
+  // the first ones' loads all at once
+  float2 pre_ml[kPre];
+  float4 pre_o[kPre];
+#pragma unroll
+  for (int x = 0; x < kPre; ++x) {
+    const int s = part + x * kParts;
+    pre_ml[x] = s < a.n_split ? chunk(s) : make_float2(-INFINITY, 0.f);
+    pre_o[x] = s < a.n_split ? outputs(s) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+#pragma unroll
+  for (int x = 0; x < kPre; ++x) m = fmaxf(m, pre_ml[x].x);
+  for (int s = part + kPre * kParts; s < a.n_split; s += kParts) m = fmaxf(m, chunk(s).x);
+#pragma unroll
+  for (int x = 0; x < kPre; ++x) add(pre_ml[x], pre_o[x]);
+#pragma unroll 4
+  for (int s = part + kPre * kParts; s < a.n_split; s += kParts) add(chunk(s), outputs(s));
   sO[part][d / 4] = y;
   if (d == 0) {
     sM[part] = m;
