@@ -12,12 +12,16 @@
 // The scale 2^e of a value would leave half's range in a weight, so weights are
 //   w_j = 2^(s_j + e_j - m'),  out = sum w_j c_j 2^(m' - m) / sum 2^(s_j - m)
 // in base 2, with a maximum m' of their own: the row's largest weight is between
-// 1 and 2^5, whatever the scales. Queries become halves times a power of two a row
-// (exact for values down to 2^-17 of the row's largest).
-// Roundings: weights to half (2^-11 of a weight at most; of weights below 2^-14, half's
-// least normal number, 2^-25, where the row's largest is 1 or more and its codes reach
-// 224: beside what that adds to the row's outputs nothing). A bf16 page's values may
-// pass half's range, so there a weight is the sum of two bf16 numbers (2^-16) in two
+// 2^10 and 2^15, whatever the scales. Where slots' scales lie far apart, though, one
+// maximum over s + e leaves the others nothing: a row's one value of 2^30 would round
+// the weights of all slots around 1 to 0, and with them the dimensions in which it is 0
+// itself. So a row whose m' - m passes some visible slot's e by 10 takes that step of 16
+// slots apart, its weights as two bf16 numbers. Every other weight is 2^(s_j - m) or
+// more. Queries become halves times a power of two a row (exact for values down to
+// 2^-17 of the row's largest).
+// Roundings: weights to half, 2^-11 of a weight at most, or 2^-25 of the row's largest
+// 2^(s - m), whatever the values. A bf16 page's values may pass half's range, so there,
+// and in steps taken apart, a weight is the sum of two bf16 numbers (2^-16) in two
 // products (one, rounded at 2^-8, made the error against 64 bits 2.3e-3 where the
 // outputs' rounding alone makes 1.7e-3). Sums and statistics are float32.
 //
@@ -43,6 +47,9 @@
 //
 // Measured, replayed from a graph: 8 x 128K slots of 8 heads, D = 128, 8 bits 309 us,
 // 7.0 TB/s; 32 ragged sequences up to 8K slots, bf16 in pages of 16 109.5 us, 6.1 TB/s.
+// (Steps taken apart cost those that are not nothing in blocks of 8 rows; in blocks of
+// 16, whose registers are used up, 1 to 5 %: 8 x 32K slots of 4 heads, D = 128, 25 rows
+// 126 instead of 125 us; 8 x 64K of 8, D = 64, 16 rows 163 instead of 156.)
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -65,7 +72,8 @@ namespace {
 constexpr int kWarps = 4;                 // that compute
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr float kRescaleLog2 = 4.f;       // weights stay below 2^5
+constexpr float kRescaleLog2 = 4.f;       // weights stay below 2^5,
+constexpr float kHalfUp = 10.f;           // halves below 2^15
 constexpr float kLn2 = 0.69314718055994531f;
 
 // d += a b.
@@ -316,7 +324,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     // Running state of rows 2c and 2c + 1. What the exponents subtract: the running
     // maximum in base 2, rounded down, so that raising it scales sums by a power of
     // two, -inf until the row has seen a slot; a score kRescaleLog2 above raises it.
-    // (sub2: that of the weights, with the values' scales.)
+    // (sub2: that of the weights, with the values' scales, less kHalfUp.)
     float o[NT][KS][4];
     float sub[NT][2], sub2[NT][2], l[NT][2];
 #pragma unroll
@@ -331,6 +339,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         sub[nt][h] = sub2[nt][h] = -INFINITY;
       }
     }
+    // 8 bits: value scales below 2^low are too far below what one of this lane's rows has met
+    float low = -INFINITY;
     auto scale_row = [&](int nt, int h, float mul) {
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
@@ -431,68 +441,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (lost(x) || !paged_sees(a, pos(nt, h), j0 + x)) s[nt][2 * i + h] = -INFINITY;
           }
         }
-        // ---- raise the maxima when a score passes its bound: rare after the first tile
-        float top[NT][2], top2[NT][2];
-        bool raise = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            top[nt][h] = top2[nt][h] = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              top[nt][h] = fmaxf(top[nt][h], s[nt][2 * i + h]);
-              if (kQuant) top2[nt][h] = fmaxf(top2[nt][h], s[nt][2 * i + h] + ev[i]);
-            }
-            raise |= top[nt][h] > sub[nt][h] + kRescaleLog2;
-            if (kQuant) raise |= top2[nt][h] > sub2[nt][h] + kRescaleLog2;
-          }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              auto raise_to = [&](float x, float& sub_) -> float {   // what sums are multiplied by
-                if (!(x > sub_ + kRescaleLog2)) return 1.f;
-                const float to = floorf(x);
-                const float alpha = sub_ == -INFINITY ? 0.f : exp2f(sub_ - to);
-                sub_ = to;
-                return alpha;
-              };
-              const float alpha = raise_to(row_max(top[nt][h]), sub[nt][h]);
-              l[nt][h] *= alpha;
-              scale_row(nt, h, kQuant ? raise_to(row_max(top2[nt][h]), sub2[nt][h]) : alpha);
-            }
-        }
-        // ---- weights, as B operands: one half, or two bf16 numbers, what the first
-        // leaves being the second
-        uint32_t pf[NT][2], pl[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          // (a row that has seen nothing has scores of -inf alone)
-          const float less[2] = {fmaxf(sub[nt][0], -FLT_MAX), fmaxf(sub[nt][1], -FLT_MAX)};
-          const float less2[2] = {fmaxf(sub2[nt][0], -FLT_MAX), fmaxf(sub2[nt][1], -FLT_MAX)};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float w[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float x = s[nt][2 * i + h];
-              const float p = sm100::ex2_approx(x - less[h]);
-              l[nt][h] += p;
-              w[h] = kQuant ? sm100::ex2_approx(x + (ev[i] - less2[h])) : p;
-            }
-            if constexpr (kQuant) {
-              pf[nt][i] = transpose8x8(pack_half2(w[0], w[1]));
-            } else {
-              const uint32_t u = sm100::pack_bf16x2(w[0], w[1]);
-              pf[nt][i] = transpose8x8(u);
-              pl[nt][i] = transpose8x8(sm100::pack_bf16x2(
-                  w[0] - __uint_as_float(u << 16), w[1] - __uint_as_float(u & 0xffff0000u)));
-            }
-          }
-        }
-        // ---- their products with the values: rows of o are dimensions
         // the halves of slots 2c, 2c + 1, and + 8 to keep: those that the row at p, or
         // (kAny) any row, sees
         constexpr int kAny = -1;
@@ -537,6 +485,134 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int i = 0; i < 4; ++i) af[x][i] &= keep[i >> 1];
         };
+        // ---- raise the maxima when a score passes its bound: rare after the first tile
+        float top[NT][2], top2[NT][2];
+        bool raise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            top[nt][h] = top2[nt][h] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              top[nt][h] = fmaxf(top[nt][h], s[nt][2 * i + h]);
+              if (kQuant) top2[nt][h] = fmaxf(top2[nt][h], s[nt][2 * i + h] + ev[i]);
+            }
+            raise |= top[nt][h] > sub[nt][h] + kRescaleLog2;
+            if (kQuant) raise |= top2[nt][h] > sub2[nt][h] + (kRescaleLog2 + kHalfUp);
+          }
+        if (kQuant) raise |= fminf(ev[0], ev[1]) < low;
+        if (__any_sync(0xffffffffu, raise)) {
+          low = -INFINITY;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // (to x rounded down, less `up`); what sums are multiplied by
+              auto raise_to = [&](float x, float up, float& sub_) -> float {
+                if (!(x > sub_ + (kRescaleLog2 + up))) return 1.f;
+                const float to = floorf(x) - up;
+                const float alpha = sub_ == -INFINITY ? 0.f : exp2f(sub_ - to);
+                sub_ = to;
+                return alpha;
+              };
+              const float alpha = raise_to(row_max(top[nt][h]), 0.f, sub[nt][h]);
+              l[nt][h] *= alpha;
+              scale_row(nt, h,
+                        kQuant ? raise_to(row_max(top2[nt][h]), kHalfUp, sub2[nt][h]) : alpha);
+              if (kQuant) low = fmaxf(low, sub2[nt][h] - sub[nt][h]);    // (NaN: nothing seen)
+            }
+          // the rows (bit 2 nt + h) that have met too much for a slot that they see, as all
+          // lanes that hold the row know
+          uint32_t wide = 0;
+          if (kQuant && __any_sync(0xffffffffu, fminf(ev[0], ev[1]) < low)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                bool far = false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  far |= s[nt][2 * i + h] > -INFINITY && ev[i] < sub2[nt][h] - sub[nt][h];
+                uint32_t of_c = __ballot_sync(0xffffffffu, far);
+                of_c |= of_c >> 16;
+                of_c |= of_c >> 8;
+                of_c |= of_c >> 4;
+                wide |= (of_c >> c & 1u) << (2 * nt + h);
+              }
+          }
+          if (kQuant && __any_sync(0xffffffffu, wide)) {
+            // Rows to which a slot's value scale is too small for a half's range: their
+            // products of this step, weights in two bf16 numbers, codes in one (exact). What
+            // follows finds them without scores: weights of 0, which NaN codes, here left to
+            // it, make NaN.
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t wh[2], wl[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float w[2] = {0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float& x = s[nt][2 * i + h];
+                  if (wide >> (2 * nt + h) & 1u) {
+                    l[nt][h] += sm100::ex2_approx(x - sub[nt][h]);
+                    w[h] = sm100::ex2_approx(x + (ev[i] - sub2[nt][h]));
+                    x = -INFINITY;
+                  }
+                }
+                const uint32_t u = sm100::pack_bf16x2(w[0], w[1]);
+                wh[i] = transpose8x8(u);
+                wl[i] = transpose8x8(sm100::pack_bf16x2(
+                    w[0] - __uint_as_float(u << 16), w[1] - __uint_as_float(u & 0xffff0000u)));
+              }
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k) {
+                uint32_t af[kPer][4];
+                load_values(k, af);
+#pragma unroll
+                for (int x = 0; x < kPer; ++x) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const float2 f = half2_values(af[x][i]);
+                    af[x][i] = sm100::pack_bf16x2(f.x == f.x ? f.x : 0.f, f.y == f.y ? f.y : 0.f);
+                  }
+                  mma16816<false>(o[nt][kPer * k + x], af[x], wh[0], wh[1]);
+                  mma16816<false>(o[nt][kPer * k + x], af[x], wl[0], wl[1]);
+                }
+              }
+            }
+          }
+        }
+        // ---- weights, as B operands: one half, or two bf16 numbers, what the first
+        // leaves being the second
+        uint32_t pf[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          // (a row that has seen nothing has scores of -inf alone)
+          const float less[2] = {fmaxf(sub[nt][0], -FLT_MAX), fmaxf(sub[nt][1], -FLT_MAX)};
+          const float less2[2] = {fmaxf(sub2[nt][0], -FLT_MAX), fmaxf(sub2[nt][1], -FLT_MAX)};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float x = s[nt][2 * i + h];
+              const float p = sm100::ex2_approx(x - less[h]);
+              l[nt][h] += p;
+              w[h] = kQuant ? sm100::ex2_approx(x + (ev[i] - less2[h])) : p;
+            }
+            if constexpr (kQuant) {
+              pf[nt][i] = transpose8x8(pack_half2(w[0], w[1]));
+            } else {
+              const uint32_t u = sm100::pack_bf16x2(w[0], w[1]);
+              pf[nt][i] = transpose8x8(u);
+              pl[nt][i] = transpose8x8(sm100::pack_bf16x2(
+                  w[0] - __uint_as_float(u << 16), w[1] - __uint_as_float(u & 0xffff0000u)));
+            }
+          }
+        }
+        // ---- their products with the values: rows of o are dimensions
         auto multiply = [&](float (&acc)[4], const uint32_t (&af)[4], int nt) {
           mma16816<kQuant>(acc, af, pf[nt][0], pf[nt][1]);
           if (!kQuant) mma16816<kQuant>(acc, af, pl[nt][0], pl[nt][1]);
