@@ -17,8 +17,8 @@
 // the weights of all slots around 1 to 0, and with them the dimensions in which it is 0
 // itself. So a row whose m' - m passes some visible slot's e by 10 takes that step of 16
 // slots apart, its weights as two bf16 numbers. Every other weight is 2^(s_j - m) or
-// more. Queries become halves times a power of two a row (exact for values down to
-// 2^-17 of the row's largest).
+// more. Queries become halves times a power of two a row, exact for values down to
+// 2^-31 of the row's largest; rows with smaller ones are multiplied as bf16 numbers.
 // Roundings: weights to half, 2^-11 of a weight at most, or 2^-25 of the row's largest
 // 2^(s - m), whatever the values. A bf16 page's values may pass half's range, so there,
 // and in steps taken apart, a weight is the sum of two bf16 numbers (2^-16) in two
@@ -47,9 +47,9 @@
 //
 // Measured, replayed from a graph: 8 x 128K slots of 8 heads, D = 128, 8 bits 309 us,
 // 7.0 TB/s; 32 ragged sequences up to 8K slots, bf16 in pages of 16 109.5 us, 6.1 TB/s.
-// (Steps taken apart cost those that are not nothing in blocks of 8 rows; in blocks of
-// 16, whose registers are used up, 1 to 5 %: 8 x 32K slots of 4 heads, D = 128, 25 rows
-// 126 instead of 125 us; 8 x 64K of 8, D = 64, 16 rows 163 instead of 156.)
+// (Telling what has to be taken apart costs blocks of 8 rows nothing; blocks of 16, whose
+// registers are used up, 2 %: 8 x 32K slots of 4 heads, D = 128, 25 rows 127.4 us instead
+// of 124.8; 8 x 64K of 8, D = 64, 16 rows 159.8 instead of 155.7.)
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -130,7 +130,8 @@ struct Smem {
   static constexpr int kOut = kWarps * 8 * NT * D * 4;
   static constexpr int kData = kRing > kOut ? kRing : kOut;
   static constexpr int kMl = kData;                                // [2][kWarps][8 NT]
-  static constexpr int kFull = kMl + 2 * kWarps * 8 * NT * 4;      // [kStages]
+  static constexpr int kFar = kMl + 2 * kWarps * 8 * NT * 4;       // [2][kWarps][8 NT]
+  static constexpr int kFull = kFar + 2 * kWarps * 8 * NT * 4;     // [kStages]
   static constexpr int kFree = kFull + kStages * 8;                // [kStages]
   static constexpr int kGone = kFree + kStages * 8;                // [kStages] pages not there
   static constexpr int kAbort = kGone + kStages * 4;               // abort flag, then a 0
@@ -271,12 +272,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     // 16 k + 2 c, + 1, + 8, + 9 of step k; codes come four to a lane, 16 k + 4 c on
     uint32_t qf[NT][KS][2];
     float sl2[NT][2];                        // of rows 2c and 2c + 1
+    // 8 bits: rows with a value too small beside the largest for a half: what their values
+    // are multiplied by, 0 of the others, and where they lie, in rows of D (volatile: read
+    // where they are needed, and nothing of it kept in registers)
+    volatile float* far_down = reinterpret_cast<float*>(smem + S::kFar) + warp * RB;
+    volatile int* far_row = reinterpret_cast<int*>(smem + S::kFar) + (kWarps + warp) * RB;
+    bool any_far = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g;
       const bool row_ok = r < R;
-      const long long off =
-          row_ok ? ((long long)(sq.row0 + (r0 + r) / grp) * a.H_q + hk * grp + (r0 + r) % grp) * D : 0;
+      const int row = row_ok ? (sq.row0 + (r0 + r) / grp) * a.H_q + hk * grp + (r0 + r) % grp : 0;
+      const long long off = (long long)row * D;
       const bool ok = row_ok && in_range(off, D, (long long)a.rows * a.H_q * D, a.status);
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + off;
       if constexpr (kQuant) {
@@ -295,12 +302,25 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         // the largest value becomes 2^14 to 2^15
         const int e = max((int)(__float_as_uint(top) >> 23), 16);
         const float down = pow2_field(268 - e), up = pow2_field(e - 14);
+        bool lost = false;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          qf[nt][k][0] = pack_half2(__uint_as_float(u[k].x << 16) * down,
-                                    __uint_as_float(u[k].x & 0xffff0000u) * down);
-          qf[nt][k][1] = pack_half2(__uint_as_float(u[k].y << 16) * down,
-                                    __uint_as_float(u[k].y & 0xffff0000u) * down);
+          auto halves = [&](uint32_t x) -> uint32_t {
+            const float lo = __uint_as_float(x << 16) * down;
+            const float hi = __uint_as_float(x & 0xffff0000u) * down;
+            const uint32_t h = pack_half2(lo, hi);
+            const float2 back = half2_values(h);
+            lost |= back.x != lo || back.y != hi;
+            return h;
+          };
+          qf[nt][k][0] = halves(u[k].x);
+          qf[nt][k][1] = halves(u[k].y);
+        }
+        const bool far = (__ballot_sync(0xffffffffu, lost) >> (4 * g) & 15u) != 0;
+        any_far |= __any_sync(0xffffffffu, lost);
+        if (c == 0) {
+          far_down[r] = far ? down : 0.f;
+          far_row[r] = row;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -315,6 +335,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         sl2[nt][0] = sl2[nt][1] = a.scale_log2;
       }
     }
+    __syncwarp();
     // the position of row 2c + h; below 0: sees nothing
     auto pos = [&](int nt, int h) -> int {
       const int r = nt * 8 + 2 * c + h;
@@ -357,342 +378,391 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     };
     constexpr int kSteps = kQuant ? KS / 2 : KS, kPer = kQuant ? 2 : 1;
 
-    int stage = 0;
+    int stage = 0, it = 0, w0 = WS * warp;
     uint32_t phase = 0;
-    for (int it = 0; it < n_tiles; ++it) {
-      // most tiles have landed: one test, and the bounded wait only when not
-      if (!__all_sync(0xffffffffu, sm100::mbar_test_wait(full + 8 * stage, phase)) &&
-          !sm100::mbar_wait_warp(full + 8 * stage, phase, abort_flag, kTimeoutNs))
-        break;
-      const uint32_t tile = ring + stage * S::kStage;
-      const uint32_t missing = gone[stage];
-      const int box_rows = min(a.p.page, kTile), box_shift = 31 - __clz(box_rows);
-      // 16 slots at a time, in a loop that is not unrolled: code that a short call runs
-      // once or twice costs it more to fetch than to run (two at a time side by side:
-      // 31 instead of 25 us for 4 x 4 tokens under a window of 4096, and no less for 8
-      // x 128K slots)
+    // The walk over the tiles, of 8-bit pages in two forms: the plain one stops (true) before
+    // the first step in which a row has to be taken apart, and the other goes on from there;
+    // queries with far smaller values begin with it. (One loop with both: what it
+    // never runs costs it registers, blocks of 16 rows 2 to 6 %.)
+    auto walk = [&](auto both) -> bool {
+      constexpr bool kBoth = decltype(both)::value;
+      for (; it < n_tiles; ++it) {
+        // most tiles have landed: one test, and the bounded wait only when not
+        if (!__all_sync(0xffffffffu, sm100::mbar_test_wait(full + 8 * stage, phase)) &&
+            !sm100::mbar_wait_warp(full + 8 * stage, phase, abort_flag, kTimeoutNs))
+          return false;
+        const uint32_t tile = ring + stage * S::kStage;
+        const uint32_t missing = gone[stage];
+        const int box_rows = min(a.p.page, kTile), box_shift = 31 - __clz(box_rows);
+        // 16 slots at a time, in a loop that is not unrolled: code that a short call runs
+        // once or twice costs it more to fetch than to run (two at a time side by side:
+        // 31 instead of 25 us for 4 x 4 tokens under a window of 4096, and no less for 8
+        // x 128K slots)
 #pragma unroll 1
-      for (int w0 = WS * warp; w0 < WS * (warp + 1); w0 += 16) {
-        const int j0 = sp.tile(v_begin + it) * kTile + w0;
-        // where the first row of 16 lies, of the keys; from one part of it to the next
-        const uint32_t rows =
-            tile + (uint32_t)((w0 & ~(box_rows - 1)) * S::kParts * S::kRowBytes +
-                              (w0 & (box_rows - 1)) * S::kRowBytes);
-        const uint32_t next_part = (uint32_t)(box_rows * S::kRowBytes);
-        // ---- scores: rows of s are slots, columns query rows
-        float s[NT][4];
-        float ev[2];                     // the value scales' exponents
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-        if constexpr (kQuant) {
-          float ks[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint8_t* at = smem + stage * S::kStage + w0 + 8 * i + g;
-            ks[i] = pow2_byte(at[S::kKs]);
-            ev[i] = (float)((int)at[S::kVs] - 127);
-          }
-#pragma unroll
-          for (int x = 0; x < KS / 2; ++x) {   // two chunks of 16 dimensions
-            uint32_t w[4];
-            ldmatrix4(w, rows + swizzled<S::kRowBytes>(lane & 15, 2 * x + (lane >> 4)));
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t af[4] = {e4m3x2_half2(w[2 * y]), e4m3x2_half2(w[2 * y + 1]),
-                                      e4m3x2_half2(w[2 * y] >> 16),
-                                      e4m3x2_half2(w[2 * y + 1] >> 16)};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816<true>(s[nt], af, qf[nt][2 * x + y][0], qf[nt][2 * x + y][1]);
-            }
-          }
+        for (; w0 < WS * (warp + 1); w0 += 16) {
+          const int j0 = sp.tile(v_begin + it) * kTile + w0;
+          // where the first row of 16 lies, of the keys; from one part of it to the next
+          const uint32_t rows =
+              tile + (uint32_t)((w0 & ~(box_rows - 1)) * S::kParts * S::kRowBytes +
+                                (w0 & (box_rows - 1)) * S::kRowBytes);
+          const uint32_t next_part = (uint32_t)(box_rows * S::kRowBytes);
+          // ---- scores: rows of s are slots, columns query rows
+          float s[NT][4];
+          float ev[2];                     // the value scales' exponents
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[nt][i] *= ks[i >> 1] * sl2[nt][i & 1];
-        } else {
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            uint32_t af[4];
-            ldmatrix4(af, rows + (k / 4) * next_part +
-                              swizzled<S::kRowBytes>(lane & 15, 2 * (k % 4) + (lane >> 4)));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816<false>(s[nt], af, qf[nt][k][0], qf[nt][k][1]);
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[nt][i] *= sl2[nt][i & 1];
-        }
-        // ---- slots that some row does not see
-        const bool whole = missing == 0 && sp.whole(a, j0, 16);
-        auto lost = [&](int x) { return (missing >> ((w0 + x) >> box_shift) & 1u) != 0; };
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int x = 8 * i + g;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (lost(x) || !paged_sees(a, pos(nt, h), j0 + x)) s[nt][2 * i + h] = -INFINITY;
-          }
-        }
-        // the halves of slots 2c, 2c + 1, and + 8 to keep: those that the row at p, or
-        // (kAny) any row, sees
-        constexpr int kAny = -1;
-        auto keep_slots = [&](int p, uint32_t (&keep)[2]) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            keep[i] = 0;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int x = 8 * i + 2 * c + y;
-              const bool see = p == kAny ? j0 + x < sp.hi && sp.meets(a, j0 + x, 1)
-                                         : paged_sees(a, p, j0 + x);
-              if (see && !lost(x)) keep[i] |= 0xffffu << (16 * y);
-            }
-          }
-        };
-        // the operand of 16 slots and of 16 dimensions (8 bits: two steps' at once)
-        auto load_values = [&](int k, uint32_t (&af)[kPer][4]) {
+            for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
           if constexpr (kQuant) {
-            uint32_t w[4];
-            ldmatrix4_trans(w, rows + S::kKv +
-                                   swizzled<S::kRowBytes>(lane & 15, 2 * k + (lane >> 4)));
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              // bytes: (slot 2c, dimensions 2g, 2g + 1), (slot 2c + 1, the same)
-              const uint32_t lo = __byte_perm(w[2 * y], 0, 0x3120);
-              const uint32_t hi = __byte_perm(w[2 * y + 1], 0, 0x3120);
-              af[y][0] = e4m3x2_half2(lo);
-              af[y][1] = e4m3x2_half2(lo >> 16);
-              af[y][2] = e4m3x2_half2(hi);
-              af[y][3] = e4m3x2_half2(hi >> 16);
-            }
-          } else {
-            const int row = (lane & 7) + ((lane & 16) >> 1);
-            ldmatrix4_trans(af[0], rows + S::kKv + (k / 4) * next_part +
-                                       swizzled<S::kRowBytes>(row, 2 * (k % 4) + ((lane >> 3) & 1)));
-          }
-        };
-        auto mask = [&](const uint32_t (&keep)[2], uint32_t (&af)[kPer][4]) {
-#pragma unroll
-          for (int x = 0; x < kPer; ++x)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) af[x][i] &= keep[i >> 1];
-        };
-        // ---- raise the maxima when a score passes its bound: rare after the first tile
-        float top[NT][2], top2[NT][2];
-        bool raise = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            top[nt][h] = top2[nt][h] = -INFINITY;
+            float ks[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              top[nt][h] = fmaxf(top[nt][h], s[nt][2 * i + h]);
-              if (kQuant) top2[nt][h] = fmaxf(top2[nt][h], s[nt][2 * i + h] + ev[i]);
+              const uint8_t* at = smem + stage * S::kStage + w0 + 8 * i + g;
+              ks[i] = pow2_byte(at[S::kKs]);
+              ev[i] = (float)((int)at[S::kVs] - 127);
             }
-            raise |= top[nt][h] > sub[nt][h] + kRescaleLog2;
-            if (kQuant) raise |= top2[nt][h] > sub2[nt][h] + (kRescaleLog2 + kHalfUp);
+#pragma unroll
+            for (int x = 0; x < KS / 2; ++x) {   // two chunks of 16 dimensions
+              uint32_t w[4];
+              ldmatrix4(w, rows + swizzled<S::kRowBytes>(lane & 15, 2 * x + (lane >> 4)));
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t af[4] = {e4m3x2_half2(w[2 * y]), e4m3x2_half2(w[2 * y + 1]),
+                                        e4m3x2_half2(w[2 * y] >> 16),
+                                        e4m3x2_half2(w[2 * y + 1] >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma16816<true>(s[nt], af, qf[nt][2 * x + y][0], qf[nt][2 * x + y][1]);
+              }
+            }
+            if (kBoth && any_far) {
+              // those rows' products anew: values and codes as bf16 numbers, both exact
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float down = far_down[nt * 8 + g];
+                const uint2* q = reinterpret_cast<const uint2*>(
+                    static_cast<const __nv_bfloat16*>(a.q) + (long long)far_row[nt * 8 + g] * D);
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int x = 0; x < KS / 2; ++x) {
+                  uint32_t w[4];
+                  ldmatrix4(w, rows + swizzled<S::kRowBytes>(lane & 15, 2 * x + (lane >> 4)));
+#pragma unroll
+                  for (int y = 0; y < 2; ++y) {
+                    const uint2 u = down > 0.f ? q[4 * (2 * x + y) + c] : make_uint2(0, 0);
+                    auto times = [&](uint32_t v) -> uint32_t {
+                      return sm100::pack_bf16x2(__uint_as_float(v << 16) * down,
+                                                __uint_as_float(v & 0xffff0000u) * down);
+                    };
+                    auto bf16 = [](uint32_t codes) -> uint32_t {
+                      const float2 f = half2_values(e4m3x2_half2(codes));
+                      return sm100::pack_bf16x2(f.x, f.y);
+                    };
+                    const uint32_t af[4] = {bf16(w[2 * y]), bf16(w[2 * y + 1]),
+                                            bf16(w[2 * y] >> 16), bf16(w[2 * y + 1] >> 16)};
+                    mma16816<false>(t, af, times(u.x), times(u.y));
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (far_down[nt * 8 + 2 * c + (i & 1)] > 0.f) s[nt][i] = t[i];
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[nt][i] *= ks[i >> 1] * sl2[nt][i & 1];
+          } else {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              uint32_t af[4];
+              ldmatrix4(af, rows + (k / 4) * next_part +
+                                swizzled<S::kRowBytes>(lane & 15, 2 * (k % 4) + (lane >> 4)));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816<false>(s[nt], af, qf[nt][k][0], qf[nt][k][1]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[nt][i] *= sl2[nt][i & 1];
           }
-        if (kQuant) raise |= fminf(ev[0], ev[1]) < low;
-        if (__any_sync(0xffffffffu, raise)) {
-          low = -INFINITY;
+          // ---- slots that some row does not see
+          const bool whole = missing == 0 && sp.whole(a, j0, 16);
+          auto lost = [&](int x) { return (missing >> ((w0 + x) >> box_shift) & 1u) != 0; };
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int x = 8 * i + g;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (lost(x) || !paged_sees(a, pos(nt, h), j0 + x)) s[nt][2 * i + h] = -INFINITY;
+            }
+          }
+          // the halves of slots 2c, 2c + 1, and + 8 to keep: those that the row at p, or
+          // (kAny) any row, sees
+          constexpr int kAny = -1;
+          auto keep_slots = [&](int p, uint32_t (&keep)[2]) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              keep[i] = 0;
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int x = 8 * i + 2 * c + y;
+                const bool see = p == kAny ? j0 + x < sp.hi && sp.meets(a, j0 + x, 1)
+                                           : paged_sees(a, p, j0 + x);
+                if (see && !lost(x)) keep[i] |= 0xffffu << (16 * y);
+              }
+            }
+          };
+          // the operand of 16 slots and of 16 dimensions (8 bits: two steps' at once)
+          auto load_values = [&](int k, uint32_t (&af)[kPer][4]) {
+            if constexpr (kQuant) {
+              uint32_t w[4];
+              ldmatrix4_trans(w, rows + S::kKv +
+                                     swizzled<S::kRowBytes>(lane & 15, 2 * k + (lane >> 4)));
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                // bytes: (slot 2c, dimensions 2g, 2g + 1), (slot 2c + 1, the same)
+                const uint32_t lo = __byte_perm(w[2 * y], 0, 0x3120);
+                const uint32_t hi = __byte_perm(w[2 * y + 1], 0, 0x3120);
+                af[y][0] = e4m3x2_half2(lo);
+                af[y][1] = e4m3x2_half2(lo >> 16);
+                af[y][2] = e4m3x2_half2(hi);
+                af[y][3] = e4m3x2_half2(hi >> 16);
+              }
+            } else {
+              const int row = (lane & 7) + ((lane & 16) >> 1);
+              const int chunk = 2 * (k % 4) + ((lane >> 3) & 1);
+              ldmatrix4_trans(af[0], rows + S::kKv + (k / 4) * next_part +
+                                         swizzled<S::kRowBytes>(row, chunk));
+            }
+          };
+          auto mask = [&](const uint32_t (&keep)[2], uint32_t (&af)[kPer][4]) {
+#pragma unroll
+            for (int x = 0; x < kPer; ++x)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) af[x][i] &= keep[i >> 1];
+          };
+          // ---- raise the maxima when a score passes its bound: rare after the first tile
+          float top[NT][2], top2[NT][2];
+          bool raise = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              // (to x rounded down, less `up`); what sums are multiplied by
-              auto raise_to = [&](float x, float up, float& sub_) -> float {
-                if (!(x > sub_ + (kRescaleLog2 + up))) return 1.f;
-                const float to = floorf(x) - up;
-                const float alpha = sub_ == -INFINITY ? 0.f : exp2f(sub_ - to);
-                sub_ = to;
-                return alpha;
-              };
-              const float alpha = raise_to(row_max(top[nt][h]), 0.f, sub[nt][h]);
-              l[nt][h] *= alpha;
-              scale_row(nt, h,
-                        kQuant ? raise_to(row_max(top2[nt][h]), kHalfUp, sub2[nt][h]) : alpha);
-              if (kQuant) low = fmaxf(low, sub2[nt][h] - sub[nt][h]);    // (NaN: nothing seen)
+              top[nt][h] = top2[nt][h] = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                top[nt][h] = fmaxf(top[nt][h], s[nt][2 * i + h]);
+                if (kQuant) top2[nt][h] = fmaxf(top2[nt][h], s[nt][2 * i + h] + ev[i]);
+              }
+              raise |= top[nt][h] > sub[nt][h] + kRescaleLog2;
+              if (kQuant) raise |= top2[nt][h] > sub2[nt][h] + (kRescaleLog2 + kHalfUp);
             }
-          // the rows (bit 2 nt + h) that have met too much for a slot that they see, as all
-          // lanes that hold the row know
-          uint32_t wide = 0;
-          if (kQuant && __any_sync(0xffffffffu, fminf(ev[0], ev[1]) < low)) {
+          if (kQuant) raise |= fminf(ev[0], ev[1]) < low;
+          if (__any_sync(0xffffffffu, raise)) {
+            low = -INFINITY;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                bool far = false;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  far |= s[nt][2 * i + h] > -INFINITY && ev[i] < sub2[nt][h] - sub[nt][h];
-                uint32_t of_c = __ballot_sync(0xffffffffu, far);
-                of_c |= of_c >> 16;
-                of_c |= of_c >> 8;
-                of_c |= of_c >> 4;
-                wide |= (of_c >> c & 1u) << (2 * nt + h);
+                // (to x rounded down, less `up`); what sums are multiplied by
+                auto raise_to = [&](float x, float up, float& sub_) -> float {
+                  if (!(x > sub_ + (kRescaleLog2 + up))) return 1.f;
+                  const float to = floorf(x) - up;
+                  const float alpha = sub_ == -INFINITY ? 0.f : exp2f(sub_ - to);
+                  sub_ = to;
+                  return alpha;
+                };
+                const float alpha = raise_to(row_max(top[nt][h]), 0.f, sub[nt][h]);
+                l[nt][h] *= alpha;
+                scale_row(nt, h,
+                          kQuant ? raise_to(row_max(top2[nt][h]), kHalfUp, sub2[nt][h]) : alpha);
+                if (kQuant) low = fmaxf(low, sub2[nt][h] - sub[nt][h]);    // (NaN: nothing seen)
               }
-          }
-          if (kQuant && __any_sync(0xffffffffu, wide)) {
-            // Rows to which a slot's value scale is too small for a half's range: their
-            // products of this step, weights in two bf16 numbers, codes in one (exact). What
-            // follows finds them without scores: weights of 0, which NaN codes, here left to
-            // it, make NaN.
+            // the rows (bit 2 nt + h) that have met too much for a slot that they see, as all
+            // lanes that hold the row know
+            uint32_t wide = 0;
+            if (kQuant && __any_sync(0xffffffffu, fminf(ev[0], ev[1]) < low)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              uint32_t wh[2], wl[2];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float w[2] = {0.f, 0.f};
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  float& x = s[nt][2 * i + h];
-                  if (wide >> (2 * nt + h) & 1u) {
-                    l[nt][h] += sm100::ex2_approx(x - sub[nt][h]);
-                    w[h] = sm100::ex2_approx(x + (ev[i] - sub2[nt][h]));
-                    x = -INFINITY;
+                  bool far = false;
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    far |= s[nt][2 * i + h] > -INFINITY && ev[i] < sub2[nt][h] - sub[nt][h];
+                  uint32_t of_c = __ballot_sync(0xffffffffu, far);
+                  of_c |= of_c >> 16;
+                  of_c |= of_c >> 8;
+                  of_c |= of_c >> 4;
+                  wide |= (of_c >> c & 1u) << (2 * nt + h);
+                }
+            }
+            if (!kBoth && __any_sync(0xffffffffu, wide)) return true;
+            if (kBoth && __any_sync(0xffffffffu, wide)) {
+              // Rows to which a slot's value scale is too small for a half's range: their
+              // products of this step, weights in two bf16 numbers, codes in one (exact). What
+              // follows finds them without scores: weights of 0, which NaN codes, here left to
+              // it, make NaN.
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                uint32_t wh[2], wl[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  float w[2] = {0.f, 0.f};
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    float& x = s[nt][2 * i + h];
+                    if (wide >> (2 * nt + h) & 1u) {
+                      l[nt][h] += sm100::ex2_approx(x - sub[nt][h]);
+                      w[h] = sm100::ex2_approx(x + (ev[i] - sub2[nt][h]));
+                      x = -INFINITY;
+                    }
+                  }
+                  const uint32_t u = sm100::pack_bf16x2(w[0], w[1]);
+                  wh[i] = transpose8x8(u);
+                  wl[i] = transpose8x8(sm100::pack_bf16x2(
+                      w[0] - __uint_as_float(u << 16), w[1] - __uint_as_float(u & 0xffff0000u)));
+                }
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                  uint32_t af[kPer][4];
+                  load_values(k, af);
+#pragma unroll
+                  for (int x = 0; x < kPer; ++x) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      const float2 f = half2_values(af[x][i]);
+                      af[x][i] = sm100::pack_bf16x2(f.x == f.x ? f.x : 0.f, f.y == f.y ? f.y : 0.f);
+                    }
+                    mma16816<false>(o[nt][kPer * k + x], af[x], wh[0], wh[1]);
+                    mma16816<false>(o[nt][kPer * k + x], af[x], wl[0], wl[1]);
                   }
                 }
+              }
+            }
+          }
+          // ---- weights, as B operands: one half, or two bf16 numbers, what the first
+          // leaves being the second
+          uint32_t pf[NT][2], pl[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            // (a row that has seen nothing has scores of -inf alone)
+            const float less[2] = {fmaxf(sub[nt][0], -FLT_MAX), fmaxf(sub[nt][1], -FLT_MAX)};
+            const float less2[2] = {fmaxf(sub2[nt][0], -FLT_MAX), fmaxf(sub2[nt][1], -FLT_MAX)};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float w[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float x = s[nt][2 * i + h];
+                const float p = sm100::ex2_approx(x - less[h]);
+                l[nt][h] += p;
+                w[h] = kQuant ? sm100::ex2_approx(x + (ev[i] - less2[h])) : p;
+              }
+              if constexpr (kQuant) {
+                pf[nt][i] = transpose8x8(pack_half2(w[0], w[1]));
+              } else {
                 const uint32_t u = sm100::pack_bf16x2(w[0], w[1]);
-                wh[i] = transpose8x8(u);
-                wl[i] = transpose8x8(sm100::pack_bf16x2(
+                pf[nt][i] = transpose8x8(u);
+                pl[nt][i] = transpose8x8(sm100::pack_bf16x2(
                     w[0] - __uint_as_float(u << 16), w[1] - __uint_as_float(u & 0xffff0000u)));
               }
-#pragma unroll
-              for (int k = 0; k < kSteps; ++k) {
-                uint32_t af[kPer][4];
-                load_values(k, af);
-#pragma unroll
-                for (int x = 0; x < kPer; ++x) {
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const float2 f = half2_values(af[x][i]);
-                    af[x][i] = sm100::pack_bf16x2(f.x == f.x ? f.x : 0.f, f.y == f.y ? f.y : 0.f);
-                  }
-                  mma16816<false>(o[nt][kPer * k + x], af[x], wh[0], wh[1]);
-                  mma16816<false>(o[nt][kPer * k + x], af[x], wl[0], wl[1]);
-                }
-              }
             }
           }
-        }
-        // ---- weights, as B operands: one half, or two bf16 numbers, what the first
-        // leaves being the second
-        uint32_t pf[NT][2], pl[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          // (a row that has seen nothing has scores of -inf alone)
-          const float less[2] = {fmaxf(sub[nt][0], -FLT_MAX), fmaxf(sub[nt][1], -FLT_MAX)};
-          const float less2[2] = {fmaxf(sub2[nt][0], -FLT_MAX), fmaxf(sub2[nt][1], -FLT_MAX)};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float w[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float x = s[nt][2 * i + h];
-              const float p = sm100::ex2_approx(x - less[h]);
-              l[nt][h] += p;
-              w[h] = kQuant ? sm100::ex2_approx(x + (ev[i] - less2[h])) : p;
-            }
-            if constexpr (kQuant) {
-              pf[nt][i] = transpose8x8(pack_half2(w[0], w[1]));
-            } else {
-              const uint32_t u = sm100::pack_bf16x2(w[0], w[1]);
-              pf[nt][i] = transpose8x8(u);
-              pl[nt][i] = transpose8x8(sm100::pack_bf16x2(
-                  w[0] - __uint_as_float(u << 16), w[1] - __uint_as_float(u & 0xffff0000u)));
-            }
-          }
-        }
-        // ---- their products with the values: rows of o are dimensions
-        auto multiply = [&](float (&acc)[4], const uint32_t (&af)[4], int nt) {
-          mma16816<kQuant>(acc, af, pf[nt][0], pf[nt][1]);
-          if (!kQuant) mma16816<kQuant>(acc, af, pl[nt][0], pl[nt][1]);
-        };
-        if (whole) {
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            uint32_t af[kPer][4];
-            load_values(k, af);
-#pragma unroll
-            for (int x = 0; x < kPer; ++x)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) multiply(o[nt][kPer * k + x], af[x], nt);
-          }
-        } else {
-          // where tokens differ in what they see, a value that is not finite would reach
-          // the rows that do not see it
-          bool apart = false;
-          if (sp.pmin != sp.pmax) {
-            uint32_t keep[2];
-            keep_slots(kAny, keep);
-#pragma unroll 1
-            for (int k = 0; k < kSteps; ++k) {
-              uint32_t af[kPer][4];
-              load_values(k, af);
-              mask(keep, af);
-              constexpr uint32_t ones = kQuant ? 0x7c007c00u : 0x7f807f80u;   // exponents
-#pragma unroll
-              for (int x = 0; x < kPer; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t u = af[x][i] & ones;
-                  apart |= (u & 0xffffu) == (ones & 0xffffu) || (u >> 16) == (ones >> 16);
-                }
-            }
-            apart = __any_sync(0xffffffffu, apart);
-          }
-          if (!apart) {
-            uint32_t keep[2];
-            keep_slots(kAny, keep);
+          // ---- their products with the values: rows of o are dimensions
+          auto multiply = [&](float (&acc)[4], const uint32_t (&af)[4], int nt) {
+            mma16816<kQuant>(acc, af, pf[nt][0], pf[nt][1]);
+            if (!kQuant) mma16816<kQuant>(acc, af, pl[nt][0], pl[nt][1]);
+          };
+          if (whole) {
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
               uint32_t af[kPer][4];
               load_values(k, af);
-              mask(keep, af);
 #pragma unroll
               for (int x = 0; x < kPer; ++x)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) multiply(o[nt][kPer * k + x], af[x], nt);
             }
-          }
-          for (int p = max(sp.pmin, 0); apart && p <= sp.pmax; ++p) {
-            uint32_t keep[2];
-            keep_slots(p, keep);
+          } else {
+            // where tokens differ in what they see, a value that is not finite would reach
+            // the rows that do not see it
+            bool apart = false;
+            if (sp.pmin != sp.pmax) {
+              uint32_t keep[2];
+              keep_slots(kAny, keep);
+#pragma unroll 1
+              for (int k = 0; k < kSteps; ++k) {
+                uint32_t af[kPer][4];
+                load_values(k, af);
+                mask(keep, af);
+                constexpr uint32_t ones = kQuant ? 0x7c007c00u : 0x7f807f80u;   // exponents
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-              uint32_t af[kPer][4];
-              load_values(k, af);
-              mask(keep, af);
+                for (int x = 0; x < kPer; ++x)
 #pragma unroll
-              for (int x = 0; x < kPer; ++x)
+                  for (int i = 0; i < 4; ++i) {
+                    const uint32_t u = af[x][i] & ones;
+                    apart |= (u & 0xffffu) == (ones & 0xffffu) || (u >> 16) == (ones >> 16);
+                  }
+              }
+              apart = __any_sync(0xffffffffu, apart);
+            }
+            if (!apart) {
+              uint32_t keep[2];
+              keep_slots(kAny, keep);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  float(&acc)[4] = o[nt][kPer * k + x];
-                  float y[4] = {acc[0], acc[1], acc[2], acc[3]};
-                  multiply(y, af[x], nt);
+              for (int k = 0; k < kSteps; ++k) {
+                uint32_t af[kPer][4];
+                load_values(k, af);
+                mask(keep, af);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    if (pos(nt, i & 1) == p) acc[i] = y[i];
-                }
+                for (int x = 0; x < kPer; ++x)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) multiply(o[nt][kPer * k + x], af[x], nt);
+              }
+            }
+            for (int p = max(sp.pmin, 0); apart && p <= sp.pmax; ++p) {
+              uint32_t keep[2];
+              keep_slots(p, keep);
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k) {
+                uint32_t af[kPer][4];
+                load_values(k, af);
+                mask(keep, af);
+#pragma unroll
+                for (int x = 0; x < kPer; ++x)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    float(&acc)[4] = o[nt][kPer * k + x];
+                    float y[4] = {acc[0], acc[1], acc[2], acc[3]};
+                    multiply(y, af[x], nt);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                      if (pos(nt, i & 1) == p) acc[i] = y[i];
+                  }
+              }
             }
           }
         }
+        w0 = WS * warp;
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(free_ + 8 * stage);
+        if (++stage == S::kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
-      __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(free_ + 8 * stage);
-      if (++stage == S::kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
+      return false;
+    };
+    if constexpr (kQuant) {
+      if (any_far || walk(std::false_type())) walk(std::true_type());
+    } else {
+      walk(std::false_type());
     }
     __syncthreads();                         // every warp has read the ring
 

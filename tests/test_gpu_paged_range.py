@@ -166,3 +166,26 @@ def test_not_a_number_beside_a_far_larger_value(T, group, where):
     assert bool(got[:, T - seen:, :, 9].isnan().all())
     got[:, T - seen:, :, 9] = out[:, T - seen:, :, 9]
     assert torch.equal(got, out)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,group", ROWS)
+@pytest.mark.parametrize("power", [20, 40, 100])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_far_larger_query_value(kind, T, group, power, D):
+    """A query's one value of 2^power meets keys that are 0 there: the scores come from
+    the others, those of the rows beside it as before, to the bit."""
+    n, H = 300, 2
+    g = torch.Generator().manual_seed(power + T)
+    k, v = (torch.randn(n, H, D, generator=g) for _ in range(2))
+    k[..., 5] = 0.0
+    q = torch.randn(T, H * group, D, generator=g).to(torch.bfloat16)
+    cache, table = filled(kind, k, v)
+    before, before_l = binding.paged_attn(q[None].to(DEV), cache, table, ints([n]))
+    q[::2, ::3, 5] = 2.0 ** power
+    compare(kind, cache, table, q, n)
+    after, after_l = binding.paged_attn(q[None].to(DEV), cache, table, ints([n]))
+    same = torch.ones(T, H * group, dtype=torch.bool)
+    same[::2, ::3] = False
+    assert torch.equal(after[0][same], before[0][same])
+    assert torch.equal(after_l[0].T[same], before_l[0].T[same])
