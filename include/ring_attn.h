@@ -687,9 +687,12 @@ ra_status paged_attn_workspace(const ra_pages* pages, int B, int S_q, int total,
  * A row's results depend on the slots that it sees alone, to the bit, whatever the
  * others hold (slots past lens[b], behind the windows, later tokens' slots): NaN and
  * infinities included. A value that is not finite makes its own dimension of the rows
- * that see it NaN or infinite. A slot whose page is not there is not seen, and sets
- * RA_ERR_RANGE in `dev_status` where a row would have seen it; pages that every window
- * has left behind may be taken out of the table.
+ * that see it infinite with its sign, or NaN if it is NaN, if there are infinities of
+ * both signs, or (possibly) where the slot's weight is below 2^-100 of the row's
+ * largest. Finite values of up to 2^88 in magnitude (beyond them results may be
+ * infinite). A slot whose page is not there is not seen, and sets RA_ERR_RANGE in
+ * `dev_status` where a row would have seen it; pages that every window has left behind
+ * may be taken out of the table.
  * dtype RA_BF16. scale <= 0 means 1 / sqrt(D). The workspace is the caller's,
  * 16-byte aligned; its contents do not matter. Calls that may overlap on the GPU
  * need workspaces of their own. Results repeat bit for bit.

@@ -667,7 +667,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
               if constexpr (kQuant) {
                 pf[nt][i] = transpose8x8(pack_half2(w[0], w[1]));
               } else {
-                const uint32_t u = sm100::pack_bf16x2(w[0], w[1]);
+                // the first below the weight, so that both are above 0, and infinite values
+                // times both keep their sign
+                const uint32_t b0 = max(__float_as_uint(w[0]), 1u) - 1u;
+                const uint32_t b1 = max(__float_as_uint(w[1]), 1u) - 1u;
+                const uint32_t u = __byte_perm(b0, b1, 0x7632);
                 pf[nt][i] = transpose8x8(u);
                 pl[nt][i] = transpose8x8(sm100::pack_bf16x2(
                     w[0] - __uint_as_float(u << 16), w[1] - __uint_as_float(u & 0xffff0000u)));

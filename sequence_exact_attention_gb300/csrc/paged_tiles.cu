@@ -89,11 +89,11 @@ struct Cfg {
   static constexpr int kRedOff = kBarOff + kBarBytes;
   static constexpr int kRedBytes = (512 + 512) * 4;
   // values that are not finite, of tiles that rows differ in: a bit each, [kEdges][128
-  // slots][D / 32]. The block's 256 positions make at most three such tiles at each end
+  // slots][2][D / 32], first infinity or NaN, then minus infinity or NaN. The block's 256 positions make at most three such tiles at each end
   // of a window, the first slots' last tile one more.
   static constexpr int kEdges = 7;
   static constexpr int kOddOff = kRedOff + kRedBytes;
-  static constexpr int kOddBytes = kEdges * kTile * (D / 32) * 4;
+  static constexpr int kOddBytes = kEdges * kTile * 2 * (D / 32) * 4;
   static constexpr int kUsed = kOddOff + kOddBytes + 1024;   // + alignment slack
   // more than half an SM's shared memory: one CTA an SM, so the allocation of all
   // tensor memory never waits for another CTA
@@ -119,10 +119,10 @@ struct Cfg {
   static_assert(kOCol + 2 * D <= kTmemCols, "tensor memory budget");
 };
 
-// Notes the values of a tile's rows [from, to) that are not finite, but not those of
-// rows [skip_from, skip_to), in `odd` [128][D / 32] and makes them 0: a row that does
-// not see them has the weight 0 for them. By the checking threads.
-// Says whether this thread found any.
+// Notes the values of a tile's first `to` rows that are not finite, but not those of rows
+// [skip_from, skip_to), in `odd` and makes them 0: a row that does
+// not see them has the weight 0 for them. (`odd`: a tile's part of Cfg::kOddOff.) By the
+// checking threads. Says whether this thread found any.
 template <int D>
 __device__ __forceinline__ bool take_odd_values(uint8_t* tile, int to, int skip_from, int skip_to,
                                                 uint32_t* odd, int thread) {
@@ -144,22 +144,22 @@ __device__ __forceinline__ bool take_odd_values(uint8_t* tile, int to, int skip_
     if (row >= to || (row >= skip_from && row < skip_to)) continue;
     uint4* at = reinterpret_cast<uint4*>(tile) + i;
     const uint4 v = *at;
-    uint32_t w[4] = {v.x, v.y, v.z, v.w}, bits = 0;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, up = 0, down = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t e = w[k] & kOnes;
-      if ((e & 0xffffu) == (kOnes & 0xffffu)) {
-        bits |= 1u << (2 * k);
-        w[k] &= 0xffff0000u;
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t u = w[k] >> (16 * y) & 0xffffu;
+        if ((u & 0x7f80u) != 0x7f80u) continue;
+        if (u != 0xff80u) up |= 1u << (2 * k + y);           // infinity or NaN
+        if (u != 0x7f80u) down |= 1u << (2 * k + y);         // minus infinity or NaN
+        w[k] &= y ? 0x0000ffffu : 0xffff0000u;
       }
-      if ((e >> 16) == (kOnes >> 16)) {
-        bits |= 2u << (2 * k);
-        w[k] &= 0x0000ffffu;
-      }
-    }
-    if (bits) {
+    if (up | down) {
       *at = make_uint4(w[0], w[1], w[2], w[3]);
-      atomicOr(odd + row * (D / 32) + chunk / 4, bits << (8 * (chunk % 4)));
+      uint32_t* to_bits = odd + row * (2 * (D / 32)) + chunk / 4;
+      atomicOr(to_bits, up << (8 * (chunk % 4)));
+      atomicOr(to_bits + D / 32, down << (8 * (chunk % 4)));
       noted = true;
     }
   }
@@ -444,7 +444,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
         if (z0 < z1) zero_rows(smem_u32(tile), C::kBoxes, z0, z1, thread);
         if (z2 < kTile) zero_rows(smem_u32(tile), C::kBoxes, z2, kTile, thread);
         if (n_edges < C::kEdges) {
-          found |= take_odd_values<D>(tile, z2, z0, z1, odd + n_edges * kTile * (D / 32), thread);
+          found |= take_odd_values<D>(tile, z2, z0, z1, odd + n_edges * kTile * 2 * (D / 32),
+                                      thread);
           if (thread == 0) edge_lo[n_edges] = lo;
           ++n_edges;
         }
@@ -580,14 +581,17 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
       const long long orow = (long long)(sq.row0 + t) * a.H_q + h;
       const uint32_t tO = tmem + t_lane + kOCol + (uint32_t)(qi * D + part * (D / 2));
       const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);   // 0: no slot; NaN stays
-      // this part's dimensions in which the row sees a value that is not finite
-      uint32_t bad[D / 64] = {};
+      // this part's dimensions in which the row sees an infinity or NaN, and the other one
+      uint32_t up[D / 64] = {}, down[D / 64] = {};
       if (*any_odd) {
         const int q_pos = first + qi * tt + tok;
         for (int i = 0; i < *any_odd * kTile; ++i) {
           if (!paged_sees(a, q_pos, edge_lo[i / kTile] + i % kTile)) continue;
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) bad[c] |= odd[i * (D / 32) + part * (D / 64) + c];
+          for (int c = 0; c < D / 64; ++c) {
+            up[c] |= odd[2 * i * (D / 32) + part * (D / 64) + c];
+            down[c] |= odd[(2 * i + 1) * (D / 32) + part * (D / 64) + c];
+          }
         }
       }
       const long long prow = paged_part(a, work.item, work.split, qi * kTile + row);
@@ -610,10 +614,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
           for (int i = 0; i < 32; ++i) uo[i] = 0u;
         }
-        if (bad[c]) {
+        if (up[c] | down[c]) {                   // infinities of both signs: NaN
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (bad[c] >> i & 1u) uo[i] = 0x7fc00000u;
+          for (int i = 0; i < 32; ++i) {
+            if (up[c] >> i & 1u) uo[i] = __float_as_uint(__uint_as_float(uo[i]) + INFINITY);
+            if (down[c] >> i & 1u) uo[i] = __float_as_uint(__uint_as_float(uo[i]) - INFINITY);
+          }
         }
         if (whole) {
 #pragma unroll

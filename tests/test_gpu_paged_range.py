@@ -189,3 +189,37 @@ def test_one_far_larger_query_value(kind, T, group, power, D):
     same[::2, ::3] = False
     assert torch.equal(after[0][same], before[0][same])
     assert torch.equal(after_l[0].T[same], before_l[0].T[same])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,group", [(1, 1), (4, 2), (12, 1), (40, 4), (300, 1)])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (120, 3)])
+def test_infinite_values_keep_their_sign(D, T, group, window, n_sink):
+    """bf16 pages: a value of infinity makes its dimension of the rows that see it infinite
+    with its sign, and both signs, or a NaN, make it NaN: in whole tiles of slots, at a
+    window's edges and among the new tokens, in calls of any size."""
+    n = 700
+    g = torch.Generator().manual_seed(T)
+    k, v = (torch.randn(n, 1, D, generator=g) for _ in range(2))
+    kw = dict(window=window, n_sink=n_sink)
+    q = torch.randn(1, T, group, D, generator=g).to(torch.bfloat16).to(DEV)
+    cache, table = filled("bf16", k, v)
+    out, lse = binding.paged_attn(q, cache, table, ints([n]), **kw)
+    bad = [(at, d, x) for at in (1, 100, 300, 450, n - T - 60, n - T, n - 2, n - 1)
+           for d, x in ((at % 7, INF), (7 + at % 5, -INF), (12 + at % 3, float("nan")))]
+    bad += [(20, 20, INF), (640, 20, INF), (640, 21, -INF), (1, 21, -INF), (699, 22, INF), (0, 22, -INF), (650, 23, -INF),
+            (649, 23, INF)]
+    for at, d, x in bad:
+        cache.v[int(table[0, at // 32]), 0, at % 32, d] = x
+    got, got_l = binding.paged_attn(q, cache, table, ints([n]), **kw)
+    assert torch.equal(got_l, lse)
+    want = out.clone()
+    for t in range(T):
+        p = n - T + t
+        for at, d, x in bad:
+            if at <= p and (window == 0 or at > p - window or at < n_sink):
+                y = want[0, t, 0, d].item()
+                want[0, t, :, d] = x if np.isfinite(y) else y + x
+    nan = want.isnan()
+    assert torch.equal(got.isnan(), nan)
+    assert torch.equal(got[~nan], want[~nan])
