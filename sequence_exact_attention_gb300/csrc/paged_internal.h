@@ -80,6 +80,10 @@ struct PagedAttnArgs {
 // Few rows: slots of a tile, 32 KB of keys and values at most.
 constexpr int paged_rows_tile(int D, bool quant) { return !quant && D == 128 ? 64 : 128; }
 
+// Many rows over 8-bit pages: a tile of 128 slots of one head is expanded in D / kPagedShare
+// shares.
+constexpr int kPagedShare = 32;
+
 // Fills the plan fields for the sizes in `a`, and, where short sequences of a packed
 // call have a launch of their own, makes `few` that launch's arguments (else its n_items
 // is 0); bytes: the workspace needed. paged_attn_place puts their parts there.

@@ -97,8 +97,10 @@ ra_status plan_many(PagedAttnArgs* a) {
   // keys and values within half of the 126 MB L2
   a->rb_major = (long long)a->B * a->max_len * a->p.H_kv * a->p.D * 4 <= (64ll << 20);
   if (a->p.quant) {
+    // (the expansion counts shares of tiles in 32 bits)
     const long long e = tiles_seen(*a, 128, a->T);
-    if ((long long)a->B * e * a->p.H_kv > 0x7fffffffLL) return RA_ERR_RANGE;
+    if ((long long)a->B * e * a->p.H_kv > 0x7fffffffLL / (a->p.D / kPagedShare))
+      return RA_ERR_RANGE;
     a->n_expanded = (int)e;
   }
   return cut(a, items, whole, rest, tiles, best, 4);

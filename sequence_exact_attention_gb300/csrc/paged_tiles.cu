@@ -689,6 +689,7 @@ template <int D>
 __global__ void __launch_bounds__(kExpandThreads)
 paged_expand_kernel(const PagedAttnArgs a, uint32_t shares) {
   constexpr int kLanes = D / 16, kRows = kExpandThreads / kLanes, kShares = kTile / kRows;
+  static_assert(kShares == D / kPagedShare, "what the plan counts");
   let_dependents_start();
   wait_for_prior_grid();
   const int shift = 31 - __clz(a.p.page), lane = threadIdx.x & 31;
@@ -751,9 +752,7 @@ ra_status launch_tiles(const PagedAttnArgs& a, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
   PagePool p = a.p;
   if (kExpanded) {
-    const long long shares =
-        (long long)a.B * a.n_expanded * a.p.H_kv * (kTile * (D / 16) / kExpandThreads);
-    if (shares > 0x7fffffffLL) return RA_ERR_RANGE;
+    const long long shares = (long long)a.B * a.n_expanded * a.p.H_kv * (D / kPagedShare);
     const long long ctas = shares < kExpandCtas ? shares : kExpandCtas;
     if (!launch_early(paged_expand_kernel<D>, ctas, kExpandThreads, 0, stream, a, (uint32_t)shares))
       return RA_ERR_LAUNCH;
