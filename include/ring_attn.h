@@ -661,10 +661,12 @@ ra_status paged_read(const ra_pages* pages, const int* table, int width, const i
 
 /* Bytes of workspace that paged_attn needs for these sizes, and (varlen = 1, B =
  * n_seq, S_q = max_seqlen) paged_attn_varlen of `total` rows; host only. Of the
- * pages their sizes and type count. Partial results of long contexts take some
+ * pages their sizes, number and type count. Partial results of long contexts take some
  * hundred MB at most; 8-bit pages besides, where S_q tokens are many (more than 48
- * query rows a key/value head), bfloat16 keys and values of all that the windows see
- * of B sequences of max_len slots: a max_len near the real lengths saves memory. */
+ * query rows a key/value head), 4 GB at most of bfloat16 keys and values (of what the
+ * windows see of B sequences of max_len slots, or of the whole pool, or of some
+ * sequences at a time), or what one sequence of max_len slots takes, if that is more: a
+ * max_len near the real lengths saves memory and time. */
 ra_status paged_attn_workspace(const ra_pages* pages, int B, int S_q, int total, int H_q,
                                int max_len, int window, int n_sink, int varlen,
                                size_t* bytes);

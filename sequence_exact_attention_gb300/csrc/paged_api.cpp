@@ -160,13 +160,21 @@ ra_status attn(const void* q, const ra_pages* pages, const int* table, int width
   if (overlap(outs, ins)) return RA_ERR_BUFFER;
   st = check_device(nullptr);
   if (st != RA_OK) return st;
-  paged_attn_place(&a, &few, workspace);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (few.n_items > 0) {
+    paged_attn_place(&few, workspace);
     st = launch(few, s);
     if (st != RA_OK) return st;
   }
-  return launch(a, s);
+  for (long long b0 = 0; b0 < B; b0 += a.n_group) {
+    PagedAttnArgs group;
+    st = paged_attn_group(a, (int)b0, &group);
+    if (st != RA_OK) return st;
+    paged_attn_place(&group, workspace);
+    st = launch(group, s);
+    if (st != RA_OK) return st;
+  }
+  return RA_OK;
 }
 
 }  // namespace

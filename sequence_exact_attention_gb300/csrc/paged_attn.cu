@@ -968,6 +968,7 @@ paged_join_many_kernel(const PagedAttnArgs a) {
   const int d = lane % kLanes * 4;
   const int r0 = blockIdx.x % (256 / kRows) * kRows + warp * (kAtOnce * kPer);   // the warp's first
   const int4 blk = a.part_block[cut];
+  if (a.cu && blk.y <= 0) return;                  // no such block (packed calls alone)
   // chunk s of row r is part s * 256 + r of the block's
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (size_t)cut * a.n_split * 256;
   const float* o = a.part_o + ((size_t)cut * a.n_split * 256 + r0 + half) * D + d;

@@ -66,13 +66,15 @@ struct PagedAttnArgs {
   int n_rb;                // blocks of the longest sequence and head
   int few_rows;            // packed: sequences of up to so many rows a head are the few rows'
                            // kernel's, longer ones the other's; 0: all are this one's
+  int n_group;             // many rows: sequences a launch (paged_attn_group)
   int rb_major;            // many rows: the blocks' order, see there
   int n_expanded;          // many rows over 8-bit pages: tiles a sequence's rows see at most
+  int by_page;             // 1: they are expanded page by page, to a pool of bf16 pages
   float* part_o;           // [n_cut][n_split][block_rows][D]
   float* part_ml;          // [n_cut][n_split][block_rows][2]: maximum (base 2), sum
   int4* part_block;        // many rows: [n_cut] the block's first row in q, its tokens (0: there
                            // is no such block), its key/value head
-  __nv_bfloat16* expanded_k;     // [B][n_expanded][H_kv][128][D]
+  __nv_bfloat16* expanded_k;     // [B][n_expanded][H_kv][128][D] or, by page, as the pool
   __nv_bfloat16* expanded_v;
   int* status;
 };
@@ -86,9 +88,14 @@ constexpr int kPagedShare = 32;
 
 // Fills the plan fields for the sizes in `a`, and, where short sequences of a packed
 // call have a launch of their own, makes `few` that launch's arguments (else its n_items
-// is 0); bytes: the workspace needed. paged_attn_place puts their parts there.
+// is 0); bytes: the workspace needed. Then a->n_group sequences are a launch: all, or, where
+// neither their expanded tiles nor the pool's pages fit in kPagedExpanded bytes, fewer.
 ra_status paged_attn_plan(PagedAttnArgs* a, PagedAttnArgs* few, size_t* bytes);
-void paged_attn_place(PagedAttnArgs* a, PagedAttnArgs* few, void* workspace);
+constexpr size_t kPagedExpanded = size_t(4) << 30;
+// The arguments of the launch of sequences b0 on, a->n_group at most, of a planned call.
+ra_status paged_attn_group(const PagedAttnArgs& a, int b0, PagedAttnArgs* group);
+// Puts a launch's parts into the workspace, which a call's launches use in turn.
+void paged_attn_place(PagedAttnArgs* a, void* workspace);
 // The launchers of the two kernels and of the join of their chunks.
 ra_status launch_paged_rows(const PagedAttnArgs& a, cudaStream_t stream);
 ra_status launch_paged_tiles(const PagedAttnArgs& a, cudaStream_t stream);

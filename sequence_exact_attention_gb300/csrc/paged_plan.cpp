@@ -1,6 +1,8 @@
 // How an attention call over pages is cut up: which kernel, its blocks of query rows
 // and its chunks of slots. Host only, and the same where there is no device to ask,
 // as the workspace's size follows from it: the card's numbers are a GB300's.
+#include <algorithm>
+
 #include "paged_internal.h"
 
 namespace ra {
@@ -97,7 +99,7 @@ ra_status plan_many(PagedAttnArgs* a) {
   // keys and values within half of the 126 MB L2
   a->rb_major = (long long)a->B * a->max_len * a->p.H_kv * a->p.D * 4 <= (64ll << 20);
   if (a->p.quant) {
-    // (the expansion counts shares of tiles in 32 bits)
+    // (the expansion counts shares of tiles in 32 bits, also where it goes by page)
     const long long e = tiles_seen(*a, 128, a->T);
     if ((long long)a->B * e * a->p.H_kv > 0x7fffffffLL / (a->p.D / kPagedShare))
       return RA_ERR_RANGE;
@@ -106,12 +108,22 @@ ra_status plan_many(PagedAttnArgs* a) {
   return cut(a, items, whole, rest, tiles, best, 4);
 }
 
-size_t part_bytes(const PagedAttnArgs& a) {
-  return parts(a) * (a.p.D + 2) * sizeof(float) + (size_t)a.n_cut * sizeof(int4);
-}
 // One of the two expanded tensors' values.
 size_t expanded(const PagedAttnArgs& a) {
+  if (a.by_page) return (size_t)a.p.n_pages * a.p.H_kv * a.p.page * a.p.D;
   return (size_t)a.B * a.n_expanded * a.p.H_kv * 128 * a.p.D;
+}
+// The workspace of a launch.
+size_t launch_bytes(const PagedAttnArgs& a) {
+  return 4 * expanded(a) + parts(a) * (a.p.D + 2) * sizeof(float) + (size_t)a.n_cut * sizeof(int4);
+}
+
+// A launch of many rows for n of the call's sequences; its tensors are still the call's.
+ra_status plan_group(const PagedAttnArgs& a, int n, PagedAttnArgs* group) {
+  *group = a;
+  group->B = n;
+  if (!a.packed) group->rows = n * a.T;
+  return plan_many(group);
 }
 
 }  // namespace
@@ -125,6 +137,7 @@ ra_status paged_attn_plan(PagedAttnArgs* a, PagedAttnArgs* few, size_t* bytes) {
   // 128, 25 rows 128 instead of 245 us, 40 rows 173; of short windows they are as fast.
   const int limit = a->p.quant ? 48 : 16;
   few->n_items = 0;
+  a->n_group = a->B;
   ra_status st;
   if (R <= limit) {
     st = plan_few(a, R, a->T);
@@ -140,29 +153,67 @@ ra_status paged_attn_plan(PagedAttnArgs* a, PagedAttnArgs* few, size_t* bytes) {
     if (a->packed && a->p.quant && short_rows <= limit && 2ll * a->rows <= (long long)a->B * a->T &&
         a->B * tiles_seen(*a, 128, a->T) * a->p.H_kv * 128 * a->p.D >= 1ll << 25)
       a->few_rows = short_rows;
-    st = plan_many(a);
-    if (st == RA_OK && a->few_rows > 0) {
+    // The expanded tiles of 64 places of 128K slots, 8 heads, D = 128, would take 34 GB,
+    // few of which may be used. Where they pass kPagedExpanded, the pool's pages are expanded
+    // instead, each to a page (63 tokens and a piece of 512 behind 8K slots at such a table:
+    // 2.1 GB), or, of a pool too large as well, a group of sequences at a time, in equal
+    // groups. (A group without a piece costs 15 us: 466 instead of 368 us for 8 of them.)
+    if (a->p.quant) {
+      const size_t seen = (size_t)tiles_seen(*a, 128, a->T), one = seen * a->p.H_kv * 128 * a->p.D;
+      const size_t most = std::max<size_t>(kPagedExpanded / (4 * one), 1);
+      if ((size_t)a->B > most) {
+        a->by_page = 1;
+        if (4 * expanded(*a) > kPagedExpanded) {
+          a->by_page = 0;
+          const int groups = (a->B - 1) / (int)most + 1;
+          a->n_group = (a->B - 1) / groups + 1;
+        }
+      }
+    }
+    *bytes = 0;
+    PagedAttnArgs group;
+    for (int n : {a->n_group, a->B % a->n_group}) {      // the last group may be smaller
+      if (n == 0) continue;
+      st = plan_group(*a, n, &group);
+      if (st != RA_OK) return st;
+      *bytes = std::max(*bytes, launch_bytes(group));
+    }
+    if (a->few_rows > 0) {
       *few = *a;
       st = plan_few(few, short_rows, short_rows / grp);
+      if (st == RA_OK) *bytes = std::max(*bytes, launch_bytes(*few));
     }
+    return st;
   }
+  if (st == RA_OK) *bytes = launch_bytes(*a);
+  return st;
+}
+
+ra_status paged_attn_group(const PagedAttnArgs& a, int b0, PagedAttnArgs* group) {
+  *group = a;
+  if (a.block_rows != 0) return RA_OK;      // few rows: planned already, and one launch
+  const ra_status st = plan_group(a, std::min(a.n_group, a.B - b0), group);
   if (st != RA_OK) return st;
-  *bytes = part_bytes(*a) + 4 * expanded(*a) + (few->n_items > 0 ? part_bytes(*few) : 0);
+  group->table += (size_t)b0 * a.width;
+  group->lens += b0;
+  if (a.packed) {
+    group->cu += b0;
+  } else {
+    const size_t row = (size_t)b0 * a.T * a.H_q;
+    group->q = static_cast<const __nv_bfloat16*>(a.q) + row * a.p.D;
+    group->out = static_cast<__nv_bfloat16*>(a.out) + row * a.p.D;
+    if (a.lse) group->lse += row;
+  }
   return RA_OK;
 }
 
-void paged_attn_place(PagedAttnArgs* a, PagedAttnArgs* few, void* workspace) {
+void paged_attn_place(PagedAttnArgs* a, void* workspace) {
   __nv_bfloat16* e = static_cast<__nv_bfloat16*>(workspace);
   a->expanded_k = e;
   a->expanded_v = e + expanded(*a);
-  float* at = reinterpret_cast<float*>(e + 2 * expanded(*a));
-  for (PagedAttnArgs* x : {a, few}) {
-    if (x->n_items == 0) continue;
-    x->part_o = at;
-    x->part_ml = at + parts(*x) * x->p.D;
-    x->part_block = reinterpret_cast<int4*>(x->part_ml + parts(*x) * 2);
-    at = reinterpret_cast<float*>(x->part_block + x->n_cut);
-  }
+  a->part_o = reinterpret_cast<float*>(e + 2 * expanded(*a));
+  a->part_ml = a->part_o + parts(*a) * a->p.D;
+  a->part_block = reinterpret_cast<int4*>(a->part_ml + parts(*a) * 2);
 }
 
 }  // namespace ra

@@ -679,7 +679,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 // 8-bit pages to bf16 tiles [B][n_expanded][H_kv][128][D], keys and values: the
 // tiles that the sequences' new tokens see, in order; slots past the last and those
-// that no token sees as zeros. A CTA makes some rows of one tile and head, 16 values a
+// that no token sees as zeros. (Or, a.by_page, the pages of the slots that they see, to as
+// many bf16 pages; sequences that share one write it alike.) A CTA makes some rows of one tile and head, 16 values a
 // thread, and goes on where there are more of them than the card has places: a launch
 // for all that there may be takes 100 us of CTAs that only leave, for 64 sequences of 8K
 // slots. Bound by the bytes, and by the chain of look-ups before them.
@@ -725,6 +726,8 @@ paged_expand_kernel(const PagedAttnArgs a, uint32_t shares) {
       if (id >= 0 && id < a.p.n_pages)
         from = (((long long)id * a.p.H_kv + hk) << shift) + (slot & (a.p.page - 1));
     }
+    if (a.by_page && from < 0) continue;             // (the tiles' kernel finds no page, either)
+    const size_t to = a.by_page ? (size_t)from : tile * kTile + r;
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       uint32_t w[8] = {};
@@ -738,8 +741,7 @@ paged_expand_kernel(const PagedAttnArgs a, uint32_t shares) {
           w[x] = pack_bf16x2(f.x * scale, f.y * scale);
         }
       }
-      uint4* dst = reinterpret_cast<uint4*>((side ? a.expanded_v : a.expanded_k) +
-                                            (tile * kTile + r) * D + d);
+      uint4* dst = reinterpret_cast<uint4*>((side ? a.expanded_v : a.expanded_k) + to * D + d);
       dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
       dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
@@ -758,9 +760,14 @@ ra_status launch_tiles(const PagedAttnArgs& a, cudaStream_t stream) {
       return RA_ERR_LAUNCH;
     p.k = reinterpret_cast<uint8_t*>(a.expanded_k);
     p.v = reinterpret_cast<uint8_t*>(a.expanded_v);
+    p.quant = 0;
+    if (a.by_page) {
+      PagedAttnArgs pages = a;
+      pages.p = p;
+      return launch_tiles<D, false>(pages, stream);
+    }
     p.n_pages = a.B * a.n_expanded;
     p.page = kTile;
-    p.quant = 0;
   }
   if (!make_query_map(&mq, a.q, a.rows, a.H_q, D, grp, tt) ||
       !make_page_map(&mk, p, p.k, p.page, 1) || !make_page_map(&mv, p, p.v, p.page, 1))
