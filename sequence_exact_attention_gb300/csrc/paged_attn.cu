@@ -219,7 +219,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (j >= sp.hi || !sp.meets(a, j, box_rows)) return x;
       x.wanted = true;
       x.row = j & (a.p.page - 1);
-      if ((j >> shift) < a.width) x.id = a.table[(size_t)b * a.width + (j >> shift)];
+      x.id = paged_entry(a, b, j >> shift);
       return x;
     };
     Box next = look_up(0);
@@ -232,7 +232,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (i >= S::kStages &&
           !sm100::mbar_wait_warp(free_ + 8 * stage, phase ^ 1, abort_flag, kTimeoutNs))
         break;
-      const bool held = cur.id >= 0 && cur.id < a.p.n_pages;
+      const long long row = ((long long)cur.id * H_kv + hk) * a.p.page + cur.row;
+      const bool held =
+          paged_held(a, cur.id) && in_range(row, box_rows, paged_pool_rows(a.p), a.status);
       const uint32_t boxes = __ballot_sync(0xffffffffu, held);
       const uint32_t missing = __ballot_sync(0xffffffffu, cur.wanted && !held);
       const uint32_t dst = ring + stage * S::kStage, bar = full + 8 * stage;
@@ -249,9 +251,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
         sm100::tma_load_4d(to, &tm_k, bar, 0, cur.row, 0, z);
         sm100::tma_load_4d(to + S::kKv, &tm_v, bar, 0, cur.row, 0, z);
         if (kQuant) {
-          const size_t from = (size_t)z * a.p.page + cur.row;
-          sm100::bulk_load(dst + S::kKs + at, a.p.ks + from, box_rows, bar);
-          sm100::bulk_load(dst + S::kVs + at, a.p.vs + from, box_rows, bar);
+          sm100::bulk_load(dst + S::kKs + at, a.p.ks + row, box_rows, bar);
+          sm100::bulk_load(dst + S::kVs + at, a.p.vs + row, box_rows, bar);
         }
       }
       if (++stage == S::kStages) {
@@ -824,6 +825,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
     const long long row = (long long)(sq.row0 + t) * a.H_q + h;
     if (a.n_split > 1) {
       const long long part = paged_part(a, item, split, r);
+      if (!in_range(part, 1, paged_part_rows(a), a.status)) continue;
       if (d == 0) {
         a.part_ml[2 * part] = mx;
         a.part_ml[2 * part + 1] = ls;
@@ -889,6 +891,9 @@ paged_join_few_kernel(const PagedAttnArgs a, int rows) {
   const int r_head = blk.rb * a.block_rows + r;        // of the head's rows
   if (r_head >= sq.n * grp || !paged_mine(a, sq)) return;
   const int part = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+  if (!in_range(paged_part(a, item, 0, r), (long long)(a.n_split - 1) * a.block_rows + 1,
+                paged_part_rows(a), a.status))
+    return;
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + paged_part(a, item, 0, r);
   const float* o = a.part_o + paged_part(a, item, 0, r) * D + d;
   float m = -INFINITY, l = 0.f;
@@ -967,6 +972,7 @@ paged_join_many_kernel(const PagedAttnArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane / kLanes;
   const int d = lane % kLanes * 4;
   const int r0 = blockIdx.x % (256 / kRows) * kRows + warp * (kAtOnce * kPer);   // the warp's first
+  if (!in_range(cut, 1, a.n_cut, a.status)) return;
   const int4 blk = a.part_block[cut];
   if (a.cu && blk.y <= 0) return;                  // no such block (packed calls alone)
   // chunk s of row r is part s * 256 + r of the block's

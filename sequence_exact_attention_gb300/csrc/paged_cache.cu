@@ -117,10 +117,12 @@ __device__ __forceinline__ Place locate(const PagedRowArgs& a, const Divisors& b
   const long long slot = (long long)(a.start ? a.start[b] : 0) + t;
   const int shift = 31 - __clz(a.p.page);
   if (slot < 0 || (slot >> shift) >= a.width) return x;
-  const int id = a.table[(size_t)b * a.width + (slot >> shift)];
+  const long long entry = (long long)b * a.width + (slot >> shift);
+  if (!in_range(entry, 1, (long long)a.B * a.width, a.status)) return x;
+  const int id = a.table[entry];
   if (id < 0 || id >= a.p.n_pages) return x;
   x.row = ((((long long)id * a.p.H_kv + h) << shift)) + (slot & (a.p.page - 1));
-  x.held = in_range(x.row, 1, (long long)a.p.n_pages * a.p.H_kv * a.p.page, a.status);
+  x.held = in_range(x.row, 1, paged_pool_rows(a.p), a.status);
   return x;
 }
 
@@ -172,6 +174,7 @@ paged_append_kernel(const PagedRowArgs a, const Divisors by, uint32_t rows) {
   const uint32_t mask = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
   if (i >= rows) return;
   const size_t elem = (size_t)i * D + lane * kVals;
+  if (!in_range((long long)elem, kVals, a.rows * a.p.H_kv * D, a.status)) return;
   Lane<T> k, v;
   k.load(static_cast<const T*>(a.k) + elem);
   v.load(static_cast<const T*>(a.v) + elem);
@@ -269,6 +272,7 @@ paged_read_kernel(const PagedRowArgs a, const Divisors by, uint32_t rows) {
       decode(wv[x], v);
     }
     const size_t elem = (size_t)i * D + d;
+    if (!in_range((long long)elem, kReadVals, a.rows * a.p.H_kv * D, a.status)) continue;
     if (a.k) store(static_cast<T*>(a.k) + elem, k);
     if (a.v) store(static_cast<T*>(a.v) + elem, v);
   }

@@ -6,6 +6,7 @@
 
 #include <cstdint>
 
+#include "checks.cuh"
 #include "paged_internal.h"
 #include "paged_iter.cuh"
 
@@ -36,6 +37,24 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
+}
+
+// The table's entry for a sequence's slots from p * page on; -1 past its end. (Whether it is
+// a page is tested where it is used, not here: a test would wait for the load.)
+__device__ __forceinline__ int paged_entry(const PagedAttnArgs& a, int b, int p) {
+  const long long at = (long long)b * a.width + p;
+  if (p >= a.width || !in_range(at, 1, (long long)a.B * a.width, a.status)) return -1;
+  return a.table[at];
+}
+__device__ __forceinline__ bool paged_held(const PagedAttnArgs& a, int id) {
+  return id >= 0 && id < a.p.n_pages;
+}
+// What the bounds checks know of the pool's rows and of the partial results'.
+__device__ __forceinline__ long long paged_pool_rows(const PagePool& p) {
+  return (long long)p.n_pages * p.H_kv * p.page;
+}
+__device__ __forceinline__ long long paged_part_rows(const PagedAttnArgs& a) {
+  return (long long)a.n_cut * a.n_split * a.block_rows;
 }
 
 // Sums of x over a warp's lanes up to each.

@@ -224,7 +224,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
   const PagedSeq sq = b >= 0 ? paged_seq(a, b) : PagedSeq{0, 0, 0};
   const int t0 = blk.rb * 2 * tt;                 // the block's first new token
   const int n_tok = min(2 * tt, sq.n - t0);
-  if (work.split == 0 && threadIdx.x == 0)        // for the join
+  if (work.split == 0 && threadIdx.x == 0 &&      // for the join
+      in_range(work.item - a.n_whole, 1, a.n_cut, a.status))
     a.part_block[work.item - a.n_whole] = make_int4(sq.row0 + t0, max(n_tok, 0), hk, 0);
   if (n_tok <= 0) return;                         // past the last block of the batch
   const bool two = n_tok > tt;
@@ -292,10 +293,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
       if (j >= n || lane >= n_box) return -1;
       const int slot = tile_lo(j) + at;
       if (slot >= sp.hi || !sp.meets(a, slot, a.p.page)) return -1;
-      const int p = slot >> shift;
-      if (p >= a.width) return -2;
-      const int id = a.table[(size_t)b * a.width + p];
-      return id >= 0 && id < a.p.n_pages ? id : -2;
+      const int id = paged_entry(a, b, slot >> shift);
+      return paged_held(a, id) ? id : -2;
     };
     auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t full, int id, int j) {
       if (lane == 0) mbar_arrive_expect_tx(full, C::kTileBytes);
@@ -642,8 +641,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
       __syncwarp();
       // where this thread's row goes, in bytes; below 0: nowhere
       const long long at_row = (whole ? orow * 2 : prow * 4) * D + part * row_bytes;
-      const bool store = valid && (whole ? in_range(orow * D, D, (long long)a.rows * a.H_q * D, a.status)
-                                         : n > 0);
+      const bool in = !valid || (whole ? in_range(orow * D, D, (long long)a.rows * a.H_q * D, a.status)
+                                       : in_range(prow, 1, paged_part_rows(a), a.status));
+      const bool store = valid && in && (whole || n > 0);
       uint8_t* to = whole ? static_cast<uint8_t*>(a.out) : reinterpret_cast<uint8_t*>(a.part_o);
       const int chunks = row_bytes / 16;                         // a row's: 4, 8 or 16
       for (int i = lane; i < 32 * chunks; i += 32) {
@@ -653,7 +653,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q,
         if (off >= 0) *reinterpret_cast<uint4*>(to + off + k * 16) = v;
       }
       __syncwarp();                                              // the next tile's rows go there, too
-      if (valid && part == 0) {
+      if (valid && in && part == 0) {
         if (work.split >= 0) {
           a.part_ml[2 * prow] = ls == 0.f ? -INFINITY : m_run[qi];
           a.part_ml[2 * prow + 1] = ls;
@@ -721,13 +721,17 @@ paged_expand_kernel(const PagedAttnArgs a, uint32_t shares) {
     const int r = share % kShares * kRows + threadIdx.x / kLanes;
     const int slot = sp.tile(v) * kTile + r;
     long long from = -1;
-    if (slot < sp.hi && sp.meets(a, slot, 1) && (slot >> shift) < a.width) {
-      const int id = a.table[(size_t)b * a.width + (slot >> shift)];
-      if (id >= 0 && id < a.p.n_pages)
-        from = (((long long)id * a.p.H_kv + hk) << shift) + (slot & (a.p.page - 1));
+    if (slot < sp.hi && sp.meets(a, slot, 1)) {
+      const int id = paged_entry(a, b, slot >> shift);
+      if (paged_held(a, id)) from = (((long long)id * a.p.H_kv + hk) << shift) + (slot & (a.p.page - 1));
+      if (from >= 0 && !in_range(from, 1, paged_pool_rows(a.p), a.status)) from = -1;
     }
     if (a.by_page && from < 0) continue;             // (the tiles' kernel finds no page, either)
     const size_t to = a.by_page ? (size_t)from : tile * kTile + r;
+    if (!in_range((long long)to, 1,
+                  a.by_page ? paged_pool_rows(a.p) : (long long)a.B * a.n_expanded * a.p.H_kv * kTile,
+                  a.status))
+      continue;
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       uint32_t w[8] = {};
