@@ -81,8 +81,9 @@ typedef enum {
   RA_ERR_BUFFER = 9,   /* a caller buffer is too small; caches: one that a call
                           writes overlaps another of its buffers                 */
   RA_ERR_RANGE = 10,   /* a size overflows 32-bit indexing, or step out of range;
-                          in dev_status (checked build only): a device index out
-                          of its tensor's range                                   */
+                          in dev_status: a slot without a page (paged_*), or, in
+                          the checked build only, a device index out of its
+                          tensor's range                                          */
   RA_ERR_SCRATCH = 11  /* the problem needs more scratch than the library's
                           built-in array holds (ring_attn_bwd_noalloc)           */
 } ra_status;

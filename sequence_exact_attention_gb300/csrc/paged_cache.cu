@@ -13,7 +13,8 @@
 // flight and what a row costs besides is little. Eight lanes (four at D = 64) share a
 // row, sixteen values each, of its key and its value, loaded before their place is
 // looked up. Measured, 8 x 8192 tokens of 8 heads, D = 128, 8 bits: append
-// 66 us, read 68 us, 6.1 and 5.9 TB/s (eight values a lane and one row: 95 and 72).
+// 66 us, read 67 us, 6.1 and 6.0 TB/s, one behind the other 129 (eight values a lane and
+// one row: 95 and 72).
 #include <cuda_bf16.h>
 
 #include <cstdint>

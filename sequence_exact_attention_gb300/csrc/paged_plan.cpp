@@ -134,7 +134,7 @@ ra_status paged_attn_plan(PagedAttnArgs* a, PagedAttnArgs* few, size_t* bytes) {
   // What is more than few rows. bf16 pages of many rows are read once, by tiles; 8-bit
   // ones are expanded first, five times their bytes, so blocks of 16 rows that read the
   // pages again (from L2, mostly) are ahead for longer: 8 x 32K slots of 4 heads, D =
-  // 128, 25 rows 128 instead of 245 us, 40 rows 173; of short windows they are as fast.
+  // 128, 25 rows 128 instead of 245 us, 40 rows 176; of short windows they are as fast.
   const int limit = a->p.quant ? 48 : 16;
   few->n_items = 0;
   a->n_group = a->B;
