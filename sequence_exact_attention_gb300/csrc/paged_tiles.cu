@@ -89,8 +89,9 @@ struct Cfg {
   static constexpr int kRedOff = kBarOff + kBarBytes;
   static constexpr int kRedBytes = (512 + 512) * 4;
   // values that are not finite, of tiles that rows differ in: a bit each, [kEdges][128
-  // slots][2][D / 32], first infinity or NaN, then minus infinity or NaN. The block's 256 positions make at most three such tiles at each end
-  // of a window, the first slots' last tile one more.
+  // slots][2][D / 32], first infinity or NaN, then minus infinity or NaN. The block's 256
+  // positions make at most three such tiles at each end of a window, the first slots' last
+  // tile one more.
   static constexpr int kEdges = 7;
   static constexpr int kOddOff = kRedOff + kRedBytes;
   static constexpr int kOddBytes = kEdges * kTile * 2 * (D / 32) * 4;
